@@ -19,17 +19,21 @@ import os
 __all__ = [
     "mr_allreduce", "mr_reduce_scatter", "mr_all_gather", "mr_allreduce_ex", "mr_reduce_scatter_ex", "mr_allreduce_rmsnorm", "mr_allreduce_sign_ef",
     "mr_reduce_scatter_sign_ef", "mr_reduce_scatter_sign_ef_noalloc", "mr_sign_ef_workspace_bytes",
+    "mr_logprob", "mr_logprob_grad", "mr_distill_topk", "mr_distill_topk_grad", "mr_distill_topk_step",
     "mr_status_string", "mr_last_error",
     "mr_allreduce_ptrs", "mr_plan_auto", "mr_plan_ring_order", "mr_plan_tree", "mr_chunk_lo", "mr_launch_count", "mr_launch_floor", "MRError",
     "load", "LIB_PATH",
-    "DTYPES", "OPS", "ALGOS", "MAX_RANKS",
+    "DTYPES", "OPS", "ALGOS", "DISTILL_MODES", "MAX_RANKS", "MAX_TOP", "MAX_TEACHER",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmr.so")
 MAX_RANKS = 64
+MAX_TOP = 64            # top alternatives per row of mr_logprob
+MAX_TEACHER = 128       # teacher entries per row of mr_distill_topk
 DTYPES = {"fp32": 0, "bf16": 1, "int32": 2}
 OPS = {"sum": 0, "prod": 1, "min": 2, "max": 3, "avg": 4}
 ALGOS = {"ring": 0, "tree": 1, "hier": 2, "auto": 3}
+DISTILL_MODES = {"renorm": 0, "tail": 1}
 STATUS = {0: "MR_OK", 1: "MR_ERR_INVALID_ARGUMENT", 2: "MR_ERR_UNSUPPORTED", 3: "MR_ERR_ALIAS", 4: "MR_ERR_CUDA"}
 
 _lib = None
@@ -92,6 +96,16 @@ def load():
     L.mr_launch_count.restype = ctypes.c_ulonglong
     L.mr_launch_floor.argtypes = [ctypes.c_uint, vp]
     L.mr_launch_floor.restype = i
+    f = ctypes.c_float
+    scores = [vp, vp, i, sz, sz, i, f]                      # logits, ld, W, rows, vocab, dtype, scale
+    teacher = [i, vp, vp, i, f]                             # K, ids, values, mode, scale
+    L.mr_logprob.argtypes = scores + [vp, i, vp, vp, vp, vp, vp, vp]
+    L.mr_logprob_grad.argtypes = scores + [vp, vp, vp, vp, vp, vp, vp, vp]
+    L.mr_distill_topk.argtypes = scores + teacher + [vp, vp, vp]
+    L.mr_distill_topk_grad.argtypes = scores + teacher + [vp, vp, vp, vp, vp]
+    L.mr_distill_topk_step.argtypes = scores + teacher + [vp, vp, vp, vp, vp]
+    for g in (L.mr_logprob, L.mr_logprob_grad, L.mr_distill_topk, L.mr_distill_topk_grad, L.mr_distill_topk_step):
+        g.restype = i
     _lib = L
     return L
 
@@ -277,6 +291,137 @@ def mr_reduce_scatter_sign_ef_noalloc(grad, err, recv, scales=None, op="avg", al
     st = load().mr_reduce_scatter_sign_ef_noalloc(
         _pointers(grad), _pointers(err), _pointers(recv), None if scales is None else scales.data_ptr(), len(grad),
         grad[0].numel(), _code(OPS, op, "op"), _code(ALGOS, algo, "algo"), _stream(stream))
+    if st:
+        _raise(st)
+
+
+# --------------------------------------------------------------------------
+# token scores over a vocabulary in shards
+# --------------------------------------------------------------------------
+
+def _score_rows(tensors, name):
+    """W rank buffers [rows, columns of the rank] -> (pointers, strides, rows, vocab, dtype code)."""
+    if not tensors:
+        raise ValueError(f"{name}: empty list of rank buffers")
+    W, t0 = len(tensors), tensors[0]
+    rows, vocab = t0.shape[0], 0
+    ptrs, lds = (ctypes.c_void_p * W)(), (ctypes.c_size_t * W)()
+    for r, t in enumerate(tensors):
+        if t.dim() != 2 or not t.is_cuda or t.dtype != t0.dtype or t.shape[0] != rows:
+            raise ValueError(f"{name}: rank buffers must be 2-D CUDA tensors [rows, columns] of one dtype")
+        n = t.shape[1]
+        ld, step = t.stride()
+        if (step != 1 and n > 1) or (ld < n and rows > 1):
+            raise ValueError(f"{name}[{r}]: the columns of a row must lie beside each other and rows must not overlap")
+        ptrs[r] = t.data_ptr()
+        lds[r] = ld if ld > n else n
+        vocab += n
+    for r, t in enumerate(tensors if W > 1 else ()):
+        if t.shape[1] != (r + 1) * vocab // W - r * vocab // W:
+            raise ValueError(f"{name}[{r}]: {t.shape[1]} columns, but rank {r} of {W} holds columns "
+                             f"[{r * vocab // W}, {(r + 1) * vocab // W}) of {vocab}")
+    return ptrs, lds, rows, vocab, _dtype_code(t0)
+
+
+def _row_ptr(t, name, rows, per, integer=False):
+    """The address of a per-row array (None stays None)."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype is not (torch.int64 if integer else torch.float32) or not t.is_cuda or not t.is_contiguous() \
+            or t.numel() != rows * per:
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {'int64' if integer else 'float32'} with "
+                         f"{rows} x {per} elements is needed")
+    return t.data_ptr()
+
+
+def _grad_rows(logits, grad, rows, vocab, code):
+    gp, gl, g_rows, g_vocab, g_code = _score_rows(grad, "grad")
+    if len(grad) != len(logits) or g_rows != rows or g_vocab != vocab or g_code != code:
+        raise ValueError("grad: rank buffers of the scores' shape and dtype are needed")
+    return gp, gl
+
+
+def mr_logprob(logits, ids=None, scale=1.0, logprob=None, entropy=None, stats=None, top_ids=None, top_logprob=None,
+               stream=None):
+    """Log probabilities of the given tokens, with entropy and top
+    alternatives.  logits: W rank buffers [T, columns of the rank] (fp32 or
+    bf16; rows may be strided); ids: [T] int64, negative leaves a row out.
+    Outputs, each optional: logprob, entropy [T] fp32; stats [T, 2] fp32 (for
+    mr_logprob_grad); top_ids [T, k] int64 and top_logprob [T, k] fp32.  y =
+    scale * logits."""
+    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
+    k = 0
+    for t in (top_ids, top_logprob):
+        if t is not None:
+            k = t.shape[-1]
+    st = load().mr_logprob(xp, ld, len(logits), rows, vocab, code, scale, _row_ptr(ids, "ids", rows, 1, True), k,
+                           _row_ptr(logprob, "logprob", rows, 1), _row_ptr(entropy, "entropy", rows, 1),
+                           _row_ptr(stats, "stats", rows, 2), _row_ptr(top_ids, "top_ids", rows, k, True),
+                           _row_ptr(top_logprob, "top_logprob", rows, k), _stream(stream))
+    if st:
+        _raise(st)
+
+
+def mr_logprob_grad(logits, ids, stats, grad, g_logprob=None, entropy=None, g_entropy=None, scale=1.0, stream=None):
+    """Gradient of g_logprob . logprob + g_entropy . entropy with respect to
+    the scores, into ``grad`` (W rank buffers; may be ``logits``).  stats and
+    entropy are mr_logprob's outputs."""
+    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
+    gp, gl = _grad_rows(logits, grad, rows, vocab, code)
+    st = load().mr_logprob_grad(xp, ld, len(logits), rows, vocab, code, scale, _row_ptr(ids, "ids", rows, 1, True),
+                                _row_ptr(stats, "stats", rows, 2), _row_ptr(entropy, "entropy", rows, 1),
+                                _row_ptr(g_logprob, "g_logprob", rows, 1), _row_ptr(g_entropy, "g_entropy", rows, 1),
+                                gp, gl, _stream(stream))
+    if st:
+        _raise(st)
+
+
+def _teacher(teacher_ids, teacher_val, rows, mode, teacher_scale):
+    k = teacher_ids.shape[-1] if teacher_ids.dim() == 2 else 0
+    return (k, _row_ptr(teacher_ids, "teacher_ids", rows, k, True), _row_ptr(teacher_val, "teacher_val", rows, k),
+            _code(DISTILL_MODES, mode, "mode"), teacher_scale)
+
+
+def mr_distill_topk(logits, teacher_ids, teacher_val, loss=None, stats=None, mode="renorm", scale=1.0,
+                    teacher_scale=1.0, stream=None):
+    """Distillation loss [T] from a teacher's top entries (teacher_ids [T, K]
+    int64, negative for no entry; teacher_val [T, K] fp32).  mode 'renorm'
+    takes logits and renormalises them over the list, 'tail' takes log
+    probabilities and treats the remaining mass as one more outcome.  stats
+    [T, 4] is what mr_distill_topk_grad takes."""
+    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
+    st = load().mr_distill_topk(xp, ld, len(logits), rows, vocab, code, scale,
+                                *_teacher(teacher_ids, teacher_val, rows, mode, teacher_scale),
+                                _row_ptr(loss, "loss", rows, 1), _row_ptr(stats, "stats", rows, 4), _stream(stream))
+    if st:
+        _raise(st)
+
+
+def mr_distill_topk_grad(logits, teacher_ids, teacher_val, stats, g_loss, grad, mode="renorm", scale=1.0,
+                         teacher_scale=1.0, stream=None):
+    """Gradient of g_loss . loss with respect to the scores, into ``grad`` (W
+    rank buffers; may be ``logits``)."""
+    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
+    gp, gl = _grad_rows(logits, grad, rows, vocab, code)
+    st = load().mr_distill_topk_grad(xp, ld, len(logits), rows, vocab, code, scale,
+                                     *_teacher(teacher_ids, teacher_val, rows, mode, teacher_scale),
+                                     _row_ptr(stats, "stats", rows, 4), _row_ptr(g_loss, "g_loss", rows, 1), gp, gl,
+                                     _stream(stream))
+    if st:
+        _raise(st)
+
+
+def mr_distill_topk_step(logits, teacher_ids, teacher_val, weight, loss, grad, mode="renorm", scale=1.0,
+                         teacher_scale=1.0, stream=None):
+    """Loss [T] (unweighted; may be None) and the gradient of weight . loss in
+    one kernel, reading the scores once (``grad`` may be ``logits``)."""
+    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
+    gp, gl = _grad_rows(logits, grad, rows, vocab, code)
+    st = load().mr_distill_topk_step(xp, ld, len(logits), rows, vocab, code, scale,
+                                     *_teacher(teacher_ids, teacher_val, rows, mode, teacher_scale),
+                                     _row_ptr(weight, "weight", rows, 1), _row_ptr(loss, "loss", rows, 1), gp, gl,
+                                     _stream(stream))
     if st:
         _raise(st)
 

@@ -118,6 +118,58 @@ constexpr uint64_t kSignMaxWorkspaceBytes = 2048ull * kL1Words * sizeof(uint32_t
 // Vector width of the decode-and-reduce kernel for a given W.
 constexpr int sign_vector_bytes(int W) { return W <= 8 ? 16 : W <= 16 ? 8 : 4; }
 
+// The token-score operators: rows of V scores, column c held by the rank whose
+// chunk [floor(r*V/W), floor((r+1)*V/W)) it lies in.  One block for all of
+// them; each uses its part.
+struct ScoreParams {
+    const void* x[kMaxRanks];       // the scores of rank r's columns ...
+    void* g[kMaxRanks];             // ... and the gradients that go to the same columns
+    uint64_t ld[kMaxRanks];         // elements from a row to the next
+    uint64_t ldg[kMaxRanks];
+    uint32_t col0[kMaxRanks + 1];   // first column of each rank
+    uint32_t sb0[kMaxRanks + 1];    // superblocks before each rank's (score_kernel.cuh)
+    uint64_t rows;
+    int W;
+    uint32_t vocab;
+    float shards_per_col;           // W / V
+    float scale;
+    int csize;                      // CTAs per cluster: a row is cut into this many runs of superblocks
+    int parts;                      // gradient kernels: warps per row,
+    uint32_t part_sb;               // and superblocks each of them takes
+    uint32_t cache_rounds;          // loss and gradient in one: rounds of a CTA's run kept in shared memory
+    // log probabilities
+    const long long* ids;
+    int top_k;
+    float* logprob;
+    float* entropy;
+    float* stats;                   // 2 (log probabilities) or 4 (distillation) floats per row
+    long long* top_ids;
+    float* top_logprob;
+    const float* stats_in;
+    const float* entropy_in;
+    const float* g_row;             // gradient of each row's log probability, or of its loss
+    const float* g_entropy;
+    // distillation
+    int K;
+    int tail;                       // 1: the teacher's mass outside the list is one more outcome
+    float teacher_scale;
+    const long long* t_ids;
+    const float* t_val;
+    float* loss;
+};
+
+// Most CTAs of a row's cluster (16 needs the non-portable opt-in).
+constexpr int kMaxScoreCluster = 16;
+// Bytes of one rank's row in a superblock.
+constexpr uint32_t kSuperblockBytes = 2048;
+constexpr int kSbRuns = 4;                          // 512-byte runs in a superblock
+constexpr size_t kStepRoundBytes = kSuperblockBytes * (kThreads / 32);  // a superblock for every warp of a CTA
+// Shared memory of the top-k path: a key for each 512-byte run of the CTA's
+// part, the selected runs, and the candidates (k - j from the j-th run).
+constexpr size_t score_top_smem(uint32_t runs, int k) {
+    return (size_t)runs * 4 + (size_t)(k + 2) * 4 + (size_t)k * (k + 1) / 2 * 8;
+}
+
 struct GatherParams {
     const void* in[kMaxRanks];
     void* out[kMaxRanks];
@@ -281,6 +333,15 @@ mr_status_t run_sign_ef(const char* what, int mode, const void* const* grad, voi
                         float* scales, int W, size_t N, mr_op_t op, mr_algo_t algo, void* workspace,
                         size_t workspace_bytes, void* stream, ScratchFn scratch = nullptr);
 cudaError_t launch_sign_ef(const SignParams& P, int op, int algo, dim3 grid, cudaStream_t s);
+// The C ABI's own state (api.cu), for entry points in other files.
+int device_sms();
+int debug_log_level();
+void count_launch();
+void clear_error();
+cudaError_t launch_logprob(const ScoreParams& P, int dtype, dim3 grid, size_t smem, cudaStream_t s);
+cudaError_t launch_distill(const ScoreParams& P, int dtype, bool step, dim3 grid, size_t smem, cudaStream_t s);
+cudaError_t launch_logprob_grad(const ScoreParams& P, int dtype, dim3 grid, cudaStream_t s);
+cudaError_t launch_distill_grad(const ScoreParams& P, int dtype, dim3 grid, cudaStream_t s);
 cudaError_t launch_allreduce_rmsnorm(const NormParams& P, int dtype, int algo, dim3 grid, size_t smem, cudaStream_t s);
 
 }  // namespace mr

@@ -1,0 +1,376 @@
+// score_api.cu -- the C ABI of the token-score operators: argument checks,
+// alias checks, the split of rows over CTAs and dispatch.  See include/mr.h.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "mr.h"
+#include "mr_internal.h"
+#include "order.cuh"
+
+namespace {
+
+using mr::report_error;
+using mr::ScoreParams;
+
+constexpr size_t kMostRows = (size_t)1 << 40, kMostStride = (size_t)1 << 40;
+
+// A byte range of the call, or (ld > 0) rows of `width` bytes every `ld` bytes from lo.
+struct Span {
+    uintptr_t lo, hi;
+    size_t ld, width;
+    const char* name;
+    int rank;       // -1: not a rank buffer
+    bool written;
+};
+
+struct Spans {
+    Span s[2 * MR_MAX_RANKS + 8];
+    int n = 0;
+    void add(const void* p, size_t bytes, const char* name, bool written) {
+        if (p && bytes) s[n++] = {(uintptr_t)p, (uintptr_t)p + bytes, 0, 0, name, -1, written};
+    }
+    void add_rows(const void* p, size_t rows, size_t ld, size_t width, const char* name, int rank, bool written) {
+        if (width) s[n++] = {(uintptr_t)p, (uintptr_t)p + (rows - 1) * ld + width, ld, width, name, rank, written};
+    }
+};
+
+// Whether two overlapping ranges never share a byte: rows of one stride whose
+// columns lie beside each other (column slices of one buffer).
+bool beside(const Span& a, const Span& b) {
+    if (!a.ld || a.ld != b.ld) return false;
+    const Span &x = a.lo <= b.lo ? a : b, &y = a.lo <= b.lo ? b : a;
+    const size_t d = (y.lo - x.lo) % x.ld;      // where y's columns start within x's rows
+    return d >= x.width && d + y.width <= x.ld;
+}
+
+mr_status_t check_spans(Spans& v) {
+    std::sort(v.s, v.s + v.n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    int open[2 * MR_MAX_RANKS + 8];
+    int nopen = 0;
+    for (int i = 0; i < v.n; ++i) {
+        const Span& b = v.s[i];
+        int keep = 0;
+        for (int j = 0; j < nopen; ++j) {
+            const Span& a = v.s[open[j]];
+            if (a.hi <= b.lo) continue;
+            open[keep++] = open[j];
+            if (!a.written && !b.written) continue;
+            // in place: a rank's gradients over its own scores, row by row
+            const bool in_place = a.rank >= 0 && a.rank == b.rank && a.written != b.written && a.lo == b.lo && a.ld == b.ld;
+            if (!in_place && !beside(a, b))
+                return report_error(MR_ERR_ALIAS, "%s[%d] overlaps %s[%d] in a form that is not an allowed in-place one",
+                                    a.name, std::max(0, a.rank), b.name, std::max(0, b.rank));
+        }
+        nopen = keep;
+        open[nopen++] = i;
+    }
+    return MR_OK;
+}
+
+struct Call {
+    const char* what;
+    ScoreParams P;
+    Spans spans;
+    size_t rows = 0;
+    mr_dtype_t dtype = MR_FP32;
+    size_t esize = 4;
+    uint32_t nsb = 0;
+};
+
+bool misaligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
+// Shapes, rank buffers and strides of the scores (and of the gradients).
+mr_status_t check_scores(Call& c, const void* const* logits, const size_t* ld, void* const* grad, const size_t* ld_grad,
+                         bool with_grad, int W, size_t rows, size_t vocab, mr_dtype_t dtype, float scale) {
+    const char* w = c.what;
+    if (W < 1 || W > MR_MAX_RANKS) return report_error(MR_ERR_INVALID_ARGUMENT, "W = %d is outside [1, %d]", W, MR_MAX_RANKS);
+    if (dtype != MR_FP32 && dtype != MR_BF16 && dtype != MR_INT32)
+        return report_error(MR_ERR_INVALID_ARGUMENT, "unknown dtype %d", (int)dtype);
+    if (dtype == MR_INT32) return report_error(MR_ERR_UNSUPPORTED, "%s takes fp32 and bf16 scores", w);
+    if (!logits || (with_grad && !grad)) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: logits or grad pointer array is NULL", w);
+    if (vocab < 1 || vocab >= ((size_t)1 << 31))
+        return report_error(MR_ERR_INVALID_ARGUMENT, "%s: vocab = %zu is outside [1, 2^31)", w, vocab);
+    if (rows > kMostRows) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: rows = %zu is more than 2^40", w, rows);
+    if (!(scale > 0.0f) || !isfinite(scale)) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: scale must be positive and finite", w);
+    ScoreParams& P = c.P;
+    const size_t b = dtype == MR_BF16 ? 2 : 4;
+    c.dtype = dtype;
+    c.esize = b;
+    c.rows = rows;
+    P.rows = rows;
+    P.W = W;
+    P.vocab = (uint32_t)vocab;
+    P.shards_per_col = (float)W / (float)vocab;
+    P.scale = scale;
+    const uint32_t sb = mr::kSuperblockBytes / b;       // scores in a superblock
+    uint32_t nsb = 0;
+    for (int r = 0; r < W; ++r) {
+        const size_t lo = mr::chunk_lo(W, vocab, r), width = mr::chunk_lo(W, vocab, r + 1) - lo;
+        P.col0[r] = (uint32_t)lo;
+        P.sb0[r] = nsb;
+        P.x[r] = logits[r];
+        P.ld[r] = ld ? ld[r] : width;
+        P.g[r] = with_grad ? grad[r] : nullptr;
+        P.ldg[r] = ld_grad ? ld_grad[r] : width;
+        if (width == 0) continue;       // fewer columns than ranks: never read
+        if (rows == 0) continue;
+        if (!logits[r]) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: logits[%d] is NULL", w, r);
+        if (misaligned(logits[r], b)) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: logits[%d] is not aligned to its element", w, r);
+        if (P.ld[r] < width || P.ld[r] > kMostStride)
+            return report_error(MR_ERR_INVALID_ARGUMENT, "%s: ld[%d] = %zu is below the rank's %zu columns (or over 2^40)", w, r,
+                                (size_t)P.ld[r], width);
+        if ((unsigned __int128)rows * P.ld[r] * b >> 62)
+            return report_error(MR_ERR_INVALID_ARGUMENT, "%s: rows * ld[%d] is too large", w, r);
+        c.spans.add_rows(logits[r], rows, P.ld[r] * b, width * b, "logits", r, false);
+        if (with_grad) {
+            if (!grad[r] || misaligned(grad[r], b))
+                return report_error(MR_ERR_INVALID_ARGUMENT, "%s: grad[%d] is NULL or not aligned to its element", w, r);
+            if (P.ldg[r] < width || P.ldg[r] > kMostStride || (unsigned __int128)rows * P.ldg[r] * b >> 62)
+                return report_error(MR_ERR_INVALID_ARGUMENT, "%s: ld_grad[%d] = %zu is below the rank's %zu columns, or too large", w, r,
+                                    (size_t)P.ldg[r], width);
+            c.spans.add_rows(grad[r], rows, P.ldg[r] * b, width * b, "grad", r, true);
+        }
+        // places before the row's start on its 16-byte boundary, over all rows
+        const size_t most = (uintptr_t)logits[r] % 16 == 0 && (rows == 1 || P.ld[r] * b % 16 == 0) ? 0
+                          : rows == 1 ? (uintptr_t)logits[r] % 16 / b : 16 / b - 1;
+        nsb += (uint32_t)((width + most + sb - 1) / sb);
+    }
+    P.col0[W] = (uint32_t)vocab;
+    P.sb0[W] = nsb;
+    c.nsb = nsb;
+    return MR_OK;
+}
+
+// A per-row array: alignment, and its range.
+template <class T>
+mr_status_t per_row(Call& c, const T* p, size_t per, const char* name, bool written, bool required) {
+    if (!p) return required ? report_error(MR_ERR_INVALID_ARGUMENT, "%s: %s is NULL", c.what, name) : MR_OK;
+    if (misaligned(p, sizeof(T))) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: %s is not aligned to its element", c.what, name);
+    c.spans.add(p, c.rows * per * sizeof(T), name, written);
+    return MR_OK;
+}
+
+// CTAs per row (a cluster), from the modelled time of the whole call: rounds
+// of rows over the resident clusters, each a CTA's part of a row at its share
+// of the bandwidth and a fixed cost of the row's start and join.
+int plan_cluster(const Call& c, size_t (*smem)(const Call&, int), int most_resident, int* resident, double passes) {
+    const double sms = mr::device_sms();
+    int best = 1;
+    double best_us = 1e300;
+    for (int C = 1; C <= mr::kMaxScoreCluster; C *= 2) {
+        if (C > 1 && (uint32_t)C * mr::kThreads / 32 > c.nsb + 7) break;        // a superblock for every warp
+        const size_t bytes = smem(c, C);
+        if (bytes > 200 * 1024) continue;
+        const int r = std::min<int>(most_resident, (int)((227 * 1024) / (bytes + 24 * 1024)));
+        const double slots = sms * std::max(1, r), clusters = std::max(1.0, floor(slots / C));
+        const double rounds = ceil((double)c.rows / clusters);
+        const double active = std::min(slots, (double)c.rows * C);
+        const double gbs = std::min(45.0, 6600.0 / active);
+        const double us = rounds * ((double)c.nsb * mr::kSuperblockBytes * passes / C / (gbs * 1e3) + (C == 1 ? 1.0 : 2.0));
+        if (us < best_us) {
+            best_us = us;
+            best = C;
+            *resident = std::max(1, r);
+        }
+    }
+    return best;
+}
+
+size_t plain_smem(const Call&, int) { return 0; }
+size_t top_smem(const Call& c, int C) { return mr::score_top_smem((c.nsb + C - 1) / C * mr::kSbRuns, c.P.top_k); }
+size_t step_smem(const Call& c, int C) {
+    const uint32_t rounds = ((c.nsb + C - 1) / C + mr::kThreads / 32 - 1) / (mr::kThreads / 32);
+    return (size_t)rounds * mr::kStepRoundBytes;
+}
+
+dim3 forward_grid(const Call& c, int C, int resident) {
+    const size_t clusters = std::max<size_t>(1, (size_t)mr::device_sms() * resident / C);
+    return dim3((unsigned)(std::min(c.rows, clusters) * C), 1, 1);
+}
+
+// Warps per row of an elementwise kernel, and the grid.
+dim3 grad_grid(Call& c) {
+    const size_t warps = (size_t)mr::device_sms() * 3 * (mr::kThreads / 32);
+    uint32_t s = 8;
+    while (s > 1 && c.rows * ((c.nsb + s - 1) / s) < 2 * warps) s /= 2;
+    c.P.part_sb = s;
+    c.P.parts = (int)((c.nsb + s - 1) / s);
+    const size_t ctas = (c.rows * c.P.parts + mr::kThreads / 32 - 1) / (mr::kThreads / 32);
+    return dim3((unsigned)std::min(ctas, (size_t)mr::device_sms() * 3), 1, 1);
+}
+
+mr_status_t launched(const Call& c, cudaError_t e, dim3 grid, size_t smem) {
+    if (e != cudaSuccess) return report_error(MR_ERR_CUDA, "%s launch failed: %s", c.what, cudaGetErrorString(e));
+    mr::count_launch();
+    if (mr::debug_log_level() > 0)
+        fprintf(stderr, "[mr] %s dtype=%s W=%d rows=%zu vocab=%u superblocks=%u grid=%u cluster=%d smem=%zu parts=%d\n", c.what,
+                c.dtype == MR_BF16 ? "bf16" : "fp32", c.P.W, c.rows, c.P.vocab, c.nsb, grid.x, c.P.csize, smem, c.P.parts);
+    return MR_OK;
+}
+
+// The teacher's list.
+mr_status_t check_teacher(Call& c, int K, const long long* ids, const float* val, mr_distill_t mode, float teacher_scale) {
+    if (K < 1 || K > MR_MAX_TEACHER)
+        return report_error(MR_ERR_INVALID_ARGUMENT, "%s: K = %d is outside [1, %d]", c.what, K, MR_MAX_TEACHER);
+    if (mode != MR_DISTILL_RENORM && mode != MR_DISTILL_TAIL)
+        return report_error(MR_ERR_INVALID_ARGUMENT, "%s: unknown mode %d", c.what, (int)mode);
+    if (!(teacher_scale > 0.0f) || !isfinite(teacher_scale))
+        return report_error(MR_ERR_INVALID_ARGUMENT, "%s: teacher_scale must be positive and finite", c.what);
+    if (mode == MR_DISTILL_TAIL && teacher_scale != 1.0f)
+        return report_error(MR_ERR_INVALID_ARGUMENT, "%s: MR_DISTILL_TAIL takes log probabilities as they are (teacher_scale 1)", c.what);
+    mr_status_t st = per_row(c, ids, (size_t)K, "teacher_ids", false, c.rows > 0);
+    if (st == MR_OK) st = per_row(c, val, (size_t)K, "teacher_val", false, c.rows > 0);
+    c.P.K = K;
+    c.P.tail = mode == MR_DISTILL_TAIL;
+    c.P.teacher_scale = teacher_scale;
+    c.P.t_ids = ids;
+    c.P.t_val = val;
+    return st;
+}
+
+mr_status_t run_distill(Call& c, bool step, void* stream) {
+    size_t smem = 0;
+    int resident = 1;
+    if (step) {
+        c.P.csize = plan_cluster(c, step_smem, 3, &resident, 2.0);
+        smem = step_smem(c, c.P.csize);
+        c.P.cache_rounds = (uint32_t)(smem / mr::kStepRoundBytes);
+        if (smem > 200 * 1024) {        // a row too long for sixteen CTAs: the rest is read again
+            c.P.cache_rounds = 4;
+            smem = 4 * mr::kStepRoundBytes;
+            resident = 2;
+            c.P.csize = mr::kMaxScoreCluster;
+        }
+    } else {
+        c.P.csize = plan_cluster(c, plain_smem, 3, &resident, 1.0);
+    }
+    const dim3 grid = forward_grid(c, c.P.csize, resident);
+    return launched(c, mr::launch_distill(c.P, c.dtype, step, grid, smem, (cudaStream_t)stream), grid, smem);
+}
+
+}  // namespace
+
+extern "C" {
+
+mr_status_t mr_logprob(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,
+                       float scale, const long long* ids, int top_k, float* logprob, float* entropy, float* stats,
+                       long long* top_ids, float* top_logprob, void* stream) {
+    mr::clear_error();
+    Call c{"mr_logprob", {}, {}};
+    mr_status_t st = check_scores(c, logits, ld, nullptr, nullptr, false, W, rows, vocab, dtype, scale);
+    if (st != MR_OK) return st;
+    if (top_k < 0 || top_k > MR_MAX_TOP || (size_t)top_k > vocab)
+        return report_error(MR_ERR_INVALID_ARGUMENT, "mr_logprob: top_k = %d is outside [0, min(%d, vocab)]", top_k, MR_MAX_TOP);
+    if (top_k > 0 && vocab > MR_MAX_TOP_VOCAB)
+        return report_error(MR_ERR_UNSUPPORTED, "mr_logprob: top_k takes a vocab of at most %d", MR_MAX_TOP_VOCAB);
+    if ((top_k > 0) != (top_ids || top_logprob))
+        return report_error(MR_ERR_INVALID_ARGUMENT, "mr_logprob: top_k and top_ids / top_logprob go together");
+    if (logprob && !ids) return report_error(MR_ERR_INVALID_ARGUMENT, "mr_logprob: logprob needs ids");
+    if (!logprob && !entropy && !stats && !top_k) return report_error(MR_ERR_INVALID_ARGUMENT, "mr_logprob: no output is asked for");
+    if (rows == 0) return MR_OK;
+    if ((st = per_row(c, ids, 1, "ids", false, false)) != MR_OK) return st;
+    if ((st = per_row(c, logprob, 1, "logprob", true, false)) != MR_OK) return st;
+    if ((st = per_row(c, entropy, 1, "entropy", true, false)) != MR_OK) return st;
+    if ((st = per_row(c, stats, 2, "stats", true, false)) != MR_OK) return st;
+    if ((st = per_row(c, top_ids, (size_t)top_k, "top_ids", true, false)) != MR_OK) return st;
+    if ((st = per_row(c, top_logprob, (size_t)top_k, "top_logprob", true, false)) != MR_OK) return st;
+    if ((st = check_spans(c.spans)) != MR_OK) return st;
+    c.P.ids = ids;
+    c.P.top_k = top_k;
+    c.P.logprob = logprob;
+    c.P.entropy = entropy;
+    c.P.stats = stats;
+    c.P.top_ids = top_ids;
+    c.P.top_logprob = top_logprob;
+    int resident = 1;
+    c.P.csize = plan_cluster(c, top_k ? top_smem : plain_smem, 3, &resident, 1.0);
+    const size_t smem = top_k ? top_smem(c, c.P.csize) : 0;
+    const dim3 grid = forward_grid(c, c.P.csize, resident);
+    return launched(c, mr::launch_logprob(c.P, dtype, grid, smem, (cudaStream_t)stream), grid, smem);
+}
+
+mr_status_t mr_logprob_grad(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,
+                            float scale, const long long* ids, const float* stats, const float* entropy,
+                            const float* g_logprob, const float* g_entropy, void* const* grad, const size_t* ld_grad,
+                            void* stream) {
+    mr::clear_error();
+    Call c{"mr_logprob_grad", {}, {}};
+    mr_status_t st = check_scores(c, logits, ld, grad, ld_grad, true, W, rows, vocab, dtype, scale);
+    if (st != MR_OK) return st;
+    if (!g_logprob && !g_entropy) return report_error(MR_ERR_INVALID_ARGUMENT, "mr_logprob_grad: neither g_logprob nor g_entropy is given");
+    if (rows == 0) return MR_OK;
+    if ((st = per_row(c, ids, 1, "ids", false, g_logprob != nullptr)) != MR_OK) return st;
+    if ((st = per_row(c, stats, 2, "stats", false, true)) != MR_OK) return st;
+    if ((st = per_row(c, entropy, 1, "entropy", false, g_entropy != nullptr)) != MR_OK) return st;
+    if ((st = per_row(c, g_logprob, 1, "g_logprob", false, false)) != MR_OK) return st;
+    if ((st = per_row(c, g_entropy, 1, "g_entropy", false, false)) != MR_OK) return st;
+    if ((st = check_spans(c.spans)) != MR_OK) return st;
+    c.P.ids = ids;
+    c.P.stats_in = stats;
+    c.P.entropy_in = entropy;
+    c.P.g_row = g_logprob;
+    c.P.g_entropy = g_entropy;
+    const dim3 grid = grad_grid(c);
+    return launched(c, mr::launch_logprob_grad(c.P, dtype, grid, (cudaStream_t)stream), grid, 0);
+}
+
+mr_status_t mr_distill_topk(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,
+                            float scale, int K, const long long* teacher_ids, const float* teacher_val, mr_distill_t mode,
+                            float teacher_scale, float* loss, float* stats, void* stream) {
+    mr::clear_error();
+    Call c{"mr_distill_topk", {}, {}};
+    mr_status_t st = check_scores(c, logits, ld, nullptr, nullptr, false, W, rows, vocab, dtype, scale);
+    if (st == MR_OK) st = check_teacher(c, K, teacher_ids, teacher_val, mode, teacher_scale);
+    if (st != MR_OK) return st;
+    if (!loss && !stats) return report_error(MR_ERR_INVALID_ARGUMENT, "mr_distill_topk: no output is asked for");
+    if (rows == 0) return MR_OK;
+    if ((st = per_row(c, loss, 1, "loss", true, false)) != MR_OK) return st;
+    if ((st = per_row(c, stats, 4, "stats", true, false)) != MR_OK) return st;
+    if ((st = check_spans(c.spans)) != MR_OK) return st;
+    c.P.loss = loss;
+    c.P.stats = stats;
+    return run_distill(c, false, stream);
+}
+
+mr_status_t mr_distill_topk_grad(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab,
+                                 mr_dtype_t dtype, float scale, int K, const long long* teacher_ids, const float* teacher_val,
+                                 mr_distill_t mode, float teacher_scale, const float* stats, const float* g_loss,
+                                 void* const* grad, const size_t* ld_grad, void* stream) {
+    mr::clear_error();
+    Call c{"mr_distill_topk_grad", {}, {}};
+    mr_status_t st = check_scores(c, logits, ld, grad, ld_grad, true, W, rows, vocab, dtype, scale);
+    if (st == MR_OK) st = check_teacher(c, K, teacher_ids, teacher_val, mode, teacher_scale);
+    if (st != MR_OK) return st;
+    if (rows == 0) return MR_OK;
+    if ((st = per_row(c, stats, 4, "stats", false, true)) != MR_OK) return st;
+    if ((st = per_row(c, g_loss, 1, "g_loss", false, true)) != MR_OK) return st;
+    if ((st = check_spans(c.spans)) != MR_OK) return st;
+    c.P.stats_in = stats;
+    c.P.g_row = g_loss;
+    const dim3 grid = grad_grid(c);
+    return launched(c, mr::launch_distill_grad(c.P, dtype, grid, (cudaStream_t)stream), grid, 0);
+}
+
+mr_status_t mr_distill_topk_step(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab,
+                                 mr_dtype_t dtype, float scale, int K, const long long* teacher_ids, const float* teacher_val,
+                                 mr_distill_t mode, float teacher_scale, const float* weight, float* loss,
+                                 void* const* grad, const size_t* ld_grad, void* stream) {
+    mr::clear_error();
+    Call c{"mr_distill_topk_step", {}, {}};
+    mr_status_t st = check_scores(c, logits, ld, grad, ld_grad, true, W, rows, vocab, dtype, scale);
+    if (st == MR_OK) st = check_teacher(c, K, teacher_ids, teacher_val, mode, teacher_scale);
+    if (st != MR_OK) return st;
+    if (rows == 0) return MR_OK;
+    if ((st = per_row(c, weight, 1, "weight", false, true)) != MR_OK) return st;
+    if ((st = per_row(c, loss, 1, "loss", true, false)) != MR_OK) return st;
+    if ((st = check_spans(c.spans)) != MR_OK) return st;
+    c.P.g_row = weight;
+    c.P.loss = loss;
+    return run_distill(c, true, stream);
+}
+
+}  // extern "C"

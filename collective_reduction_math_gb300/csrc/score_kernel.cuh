@@ -1,0 +1,395 @@
+// score_kernel.cuh -- what the token-score kernels share: the walk over a row
+// of scores that W simulated ranks hold in shards, and the running softmax
+// statistics.
+//
+// Rank r holds columns [floor(r*V/W), floor((r+1)*V/W)) of every row, so a
+// row is W runs of memory that may start at any element.  The kernels walk a
+// row in superblocks: 32 lanes x 4 vectors of 16 bytes, so 2 KiB of one
+// shard, counted from the shard row's start rounded down to 16 bytes.  A
+// column c of a shard is at place p = c + (elements from that boundary to the
+// row's start); superblock i of the shard holds places [i*kSb, (i+1)*kSb), and
+// vector j of lane l in it the places j*32*VE + l*VE ...: whole-warp loads of
+// 512 consecutive bytes.  A superblock that reaches over either end of the
+// shard row takes the element-wise loads, which read nothing outside it.
+//
+// Scores are y = scale * x.  A thread keeps a running maximum m and the sums
+//     s = sum exp(y - m),   u = sum exp(y - m) * (y - m)
+// of what it has seen, both in fp32 (y - m as one fused multiply-add, the
+// exponential by the 2^x instruction, relative error 2^-22); a new maximum
+// rescales both.  Threads join as  M = max m,  s = sum s_i e^(m_i - M).  NaN
+// and +inf live in m (the maximum passes NaN on), and m = -inf stands for
+// "nothing but -inf so far", where the sums stay 0.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mr_internal.h"
+
+namespace mr {
+
+constexpr float kLog2e = 1.4426950408889634f;
+// Differences y - m are taken no lower where they are a factor: e^d is 0 long
+// before, and 0 * -inf (a mask) or an overflowing product (a mask of the
+// type's lowest value) would be NaN.
+constexpr float kFarBelow = -1e4f;
+constexpr int kSbVectors = kSbRuns;         // 16-byte vectors per lane and superblock
+constexpr int kScoreWarps = kThreads / 32;
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
+
+// ---- packed fp32 pairs (one instruction for two lanes of arithmetic) ----
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(F2 p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// ---- a superblock's raw words, as pairs of scores ----
+template <int DT>
+struct Score;
+template <>
+struct Score<MR_FP32> {
+    static constexpr int kBytes = 4, VE = 4, kPairs = 8, kLogSb = 9, kLogVe = 2;
+    static constexpr uint32_t kFill = 0xff800000u;      // -inf
+    static __device__ __forceinline__ void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
+        a = __uint_as_float(w[2 * i]);
+        b = __uint_as_float(w[2 * i + 1]);
+    }
+    static __device__ __forceinline__ void set_pair(uint32_t (&w)[16], int i, float a, float b) {
+        w[2 * i] = __float_as_uint(a);
+        w[2 * i + 1] = __float_as_uint(b);
+    }
+    static __device__ __forceinline__ float max_words(const uint32_t* w, int n) {
+        float m = __uint_as_float(w[0]);
+#pragma unroll
+        for (int i = 1; i < n; ++i) m = max_nan(m, __uint_as_float(w[i]));
+        return m;
+    }
+    static __device__ __forceinline__ float load_one(const char* a) { return *reinterpret_cast<const volatile float*>(a); }
+    static __device__ __forceinline__ void store_one(char* a, float v) { *reinterpret_cast<volatile float*>(a) = v; }
+    // element e of vector j
+    template <int N>
+    static __device__ __forceinline__ void put(uint32_t (&w)[N], int j, int e, uint32_t bits) { w[4 * j + e] = bits; }
+    template <int N>
+    static __device__ __forceinline__ uint32_t get(const uint32_t (&w)[N], int j, int e) { return w[4 * j + e]; }
+    static __device__ __forceinline__ uint32_t load_bits(const char* a) { return *reinterpret_cast<const volatile uint32_t*>(a); }
+    static __device__ __forceinline__ void store_bits(char* a, uint32_t v) { *reinterpret_cast<volatile uint32_t*>(a) = v; }
+    static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
+};
+template <>
+struct Score<MR_BF16> {
+    static constexpr int kBytes = 2, VE = 8, kPairs = 16, kLogSb = 10, kLogVe = 3;
+    static constexpr uint32_t kFill = 0xff80ff80u;
+    static __device__ __forceinline__ void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
+        a = __uint_as_float(w[i] << 16);
+        b = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void set_pair(uint32_t (&w)[16], int i, float a, float b) {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
+    }
+    static __device__ __forceinline__ float max_words(const uint32_t* w, int n) {
+        uint32_t m = w[0];
+#pragma unroll
+        for (int i = 1; i < n; ++i) m = max_nan_bf16x2(m, w[i]);
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+    static __device__ __forceinline__ float load_one(const char* a) {
+        return __uint_as_float((uint32_t)*reinterpret_cast<const volatile uint16_t*>(a) << 16);
+    }
+    static __device__ __forceinline__ void store_one(char* a, float v) {
+        uint32_t w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v), "f"(v));
+        *reinterpret_cast<volatile uint16_t*>(a) = (uint16_t)w;
+    }
+    template <int N>
+    static __device__ __forceinline__ void put(uint32_t (&w)[N], int j, int e, uint32_t bits) {
+        const int i = 4 * j + e / 2;
+        w[i] = (e & 1) ? (w[i] & 0xffffu) | (bits << 16) : (w[i] & 0xffff0000u) | bits;
+    }
+    template <int N>
+    static __device__ __forceinline__ uint32_t get(const uint32_t (&w)[N], int j, int e) {
+        return (e & 1) ? w[4 * j + e / 2] >> 16 : w[4 * j + e / 2] & 0xffffu;
+    }
+    static __device__ __forceinline__ uint32_t load_bits(const char* a) { return *reinterpret_cast<const volatile uint16_t*>(a); }
+    static __device__ __forceinline__ void store_bits(char* a, uint32_t v) { *reinterpret_cast<volatile uint16_t*>(a) = (uint16_t)v; }
+    static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
+};
+
+// ---- where a row's shard lies ----
+struct ShardRow {
+    char* base;             // the row's start, rounded down to 16 bytes
+    uint32_t lo, hi;        // its places [lo, hi)
+};
+template <int DT>
+__device__ __forceinline__ ShardRow shard_row(const void* x, uint64_t ld, uint64_t row, uint32_t width) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x) + row * ld * Score<DT>::kBytes;
+    ShardRow s;
+    s.base = reinterpret_cast<char*>(a & ~(uintptr_t)15);
+    s.lo = (uint32_t)(a & 15) / Score<DT>::kBytes;
+    s.hi = s.lo + width;
+    return s;
+}
+
+// 16 bytes; kept in program order with the stores around it (a call may be in place).
+__device__ __forceinline__ void load16(uint32_t* w, const char* a) {
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(a));
+}
+__device__ __forceinline__ void store16(char* a, const uint32_t* w) {
+    asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};"
+                 :: "l"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+
+// The vector at places [p, p + VE) as vector j of the words; -inf outside the row.
+template <int DT, int N>
+__device__ __forceinline__ void load_vector(uint32_t (&w)[N], int j, const ShardRow& sr, uint32_t p) {
+    using S = Score<DT>;
+    if (p >= sr.lo && p + S::VE <= sr.hi) {
+        load16(&w[4 * j], sr.base + (uint64_t)p * S::kBytes);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * j + i] = S::kFill;
+#pragma unroll
+        for (int e = 0; e < S::VE; ++e)
+            if (p + e >= sr.lo && p + e < sr.hi) S::put(w, j, e, S::load_bits(sr.base + (uint64_t)(p + e) * S::kBytes));
+    }
+}
+
+// The superblock at places [p0, p0 + kSb) of a shard row; -inf outside it.
+template <int DT>
+__device__ __forceinline__ void load_superblock(uint32_t (&w)[16], const ShardRow& sr, uint32_t p0, int lane) {
+    using S = Score<DT>;
+    if (p0 >= sr.lo && p0 + (1u << S::kLogSb) <= sr.hi) {
+        const char* a = sr.base + ((uint64_t)p0 + (uint32_t)lane * S::VE) * S::kBytes;
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) load16(&w[4 * j], a + j * 512);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) load_vector<DT>(w, j, sr, p0 + (uint32_t)(j * 32 + lane) * S::VE);
+    }
+}
+
+// Stores the superblock's words at the same places of the output's shard row
+// (`out` starts its row at the same column; its own distance to a 16-byte
+// boundary may differ, and then every element is stored by itself).
+template <int DT>
+__device__ __forceinline__ void store_superblock(const uint32_t (&w)[16], const ShardRow& in, const ShardRow& out, uint32_t p0, int lane) {
+    using S = Score<DT>;
+    if (in.lo == out.lo && p0 >= in.lo && p0 + (1u << S::kLogSb) <= in.hi) {
+        char* a = out.base + ((uint64_t)p0 + (uint32_t)lane * S::VE) * S::kBytes;
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) store16(a + j * 512, &w[4 * j]);
+    } else {
+        char* row = out.base + (int64_t)((int)out.lo - (int)in.lo) * S::kBytes;    // place 0 of `in`, in the output
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) {
+            const uint32_t p = p0 + (uint32_t)(j * 32 + lane) * S::VE;
+            if (in.lo == out.lo && p >= in.lo && p + S::VE <= in.hi) {
+                store16(row + (uint64_t)p * S::kBytes, &w[4 * j]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < S::VE; ++e)
+                    if (p + e >= in.lo && p + e < in.hi) S::store_bits(row + (uint64_t)(p + e) * S::kBytes, S::get(w, j, e));
+            }
+        }
+    }
+}
+
+// ---- the walk over a row's superblocks (ordinals count through the shards) ----
+template <int DT>
+struct Walk {
+    int r = -1;                 // current shard
+    uint32_t sb_lo = 0, sb_hi = 0;
+    ShardRow sr{};
+    // Moves to the shard of superblock sb (ascending within a row).
+    __device__ __forceinline__ bool seek(const ScoreParams& P, uint64_t row, uint32_t sb) {
+        if (sb < sb_hi) return false;
+        do {
+            ++r;
+            sb_hi = P.sb0[r + 1];
+        } while (sb >= sb_hi);
+        sb_lo = P.sb0[r];
+        sr = shard_row<DT>(P.x[r], P.ld[r], row, P.col0[r + 1] - P.col0[r]);
+        return true;
+    }
+    __device__ __forceinline__ uint32_t place(uint32_t sb) const { return (sb - sb_lo) << Score<DT>::kLogSb; }
+};
+
+// The shard that holds column c (an fp32 estimate and a short walk).
+__device__ __forceinline__ int shard_of(const ScoreParams& P, uint32_t c) {
+    if (P.W == 1) return 0;
+    int r = (int)((float)c * P.shards_per_col);
+    r = r < 0 ? 0 : r >= P.W ? P.W - 1 : r;
+    while (c < P.col0[r]) --r;
+    while (c >= P.col0[r + 1]) ++r;
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ const char* score_at(const ScoreParams& P, uint64_t row, uint32_t c) {
+    const int r = shard_of(P, c);
+    return static_cast<const char*>(P.x[r]) + (row * P.ld[r] + (c - P.col0[r])) * Score<DT>::kBytes;
+}
+
+// ---- running softmax statistics ----
+struct Stat {
+    float m, s, u;
+};
+
+// Raises the running maximum to at least y (NaN included) and rescales.
+template <bool ENT>
+__device__ __forceinline__ void raise(Stat& a, float y) {
+    if (!(y <= a.m)) {
+        if (a.m != neg_inf()) {
+            const float d = fmaxf(__fadd_rn(a.m, -y), kFarBelow);
+            const float f = ex2(__fmul_rn(d, kLog2e));
+            if (ENT) a.u = __fmul_rn(__fmaf_rn(a.s, d, a.u), f);
+            a.s = __fmul_rn(a.s, f);
+        }
+        a.m = y;
+    }
+}
+
+// One superblock into a thread's statistics.
+template <int DT, bool ENT>
+__device__ __forceinline__ void accumulate(Stat& a, const uint32_t (&w)[16], float scale) {
+    using S = Score<DT>;
+    raise<ENT>(a, __fmul_rn(S::max_words(w, 16), scale));
+    const float ref = a.m == neg_inf() ? 0.0f : a.m;
+    const F2 sc = f2(scale, scale), off = f2(-ref, -ref), l2 = f2(kLog2e, kLog2e);
+    F2 s = f2(0.0f, 0.0f), u = s;
+#pragma unroll
+    for (int i = 0; i < S::kPairs; ++i) {
+        float x0, x1;
+        S::pair(w, i, x0, x1);
+        const F2 t = fma2(f2(x0, x1), sc, off);
+        float e0, e1;
+        unpack(mul2(t, l2), e0, e1);
+        const F2 e = f2(ex2(e0), ex2(e1));
+        s = add2(s, e);
+        if (ENT) {
+            float t0, t1;
+            unpack(t, t0, t1);
+            u = fma2(e, f2(fmaxf(t0, kFarBelow), fmaxf(t1, kFarBelow)), u);
+        }
+    }
+    float p, q;
+    unpack(s, p, q);
+    a.s = __fadd_rn(a.s, __fadd_rn(p, q));
+    if (ENT) {
+        unpack(u, p, q);
+        a.u = __fadd_rn(a.u, __fadd_rn(p, q));
+    }
+}
+
+// A statistic against another maximum M >= m.
+template <bool ENT>
+__device__ __forceinline__ void rebase(Stat& a, float M) {
+    if (a.m == neg_inf()) {
+        a.s = a.u = 0.0f;
+    } else {
+        const float d = fmaxf(__fadd_rn(a.m, -M), kFarBelow);
+        const float f = expf(d);
+        if (ENT) a.u = a.s == 0.0f ? 0.0f : __fmul_rn(__fmaf_rn(a.s, d, a.u), f);
+        a.s = __fmul_rn(a.s, f);
+    }
+    a.m = M;
+}
+
+// Joins the statistics of a warp's lanes; every lane gets the result.
+template <bool ENT>
+__device__ __forceinline__ Stat warp_join(Stat a) {
+    float M = a.m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = max_nan(M, __shfl_xor_sync(~0u, M, o));
+    rebase<ENT>(a, M);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        a.s = __fadd_rn(a.s, __shfl_xor_sync(~0u, a.s, o));
+        if (ENT) a.u = __fadd_rn(a.u, __shfl_xor_sync(~0u, a.u, o));
+    }
+    return a;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+
+// A row's final pair: the largest scaled score and the log of the sum of
+// exponentials relative to it; (-inf, 0) for a row of nothing but -inf, NaN
+// for both where a NaN or +inf was seen.
+__device__ __forceinline__ void finish(const Stat& a, float& m, float& logs) {
+    if (a.m == neg_inf()) {
+        m = a.m;
+        logs = 0.0f;
+    } else if (!(a.m < __int_as_float(0x7f800000))) {
+        m = logs = quiet_nan();
+    } else {
+        m = a.m;
+        logs = logf(a.s);
+    }
+}
+
+// ---- thread-block clusters ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void peer_store(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+}  // namespace mr

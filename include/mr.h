@@ -246,6 +246,115 @@ mr_status_t mr_allreduce_ex(const void* const* send, void* const* recv, int W, s
 mr_status_t mr_reduce_scatter_ex(const void* const* send, void* const* recv, int W, size_t N, mr_dtype_t dtype,
                                  mr_op_t op, const mr_order_t* order, void* stream);
 
+/*
+ * Token scores over a vocabulary in shards [SCORE].  `rows` rows of `vocab`
+ * scores (logits), one row per token; rank r holds columns
+ * [floor(r*vocab/W), floor((r+1)*vocab/W)) of every row ([EQ2], as
+ * mr_chunk_lo).  The reductions over a row -- maximum, sum of exponentials,
+ * top k -- run across the W shards in one kernel.
+ *   logits[r]: rank r's columns of row 0; ld[r] elements from one row to the
+ *     next, at least the rank's columns (ld NULL: exactly those).  Any
+ *     alignment to the element; rows on 16-byte boundaries are read fastest.
+ *     A rank with no column (vocab < W) is never looked at.
+ *   dtype: MR_FP32 or MR_BF16 (MR_INT32 returns MR_ERR_UNSUPPORTED);
+ *     1 <= vocab < 2^31; rows == 0 is a no-op.
+ *   y = scale * x (scale positive and finite: 1 / temperature), in fp32; all
+ *     sums are fp32 over a fixed split of the row, the same on every run;
+ *     results in dtype are rounded once.
+ *   -inf is a masked place: it has no part in any sum and gradient 0.  A row
+ *     with a NaN or a +inf has NaN for its statistics, log probabilities,
+ *     entropy, loss and gradients.
+ *   Overlaps: an output overlaps nothing else, except that grad[r] may be
+ *     logits[r] with the same stride (in place), and that rank buffers may be
+ *     column slices of one buffer (same stride, columns beside each other).
+ * [SCORE] NCCL M2N, the introduction's RL refit; post on NCCL all-reduce, the
+ * decode path that mr_allreduce_rmsnorm serves.  The pages name the workloads
+ * and give no formulas for these operators: the definitions here are the
+ * library's own.
+ */
+#define MR_MAX_TOP 64               /* top alternatives per row */
+#define MR_MAX_TOP_VOCAB 4194304    /* columns of a row with top_k > 0 */
+#define MR_MAX_TEACHER 128          /* teacher entries per row */
+
+/*
+ * Log probabilities of given tokens, with entropy and top alternatives.
+ * For a row with m = max y and lse = log sum exp(y):
+ *   logprob[t] = y[ids[t]] - lse (ids may be NULL if logprob is);
+ *   entropy[t] = lse - sum softmax(y) y;
+ *   stats[2t], stats[2t+1] = m, lse - m: what mr_logprob_grad takes;
+ *   top_ids, top_logprob [t * top_k + i]: the i-th largest score's column and
+ *     y - lse: larger first, equal scores (-0 equals +0) lower column first,
+ *     NaN above all.  0 <= top_k <= min(MR_MAX_TOP, vocab); vocab at most
+ *     MR_MAX_TOP_VOCAB where top_k > 0 (else MR_ERR_UNSUPPORTED).
+ * Any output may be NULL.  ids[t] < 0 leaves the row out: it is not read, and
+ * gets logprob 0, entropy 0, stats (-inf, 0), top_ids -1, top_logprob -inf.
+ * ids[t] >= vocab gives logprob NaN.  A row of nothing but -inf has stats
+ * (-inf, 0), entropy 0 and log probabilities -inf.
+ */
+mr_status_t mr_logprob(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,
+                       float scale, const long long* ids, int top_k, float* logprob, float* entropy, float* stats,
+                       long long* top_ids, float* top_logprob, void* stream);
+
+/*
+ * Its gradient: with p = softmax(y), lp = y - lse, H the entropy,
+ *   grad[t][i] = scale * ( g_logprob[t] * ([i == ids[t]] - p_i)
+ *                          - g_entropy[t] * p_i * (lp_i + H) ).
+ *   g_logprob (with ids) or g_entropy (with entropy, as mr_logprob gave it)
+ *   may be NULL, not both; stats as mr_logprob gave them.  Rows left out get
+ *   zeros; ids[t] >= vocab gives the row NaN.
+ */
+mr_status_t mr_logprob_grad(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,
+                            float scale, const long long* ids, const float* stats, const float* entropy,
+                            const float* g_logprob, const float* g_entropy, void* const* grad, const size_t* ld_grad,
+                            void* stream);
+
+/*
+ * Distillation from a teacher's top logits: the divergence of the student's
+ * softmax(y) from the teacher's distribution, known at K places of each row.
+ *   teacher_ids, teacher_val [t * K + k]: column and value of entry k;
+ *     1 <= K <= MR_MAX_TEACHER.  A negative column is no entry (a list may be
+ *     shorter than K); the columns of a row are distinct; a column >= vocab
+ *     gives the row NaN.
+ *   MR_DISTILL_RENORM: q = softmax(teacher_scale * val) over the list;
+ *   MR_DISTILL_TAIL:   q = exp(val) (val are the teacher's log probabilities,
+ *     as mr_logprob's top_logprob; teacher_scale must be 1), and the remaining
+ *     mass q_R = max(0, 1 - sum q) is one more outcome, against the student's
+ *     mass p_R outside the list.
+ *   loss[t] = sum q (log q - log p) [+ q_R (log q_R - log p_R)], 0 log 0 = 0;
+ *     +inf where the student has masked a place with q > 0.
+ *   stats[4t..]: m and lse - m over the row, then over the places outside the
+ *     list: what mr_distill_topk_grad takes.  Loss or stats may be NULL.
+ * A row with no entry is left out: not read, loss 0, stats (-inf, 0, -inf, 0),
+ * gradient 0.  So is, in the renormalised mode, the loss and gradient of a row
+ * whose teacher values are all -inf.
+ */
+typedef enum { MR_DISTILL_RENORM = 0, MR_DISTILL_TAIL = 1 } mr_distill_t;
+
+mr_status_t mr_distill_topk(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,
+                            float scale, int K, const long long* teacher_ids, const float* teacher_val, mr_distill_t mode,
+                            float teacher_scale, float* loss, float* stats, void* stream);
+
+/*
+ * Its gradient: grad[t][i] = g_loss[t] * d loss[t] / d x[t][i].  With q_i = 0
+ * outside the list, p_i - q_i, less softmax over the outside * q_R there,
+ * times scale.
+ */
+mr_status_t mr_distill_topk_grad(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab,
+                                 mr_dtype_t dtype, float scale, int K, const long long* teacher_ids, const float* teacher_val,
+                                 mr_distill_t mode, float teacher_scale, const float* stats, const float* g_loss,
+                                 void* const* grad, const size_t* ld_grad, void* stream);
+
+/*
+ * Loss and gradient in one kernel, for a training step that knows each
+ * token's weight in advance: loss[t] (unweighted, may be NULL) and
+ * grad[t][i] = weight[t] * d loss[t] / d x[t][i].  The row stays in shared
+ * memory between the two, so it is read from HBM once.
+ */
+mr_status_t mr_distill_topk_step(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab,
+                                 mr_dtype_t dtype, float scale, int K, const long long* teacher_ids, const float* teacher_val,
+                                 mr_distill_t mode, float teacher_scale, const float* weight, float* loss,
+                                 void* const* grad, const size_t* ld_grad, void* stream);
+
 /* A static, human-readable name of a status code. */
 const char* mr_status_string(mr_status_t status);
 
