@@ -31,31 +31,43 @@ constexpr uint32_t kNoPlace = ~0u;     // past every superblock: a row has fewer
 // A warp's copy of a row's list: entry k = lane + 32 i.
 struct List {
     uint32_t place[kListRegs];      // in units of scores, counted through the row's superblocks; kNoPlace if absent
-    float v[kListRegs];             // the teacher's value; NaN for a column past the vocabulary
+    float v[kListRegs];             // the teacher's value; -inf if absent, NaN for a column past the vocabulary
     bool some;                      // any entry at all
 };
 
+// The list as it lies in memory.
+struct RawList {
+    long long id[kListRegs];
+    float v[kListRegs];
+};
+__device__ __forceinline__ void load_raw(RawList& R, const ScoreParams& P, uint64_t row, int lane) {
+#pragma unroll
+    for (int i = 0; i < kListRegs; ++i) {
+        const int k = lane + 32 * i;
+        R.id[i] = -1;
+        R.v[i] = neg_inf();
+        if (k < P.K) {
+            R.id[i] = P.t_ids[row * P.K + k];
+            R.v[i] = P.t_val[row * P.K + k];
+        }
+    }
+}
 template <int DT>
-__device__ __forceinline__ void load_list(List& L, const ScoreParams& P, uint64_t row, int lane) {
+__device__ __forceinline__ void place_list(List& L, const RawList& R, const ScoreParams& P, uint64_t row, int regs) {
     using S = Score<DT>;
     bool some = false;
 #pragma unroll
     for (int i = 0; i < kListRegs; ++i) {
         L.place[i] = kNoPlace;
         L.v[i] = neg_inf();
-        const int k = lane + 32 * i;
-        if (k < P.K) {
-            const long long id = P.t_ids[row * P.K + k];
-            if (id >= 0) {
-                some = true;
-                L.v[i] = P.t_val[row * P.K + k];
-                if (id >= (long long)P.vocab) {
-                    L.v[i] = quiet_nan();
-                } else {
-                    const int r = shard_of(P, (uint32_t)id);
-                    const ShardRow sr = shard_row<DT>(P.x[r], P.ld[r], row, 0);
-                    L.place[i] = (P.sb0[r] << S::kLogSb) + ((uint32_t)id - P.col0[r] + sr.lo);
-                }
+        const long long id = i < regs ? R.id[i] : -1;
+        if (id >= 0) {
+            some = true;
+            L.v[i] = id < (long long)P.vocab ? R.v[i] : quiet_nan();
+            if (id < (long long)P.vocab) {
+                const int r = shard_of(P, (uint32_t)id);
+                const ShardRow sr = shard_row<DT>(P.x[r], P.ld[r], row, 0);
+                L.place[i] = (P.sb0[r] << S::kLogSb) + ((uint32_t)id - P.col0[r] + sr.lo);
             }
         }
     }
@@ -117,14 +129,41 @@ __device__ __forceinline__ void teacher_mass(Teacher& t, const List& L, const Sc
     }
 }
 
-// Takes the listed places of superblock sb out of its words.
+// Takes the listed places of superblock sb out of its words: where there are
+// any (one vote), through the warp's 2 KiB of shared memory.  Selecting them
+// in registers, 32 tests a lane, cost as much as the superblock's sum.
 template <int DT>
-__device__ __forceinline__ void mask_listed(uint32_t (&w)[16], const List& L, uint32_t sb, int lane, int regs) {
+__device__ __forceinline__ void mask_listed(uint32_t (&w)[16], const List& L, uint32_t sb, uint4* bounce, int lane) {
+    using S = Score<DT>;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kListRegs; ++i) any |= (L.place[i] >> S::kLogSb) == sb;
+    if (!__any_sync(~0u, any)) return;
+#pragma unroll
+    for (int j = 0; j < kSbVectors; ++j) bounce[j * 32 + lane] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kListRegs; ++i)
+        if ((L.place[i] >> S::kLogSb) == sb)
+            S::mask_one(reinterpret_cast<char*>(bounce) + (size_t)(L.place[i] & ((1u << S::kLogSb) - 1)) * S::kBytes);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kSbVectors; ++j) {
+        const uint4 v = bounce[j * 32 + lane];
+        w[4 * j] = v.x;
+        w[4 * j + 1] = v.y;
+        w[4 * j + 2] = v.z;
+        w[4 * j + 3] = v.w;
+    }
+}
+
+// The same for rows too long for the cache, which leave no shared memory.
+template <int DT>
+__device__ __forceinline__ void mask_listed_in_registers(uint32_t (&w)[16], const List& L, uint32_t sb, int lane) {
     using S = Score<DT>;
     uint32_t mine = 0;      // this lane's listed places, bit VE * vector + element
 #pragma unroll
     for (int i = 0; i < kListRegs; ++i) {
-        if (i >= regs) break;
         uint32_t hit = __ballot_sync(~0u, (L.place[i] >> S::kLogSb) == sb);
         while (hit) {
             const uint32_t p = __shfl_sync(~0u, L.place[i], __ffs(hit) - 1) & ((1u << S::kLogSb) - 1);
@@ -141,224 +180,342 @@ __device__ __forceinline__ void mask_listed(uint32_t (&w)[16], const List& L, ui
     }
 }
 
-// What the gradient of a row needs.
+// What the gradient outside the list needs: coef * 2^(c x - ref).
 struct Coef {
-    float m_rest, c_rest;       // others: c_rest * e^(y - m_rest)
+    float c, ref, coef;
 };
 
 // The places of a superblock turned into gradients.
 template <int DT>
-__device__ __forceinline__ void rest_gradient(uint32_t (&w)[16], const Coef& c, float scale) {
+__device__ __forceinline__ void rest_gradient(uint32_t (&w)[16], const Coef& k) {
     using S = Score<DT>;
-    const F2 sc = f2(scale, scale), off = f2(-c.m_rest, -c.m_rest), l2 = f2(kLog2e, kLog2e), f = f2(c.c_rest, c.c_rest);
+    const F2 cc = f2(k.c, k.c), off = f2(-k.ref, -k.ref), f = f2(k.coef, k.coef);
 #pragma unroll
     for (int i = 0; i < S::kPairs; ++i) {
-        float x0, x1, e0, e1;
+        float x0, x1, t0, t1;
         S::pair(w, i, x0, x1);
-        unpack(mul2(fma2(f2(x0, x1), sc, off), l2), e0, e1);
-        unpack(mul2(f2(ex2(e0), ex2(e1)), f), x0, x1);
+        unpack(fma2(f2(x0, x1), cc, off), t0, t1);
+        unpack(mul2(f2(ex2(t0), ex2(t1)), f), x0, x1);
         S::set_pair(w, i, x0, x1);
     }
 }
 
-template <int DT, bool STEP>
-__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_constant__ ScoreParams P) {
+__device__ __forceinline__ void copy16(uint32_t to, const char* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
+}
+// One superblock of a row into the CTA's cache (slots of 16 bytes that only
+// this thread touches): whole vectors by asynchronous copies, the row's ends
+// element by element.
+template <int DT>
+__device__ __forceinline__ void cache_superblock(uint4* slot, const ShardRow& sr, uint32_t p0, int lane) {
     using S = Score<DT>;
-    extern __shared__ uint4 cache[];        // STEP: this CTA's part of the row, [round][vector][thread]
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
+    const char* from = sr.base + ((uint64_t)p0 + (uint32_t)lane * S::VE) * S::kBytes;
+    if (p0 >= sr.lo && p0 + (1u << S::kLogSb) <= sr.hi) {
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) copy16(to + j * kThreads * 16, from + j * 512);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) {
+            const uint32_t p = p0 + (uint32_t)(j * 32 + lane) * S::VE;
+            if (p >= sr.lo && p + S::VE <= sr.hi) {
+                copy16(to + j * kThreads * 16, from + j * 512);
+            } else {
+                uint32_t v[4];
+                load_vector<DT>(v, 0, sr, p);
+                slot[j * kThreads] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// This thread's copies are there.
+__device__ __forceinline__ void cache_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void from_cache(uint32_t (&w)[16], const uint4* slot) {
+#pragma unroll
+    for (int j = 0; j < kSbVectors; ++j) {
+        const uint4 v = slot[j * kThreads];
+        w[4 * j] = v.x;
+        w[4 * j + 1] = v.y;
+        w[4 * j + 2] = v.z;
+        w[4 * j + 3] = v.w;
+    }
+}
+
+template <int DT, bool STEP>
+__global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_constant__ ScoreParams P) {
+    using S = Score<DT>;
+    extern __shared__ uint4 cache[];        // STEP: this CTA's part of a row, [round][vector][thread]
     __shared__ Stat part[2][kMaxScoreCluster * kScoreWarps];
+    __shared__ uint32_t s_place[2][MR_MAX_TEACHER];
+    __shared__ int row_out[2];              // the row is left out
     __shared__ float s_grad[MR_MAX_TEACHER];        // STEP: the listed places' gradients
     __shared__ Coef s_coef;
+    __shared__ uint4 bounce[STEP ? 1 : kScoreWarps][STEP ? 1 : kSbVectors * 32];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int C = P.csize, crank = C > 1 ? (int)cluster_rank() : 0;
     const uint32_t nsb = P.sb0[P.W];
     const uint32_t sb_lo = (uint32_t)((uint64_t)nsb * crank / C), sb_hi = (uint32_t)((uint64_t)nsb * (crank + 1) / C);
+    const uint64_t stride = gridDim.x / C;
+    uint64_t row = blockIdx.x / C;
     const int regs = (P.K + 31) / 32;
+    if (C > 1) cluster_arrive();        // every CTA of the cluster has started: waited for before the first store to a peer
     pdl_enter();
 
+    if (warp < kScoreWarps) {
+        // ================= the stream =================
+        uint32_t w[16];
+        Walk<DT> walk;
+        const uint32_t first = sb_lo + warp;
+        const uint32_t my_rounds = first < sb_hi ? (sb_hi - first + kScoreWarps - 1) / kScoreWarps : 0;
+        const uint32_t cached = STEP ? min(my_rounds, P.cache_rounds) : 0;
+        uint4* const slots = cache + threadIdx.x;
+        auto fetch = [&](uint32_t (&to)[16], uint64_t r, uint32_t sb) {
+            walk.seek(P, r, sb);
+            load_superblock<DT>(to, walk.sr, walk.place(sb), lane);
+        };
+        if (row < P.rows && my_rounds) {
+            if constexpr (STEP) {
+                for (uint32_t i = 0; i < cached; ++i) {
+                    walk.seek(P, row, first + i * kScoreWarps);
+                    cache_superblock<DT>(slots + i * kSbVectors * kThreads, walk.sr, walk.place(first + i * kScoreWarps), lane);
+                }
+            } else {
+                fetch(w, row, first);
+            }
+        }
+        bool waited = C == 1;
+        int parity = 0;
+        for (; row < P.rows; row += stride, parity ^= 1) {
+            bar_sync(kRowReady + parity);
+            const bool out = row_out[parity];
+            List L;
+#pragma unroll
+            for (int i = 0; i < kListRegs; ++i) L.place[i] = i < regs ? s_place[parity][lane + 32 * i] : kNoPlace;
+            const uint64_t next_row = row + stride;
+            Running run = start_running(P.c);
+            if constexpr (!STEP) {
+                if (out) {
+                    walk = Walk<DT>{};
+                    if (next_row < P.rows && my_rounds) fetch(w, next_row, first);
+                } else {
+                    for (uint32_t sb = first; sb < sb_hi; sb += kScoreWarps) {
+                        uint32_t nx[16];
+                        if (sb + kScoreWarps < sb_hi) {
+                            fetch(nx, row, sb + kScoreWarps);
+                        } else if (next_row < P.rows) {     // the next row's first, left out or not
+                            walk = Walk<DT>{};
+                            fetch(nx, next_row, first);
+                        }
+                        mask_listed<DT>(w, L, sb, bounce[warp], lane);
+                        accumulate<DT, false>(run, w, P.c);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = nx[i];
+                    }
+                }
+            } else if (!out) {
+                // this row's copies are there; the listed places of this warp's superblocks leave the cache
+                cache_wait();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kListRegs; ++i) {
+                    const uint32_t sb = L.place[i] >> S::kLogSb, round = (sb - first) / kScoreWarps;
+                    if (sb >= first && (sb - first) % kScoreWarps == 0 && round < cached) {
+                        const uint32_t at = L.place[i] & ((1u << S::kLogSb) - 1);      // vector, lane and element in it
+                        char* slot = reinterpret_cast<char*>(
+                            cache + ((round * kSbVectors + (at >> (S::kLogVe + 5))) * kThreads + warp * 32 + ((at >> S::kLogVe) & 31)));
+                        S::mask_one(slot + (at & (S::VE - 1)) * S::kBytes);
+                    }
+                }
+                __syncwarp();
+                for (uint32_t i = 0; i < cached; ++i) {
+                    from_cache(w, slots + i * kSbVectors * kThreads);
+                    accumulate<DT, false>(run, w, P.c);
+                }
+                walk = Walk<DT>{};
+                for (uint32_t i = cached; i < my_rounds; ++i) {     // a row longer than the cache
+                    const uint32_t sb = first + i * kScoreWarps;
+                    fetch(w, row, sb);
+                    mask_listed_in_registers<DT>(w, L, sb, lane);
+                    accumulate<DT, false>(run, w, P.c);
+                }
+            }
+            Stat a = run.a;
+            if (!out) a = warp_join<false>(a, P.c);
+            if (!waited) cluster_wait();
+            waited = true;
+            if (!out) {
+                if (C == 1) {
+                    if (lane == 0) part[parity][warp] = a;
+                } else if (lane < (STEP ? C : 1)) {
+                    const uint32_t to = peer_address(&part[parity][crank * kScoreWarps + warp], lane);
+                    peer_store(to, __float_as_uint(a.x));
+                    peer_store(to + 4, __float_as_uint(a.s));
+                }
+            }
+            if (C > 1) {
+                __syncwarp();
+                cluster_arrive();
+                waited = false;     // for this row's phase: before the next row's store, or the end
+            } else {
+                bar_arrive(kRowDone + parity);
+            }
+            if constexpr (STEP) {
+                Coef coef{P.c, 0.0f, 0.0f};
+                if (!waited) cluster_wait();
+                waited = true;
+                bar_sync(kRowStep);
+                if (!out) coef = s_coef;
+                Walk<DT> ahead;
+                walk = Walk<DT>{};
+                ShardRow to{};
+                uint32_t sb = first;
+                if (out) cache_wait();      // its copies, before the next row's into the same slots
+                for (uint32_t i = 0; i < my_rounds; ++i, sb += kScoreWarps) {
+                    if (walk.seek(P, row, sb)) to = shard_row<DT>(P.g[walk.r], P.ldg[walk.r], row, P.col0[walk.r + 1] - P.col0[walk.r]);
+                    const uint32_t p0 = walk.place(sb);
+                    if (out) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = 0;
+                    } else {
+                        if (i < cached) from_cache(w, slots + i * kSbVectors * kThreads);
+                        else load_superblock<DT>(w, walk.sr, p0, lane);
+                        rest_gradient<DT>(w, coef);
+                    }
+                    if (i < cached && next_row < P.rows) {      // the slot is free: the next row's copy into it
+                        ahead.seek(P, next_row, sb);
+                        cache_superblock<DT>(slots + i * kSbVectors * kThreads, ahead.sr, ahead.place(sb), lane);
+                    }
+                    store_superblock<DT>(w, walk.sr, to, p0, lane);
+#pragma unroll
+                    for (int e = 0; e < kListRegs; ++e) {
+                        if (e >= regs) break;
+                        const bool mine = (L.place[e] >> S::kLogSb) == sb;
+                        if (__any_sync(~0u, mine)) {        // after the vector stores of every lane
+                            __syncwarp();
+                            if (mine)
+                                S::store_one(to.base + (uint64_t)(L.place[e] - (walk.sb_lo << S::kLogSb) - walk.sr.lo + to.lo) * S::kBytes,
+                                             s_grad[lane + 32 * e]);
+                        }
+                    }
+                }
+            }
+        }
+        if (!waited) cluster_wait();
+        return;
+    }
+
+    // ================= the row warp =================
+    const bool joins = STEP || crank == 0;
+    RawList raw;        // the list after the one in `cur` / `next`
+    List cur, next;
+    float x[kListRegs], x_next[kListRegs];
+    // Sets a row up: places for the stream, then the listed scores.
+    auto set_up = [&](uint64_t r, int par) {
+        place_list<DT>(next, raw, P, r, regs);
+#pragma unroll
+        for (int i = 0; i < kListRegs; ++i)
+            if (i < regs) s_place[par][lane + 32 * i] = next.place[i];
+        if (lane == 0) row_out[par] = !next.some;
+        bar_arrive(kRowReady + par);
+        if (r + stride < P.rows) load_raw(raw, P, r + stride, lane);
+        if (joins) {
+#pragma unroll
+            for (int i = 0; i < kListRegs; ++i) {
+                x_next[i] = neg_inf();
+                if (next.place[i] != kNoPlace) x_next[i] = listed_score<DT>(P, r, next.place[i]);
+            }
+        }
+    };
+    if (row < P.rows) {
+        load_raw(raw, P, row, lane);
+        set_up(row, 0);
+    }
+    if (C > 1) cluster_wait();
     int parity = 0;
-    for (uint64_t row = blockIdx.x / C; row < P.rows; row += gridDim.x / C) {
-        List L;
-        load_list<DT>(L, P, row, lane);
-        if (!L.some) {      // left out
-            if (crank == 0 && threadIdx.x == 0) {
+    for (; row < P.rows; row += stride, parity ^= 1) {
+        cur = next;
+#pragma unroll
+        for (int i = 0; i < kListRegs; ++i) x[i] = x_next[i];
+        if (row + stride < P.rows) set_up(row + stride, parity ^ 1);
+        const bool out = !cur.some;
+        Teacher t;
+        Stat l{neg_inf(), 0.0f, 0.0f};      // the listed scores, as one more statistic
+        float g = 0.0f;
+        if (joins && !out) {
+            if (STEP) g = __fmul_rn(P.scale, P.g_row[row]);
+            teacher_mass(t, cur, P);
+#pragma unroll
+            for (int i = 0; i < kListRegs; ++i) l.x = max_nan(l.x, x[i]);
+            l.x = warp_max_nan(l.x);
+            if (l.x != neg_inf()) {
+#pragma unroll
+                for (int i = 0; i < kListRegs; ++i) l.s = __fadd_rn(l.s, ex2(__fmul_rn(__fadd_rn(x[i], -l.x), P.c)));
+                l.s = warp_sum(l.s);
+            }
+        }
+        if (C == 1) {
+            bar_sync(kRowDone + parity);
+        } else {
+            cluster_arrive();
+            cluster_wait();
+        }
+        if (!joins) continue;
+        if (out) {
+            if (lane == 0 && crank == 0) {
                 if (P.loss) P.loss[row] = 0.0f;
                 if (P.stats) {
                     P.stats[4 * row] = P.stats[4 * row + 2] = neg_inf();
                     P.stats[4 * row + 1] = P.stats[4 * row + 3] = 0.0f;
                 }
             }
-            if (STEP) {
-                Walk<DT> walk;
-                ShardRow out{};
-                uint32_t w[16] = {};
-                for (uint32_t sb = sb_lo + warp; sb < sb_hi; sb += kScoreWarps) {
-                    if (walk.seek(P, row, sb))
-                        out = shard_row<DT>(P.g[walk.r], P.ldg[walk.r], row, P.col0[walk.r + 1] - P.col0[walk.r]);
-                    store_superblock<DT>(w, walk.sr, out, walk.place(sb), lane);
-                }
-            }
+            if (STEP) bar_arrive(kRowStep);
             continue;
         }
-        const bool lister = warp == 0 && (STEP || crank == 0);      // the warp that joins
-        float x[kListRegs];
-        if (lister) {
-#pragma unroll
-            for (int i = 0; i < kListRegs; ++i) {
-                x[i] = neg_inf();
-                if (L.place[i] != kNoPlace) x[i] = listed_score<DT>(P, row, L.place[i]);
-            }
-        }
-
-        // ---- the stream over the places outside the list ----
-        Stat a{neg_inf(), 0.0f, 0.0f};
+        const Stat b = join_parts<false>(part[parity], C * kScoreWarps, lane, P.c);
+        Stat all{max_nan(b.x, l.x), 0.0f, 0.0f};
         {
-            Walk<DT> walk;
-            uint32_t w[16], nx[16];
-            uint32_t sb = sb_lo + warp, round = 0;
-            if (sb < sb_hi) {
-                walk.seek(P, row, sb);
-                load_superblock<DT>(w, walk.sr, walk.place(sb), lane);
-            }
-            while (sb < sb_hi) {
-                const uint32_t next = sb + kScoreWarps;
-                if (next < sb_hi) {
-                    walk.seek(P, row, next);
-                    load_superblock<DT>(nx, walk.sr, walk.place(next), lane);
-                }
-                if (STEP && round < P.cache_rounds) {
-#pragma unroll
-                    for (int j = 0; j < kSbVectors; ++j)
-                        cache[(round * kSbVectors + j) * kThreads + threadIdx.x] =
-                            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                }
-                mask_listed<DT>(w, L, sb, lane, regs);
-                accumulate<DT, false>(a, w, P.scale);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = nx[i];
-                sb = next;
-                ++round;
-            }
+            Stat r = b;
+            rebase<false>(r, all.x, P.c);
+            rebase<false>(l, all.x, P.c);
+            all.s = __fadd_rn(r.s, l.s);
         }
-        a = warp_join<false>(a);
-
-        // ---- join ----
-        if (lane == 0 && C == 1) part[parity][warp] = a;
-        if (C > 1 && lane < (STEP ? C : 1)) {
-            const uint32_t to = peer_address(&part[parity][crank * kScoreWarps + warp], lane);
-            peer_store(to, __float_as_uint(a.m));
-            peer_store(to + 4, __float_as_uint(a.s));
-        }
-        Teacher t;
-        if (lister) teacher_mass(t, L, P);
-        if (C == 1) __syncthreads();
-        else cluster_barrier();
-        if (lister) {
-            Stat b{neg_inf(), 0.0f, 0.0f};
-            for (int i = lane; i < C * kScoreWarps; i += 32) {
-                Stat o{part[parity][i].m, part[parity][i].s, 0.0f};
-                const float M = max_nan(b.m, o.m);
-                rebase<false>(b, M);
-                rebase<false>(o, M);
-                b.s = __fadd_rn(b.s, o.s);
-            }
-            b = warp_join<false>(b);
-            // the listed scores, as one more statistic
-            float y[kListRegs];
-            Stat l{neg_inf(), 0.0f, 0.0f};
+        const Final f = finish(all, P.scale), rest = finish(b, P.scale);
+        const float logp_rest = rest.m == neg_inf() ? neg_inf()
+                              : __fmaf_rn(__fadd_rn(b.x, -all.x), P.scale, __fadd_rn(rest.log_s, -f.log_s));
+        float logp[kListRegs];
 #pragma unroll
-            for (int i = 0; i < kListRegs; ++i) {
-                y[i] = __fmul_rn(x[i], P.scale);
-                l.m = max_nan(l.m, y[i]);
-            }
-            l.m = warp_max_nan(l.m);
-            if (l.m != neg_inf()) {
-#pragma unroll
-                for (int i = 0; i < kListRegs; ++i) l.s = __fadd_rn(l.s, expf(__fmaf_rn(x[i], P.scale, -l.m)));
-                l.s = warp_sum(l.s);
-            }
-            Stat all{max_nan(b.m, l.m), 0.0f, 0.0f};
-            {
-                Stat r = b;
-                rebase<false>(r, all.m);
-                rebase<false>(l, all.m);
-                all.s = __fadd_rn(r.s, l.s);
-            }
-            float m, logs, m_rest, logs_rest;
-            finish(all, m, logs);
-            finish(b, m_rest, logs_rest);
-            const float logp_rest = m_rest == neg_inf() ? neg_inf() : __fadd_rn(__fadd_rn(m_rest, -m), __fadd_rn(logs_rest, -logs));
-            const float p_rest = expf(logp_rest);
-            const float g = STEP ? __fmul_rn(P.scale, P.g_row ? P.g_row[row] : 1.0f) : 0.0f;
-            float loss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kListRegs; ++i) {
-                const float logp = x[i] == neg_inf() && m == m ? neg_inf() : __fadd_rn(__fmaf_rn(x[i], P.scale, -m), -logs);
-                if (!(t.q[i] == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q[i], __fadd_rn(t.logq[i], -logp)));
-                if (STEP && lane + 32 * i < P.K)
-                    s_grad[lane + 32 * i] = x[i] == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(expf(logp), t.Q, -t.q[i]));
-            }
-            loss = warp_sum(loss);
-            if (!(t.q_rest == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q_rest, __fadd_rn(logf(t.q_rest), -logp_rest)));
-            if (lane == 0) {
-                if (crank == 0) {
-                    if (P.loss) P.loss[row] = loss;
-                    if (P.stats) {
-                        P.stats[4 * row] = m;
-                        P.stats[4 * row + 1] = logs;
-                        P.stats[4 * row + 2] = m_rest;
-                        P.stats[4 * row + 3] = logs_rest;
-                    }
-                }
-                if (STEP) {
-                    const bool none = m_rest == neg_inf();
-                    s_coef.m_rest = none ? 0.0f : m_rest;
-                    s_coef.c_rest = none ? 0.0f : __fdiv_rn(__fmul_rn(g, __fmaf_rn(p_rest, t.Q, -t.q_rest)), b.s);
-                }
-            }
+        for (int i = 0; i < kListRegs; ++i) {
+            logp[i] = log_prob(x[i], all, f, P.scale);
+            if (STEP && lane + 32 * i < P.K)
+                s_grad[lane + 32 * i] = x[i] == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(expf(logp[i]), t.Q, -t.q[i]));
         }
         if (STEP) {
-            __syncthreads();
-            const Coef c = s_coef;
-            Walk<DT> walk;
-            ShardRow out{};
-            uint32_t round = 0;
-            for (uint32_t sb = sb_lo + warp; sb < sb_hi; sb += kScoreWarps, ++round) {
-                if (walk.seek(P, row, sb))
-                    out = shard_row<DT>(P.g[walk.r], P.ldg[walk.r], row, P.col0[walk.r + 1] - P.col0[walk.r]);
-                const uint32_t p0 = walk.place(sb);
-                uint32_t w[16];
-                if (round < P.cache_rounds) {
-#pragma unroll
-                    for (int j = 0; j < kSbVectors; ++j) {
-                        const uint4 v = cache[(round * kSbVectors + j) * kThreads + threadIdx.x];
-                        w[4 * j] = v.x;
-                        w[4 * j + 1] = v.y;
-                        w[4 * j + 2] = v.z;
-                        w[4 * j + 3] = v.w;
-                    }
-                } else {
-                    load_superblock<DT>(w, walk.sr, p0, lane);
-                }
-                rest_gradient<DT>(w, c, P.scale);
-                store_superblock<DT>(w, walk.sr, out, p0, lane);
-#pragma unroll
-                for (int i = 0; i < kListRegs; ++i) {
-                    if (i >= regs) break;
-                    const bool mine = (L.place[i] >> S::kLogSb) == sb;
-                    if (__any_sync(~0u, mine)) {        // after the vector stores of every lane
-                        __syncwarp();
-                        if (mine)
-                            S::store_one(out.base + (uint64_t)(L.place[i] - (walk.sb_lo << S::kLogSb) - walk.sr.lo + out.lo) * S::kBytes,
-                                         s_grad[lane + 32 * i]);
-                    }
-                }
+            if (lane == 0) {
+                const Ref k = reference(b.x, P.c);
+                const float mass = __fmul_rn(g, __fmaf_rn(expf(logp_rest), t.Q, -t.q_rest));
+                s_coef = {k.c, k.ref, rest.m == neg_inf() ? 0.0f : __fmul_rn(__fdiv_rn(mass, b.s), undo(k))};
             }
-            __syncthreads();        // before the next row takes s_grad and s_coef
+            bar_arrive(kRowStep);
         }
-        parity ^= 1;
+        if (crank != 0) continue;
+        float loss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kListRegs; ++i)
+            if (!(t.q[i] == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q[i], __fadd_rn(t.logq[i], -logp[i])));
+        loss = warp_sum(loss);
+        if (!(t.q_rest == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q_rest, __fadd_rn(logf(t.q_rest), -logp_rest)));
+        if (lane == 0) {
+            if (P.loss) P.loss[row] = loss;
+            if (P.stats) {
+                P.stats[4 * row] = f.m;
+                P.stats[4 * row + 1] = f.logs;
+                P.stats[4 * row + 2] = rest.m;
+                P.stats[4 * row + 3] = rest.logs;
+            }
+        }
     }
-    if (C > 1) cluster_barrier();       // no CTA leaves while a peer may still write to it
 }
 
 template <int DT>
@@ -374,9 +531,11 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
         const uint64_t row = unit / (uint32_t)P.parts;
         const uint32_t part = (uint32_t)(unit - row * (uint32_t)P.parts);
         const uint32_t sb_lo = part * P.part_sb, sb_hi = min(nsb, sb_lo + P.part_sb);
+        RawList raw;
+        load_raw(raw, P, row, lane);
         List L;
-        load_list<DT>(L, P, row, lane);
-        Coef c{0.0f, 0.0f};
+        place_list<DT>(L, raw, P, row, regs);
+        Coef coef{P.c, 0.0f, 0.0f};
         float m = 0.0f, logs = 0.0f, g = 0.0f;
         Teacher t;
         if (L.some) {
@@ -384,11 +543,12 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
             m = P.stats_in[4 * row];
             logs = P.stats_in[4 * row + 1];
             const float m_rest = P.stats_in[4 * row + 2], logs_rest = P.stats_in[4 * row + 3];
-            g = __fmul_rn(P.scale, P.g_row ? P.g_row[row] : 1.0f);
+            g = __fmul_rn(P.scale, P.g_row[row]);
             if (m_rest != neg_inf()) {
+                const SavedRef k = saved_reference<DT>(m_rest, P.scale, P.c);
                 const float p_rest = expf(__fadd_rn(__fadd_rn(m_rest, -m), __fadd_rn(logs_rest, -logs)));
-                c.m_rest = m_rest;
-                c.c_rest = __fmul_rn(__fmul_rn(g, __fmaf_rn(p_rest, t.Q, -t.q_rest)), expf(-logs_rest));
+                coef = {k.f.c, k.f.ref, __fmul_rn(__fmul_rn(g, __fmaf_rn(p_rest, t.Q, -t.q_rest)),
+                                                  __fmul_rn(expf(__fadd_rn(k.rho, -logs_rest)), undo(k.f)))};
             }
         }
         Walk<DT> walk;
@@ -420,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
             }
             any = __any_sync(~0u, any);
             if (any) __syncwarp();
-            rest_gradient<DT>(w, c, P.scale);
+            rest_gradient<DT>(w, coef);
             store_superblock<DT>(w, walk.sr, out, p0, lane);
             if (any) {
                 __syncwarp();
@@ -436,22 +596,11 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
     }
 }
 
-template <int DT, bool STEP>
-cudaError_t launch(const ScoreParams& P, dim3 grid, size_t smem, cudaStream_t s) {
-    auto* kernel = distill_kernel<DT, STEP>;
-    cudaError_t e = cudaSuccess;
-    // 48 KB without the opt-in, static shared memory included (up to 20 KB)
-    if (smem > 28 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && P.csize > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, grid, smem, s, P.csize > 1 ? P.csize : 0, P);
-}
-
 }  // namespace
 
-cudaError_t launch_distill(const ScoreParams& P, int dtype, bool step, dim3 grid, size_t smem, cudaStream_t s) {
-    if (dtype == MR_BF16) return step ? launch<MR_BF16, true>(P, grid, smem, s) : launch<MR_BF16, false>(P, grid, smem, s);
-    return step ? launch<MR_FP32, true>(P, grid, smem, s) : launch<MR_FP32, false>(P, grid, smem, s);
+ScoreKernel distill_forward(int dtype, bool step) {
+    if (dtype == MR_BF16) return step ? distill_kernel<MR_BF16, true> : distill_kernel<MR_BF16, false>;
+    return step ? distill_kernel<MR_FP32, true> : distill_kernel<MR_FP32, false>;
 }
 
 cudaError_t launch_distill_grad(const ScoreParams& P, int dtype, dim3 grid, cudaStream_t s) {

@@ -4,17 +4,21 @@
 // Forward: a cluster of C CTAs takes a row at a time, CTA c the c-th run of
 // its superblocks, warp w of it every 8th one.  Every score is read once; the
 // threads' running statistics join through shuffles, then through shared
-// memory of the cluster's first CTA, which writes the row's results.
+// memory of the cluster's first CTA, whose row warp writes the results.
 //
 // The top k come out of the same pass.  The stream keeps one key per run of
-// 512 bytes, the run's largest score (order-preserving bits).  Order the runs
-// by (largest score, first run first): an element of a run outside the first
-// k of them comes after k others, the largest of each of those k runs (equal
-// scores: the lower column first, and runs are in column order).  So the k
-// best elements lie in the k best runs, whatever the data: these are read
-// again, and of the run at place j only its first k - j elements at or above
-// the k-th run's largest can count.  The few that remain are ranked by
-// counting.
+// 512 bytes, the run's largest score (order-preserving bits).  The k-th
+// largest of any of the keys is a bound L that at least k scores reach, so the
+// best k are among the scores at or above L: all those above it, and of those
+// equal to it the first k (equal scores: the lower column first).  L is taken
+// from the largest keys of up to 128 groups of runs, found in registers and
+// ranked by counting; runs that reach L (a little over k of them on scores
+// without a pattern) are read again, 1/600 of the row a run, and the scores
+// that count are ranked by counting.  Scores that crowd in a few runs can
+// overflow the lists; then the runs are taken one by one: order them by
+// (largest score, first run first), and an element of the run at place j has j
+// others before it, so only its first k - j elements can count and
+// k (k + 1) / 2 places hold them all.
 //
 // Gradient: with t = y - m, p = e^t / e^logs and a, b of the row alone,
 //     dx = scale * (-g_lp p - g_H p (log p + H)) = e^t (a + b t),
@@ -36,254 +40,562 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return k == 0xffffffffu ? quiet_nan() : __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 __device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) { return __reduce_max_sync(~0u, v); }
-__device__ __forceinline__ uint32_t warp_min_u32(uint32_t v) { return __reduce_min_sync(~0u, v); }
 
-// (key, column) a before b
-__device__ __forceinline__ bool before(uint2 a, uint2 b) { return a.x > b.x || (a.x == b.x && a.y < b.y); }
+// A bound that at least k of n keys reach, and not many more (0 where fewer
+// than k are not 0): bisected, by votes, among the largest keys of up to 128
+// groups of them.  One warp.
+template <class Key>
+__device__ __forceinline__ uint32_t kth_bound(Key key, uint32_t n, int k, int lane) {
+    uint32_t top[4] = {0, 0, 0, 0};
+    for (uint32_t i = lane; i < n; i += 128) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (i + 32 * q < n) top[q] = max(top[q], key(i + 32 * q));
+    }
+    auto reach = [&](uint32_t bound) {
+        int c = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c += __popc(__ballot_sync(~0u, top[q] >= bound));
+        return c;
+    };
+    if (reach(1) < k) return 0;
+    // reach(lo) >= k > reach(hi + 1)
+    uint32_t lo = 1, hi = warp_max_u32(max(max(top[0], top[1]), max(top[2], top[3])));
+    if (hi > 0x80000000u && reach(0x80000000u) >= k) lo = 0x80000000u;      // k scores above -0
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        const int c = reach(mid);
+        if (c >= k) {
+            lo = mid;
+            if (c <= k + k / 8) break;
+        } else {
+            hi = mid - 1;
+        }
+    }
+    return lo;
+}
+
+// The best k of a CTA's runs, in order, into sel (one warp); returns how many
+// there are, and in `floor_key` the last one's key (1 where there are fewer
+// than k: then every score counts).  The runs are in groups of 32 q; lane g
+// keeps the largest key of group g, so a round looks at one group.
+__device__ __forceinline__ int select_runs(uint32_t* keys, uint32_t runs, int k, uint32_t* sel, uint32_t& floor_key, int lane) {
+    const uint32_t q = (runs + 1023) / 1024, size = 32 * q;
+    uint32_t mine = 0;
+    for (uint32_t g = 0; g * size < runs; ++g) {
+        uint32_t v = 0;
+        for (uint32_t t = 0; t < q; ++t) {
+            const uint32_t i = g * size + t * 32 + lane;
+            if (i < runs) v = max(v, keys[i]);
+        }
+        v = warp_max_u32(v);
+        if (lane == (int)g) mine = v;
+    }
+    floor_key = 1;
+    int n = 0;
+    while (n < k) {
+        const uint32_t top = warp_max_u32(mine);
+        if (top == 0) break;
+        const uint32_t g = __ffs(__ballot_sync(~0u, mine == top)) - 1;
+        uint32_t rest = 0;
+        bool found = false;
+        for (uint32_t t = 0; t < q; ++t) {
+            const uint32_t i = g * size + t * 32 + lane;
+            uint32_t key = i < runs ? keys[i] : 0;
+            if (!found) {
+                const uint32_t who = __ballot_sync(~0u, key == top);
+                if (who) {
+                    found = true;
+                    if (lane == __ffs(who) - 1) {
+                        sel[n] = i;
+                        keys[i] = key = 0;      // this lane alone reads it again
+                    }
+                }
+            }
+            rest = max(rest, key);
+        }
+        rest = warp_max_u32(rest);
+        if (lane == (int)g) mine = rest;
+        if (++n == k) floor_key = top;
+    }
+    __syncwarp();
+    return n;
+}
+
+// Where a run lies: the address of its first place, that place's column (it
+// wraps below the row's start) and the places [lo, hi) that are in the row.
+template <int DT>
+__device__ __forceinline__ uint4 locate_run(const ScoreParams& P, uint64_t row, uint32_t run) {
+    using S = Score<DT>;
+    Walk<DT> at;
+    at.seek(P, row, run / kSbRuns);
+    const uint32_t place = at.place(run / kSbRuns) + (run % kSbRuns) * 32 * S::VE;
+    const uint64_t a = reinterpret_cast<uint64_t>(at.sr.base) + (uint64_t)place * S::kBytes;
+    const uint32_t lo = place < at.sr.lo ? at.sr.lo - place : 0;
+    const uint32_t hi = place < at.sr.hi ? min(at.sr.hi - place, 32u * S::VE) : 0;
+    return make_uint4((uint32_t)a, (uint32_t)(a >> 32), P.col0[at.r] + place - at.sr.lo, lo | hi << 16);
+}
+// A lane's vector of a run; returns which of its places are in the row (-inf elsewhere).
+template <int DT, int N>
+__device__ __forceinline__ uint32_t load_run(uint32_t (&w)[N], int j, uint4 run, int lane) {
+    using S = Score<DT>;
+    const uint32_t lo = run.w & 0xffffu, hi = run.w >> 16, first = lane * S::VE;
+    const char* a = reinterpret_cast<const char*>((uint64_t)run.y << 32 | run.x) + lane * 16;
+    if (first >= lo && first + S::VE <= hi) {
+        load16(&w[4 * j], a);
+        return (1u << S::VE) - 1;
+    }
+    uint32_t in_row = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[4 * j + i] = S::kFill;
+#pragma unroll
+    for (int e = 0; e < S::VE; ++e)
+        if (first + e >= lo && first + e < hi) {
+            S::put(w, j, e, S::load_bits(a + e * S::kBytes));
+            in_row |= 1u << e;
+        }
+    return in_row;
+}
+
+// Vectors that reach the bound, waiting for a full warp of them (a ring of 64
+// for each warp).
+struct Waiting {
+    uint4 v;
+    uint32_t col, in_row;
+};
+constexpr int kWaiting = 64;
+
+// Takes batches of the n runs of `at` (in column order; `next` counts what the
+// CTA's warps have taken): appends every score above `bound` and, of those
+// equal to it, the first k that this warp meets.  Counts past the list's end
+// are not stored.  A run has a score or two that reach the bound: its lanes
+// only leave the vectors that do in the ring, and 32 of those are taken apart
+// at a time, a lane each.
+template <int DT>
+__device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t bound, int* next, Waiting* ring, uint2* cand,
+                                        int* n_cand, int lane) {
+    using S = Score<DT>;
+    constexpr int kBatch = 4;       // runs in flight
+    const int cap = score_top_candidates(k);
+    int ties = 0, head = 0, tail = 0;
+    auto take_apart = [&](int count) {
+        __syncwarp();
+        const bool mine = lane < count;
+        Waiting t = ring[(head + lane) % kWaiting];
+        if (!mine) t.in_row = 0;
+        const uint32_t v[4] = {t.v.x, t.v.y, t.v.z, t.v.w};
+        uint32_t more = 0, same = 0, key[S::VE];
+#pragma unroll
+        for (int e = 0; e < S::VE; ++e) {
+            key[e] = (t.in_row >> e) & 1 ? order_key(S::value(S::get(v, 0, e))) : 0;
+            more |= (uint32_t)(key[e] > bound) << e;
+            same |= (uint32_t)(key[e] == bound && key[e] != 0) << e;
+        }
+        if (__any_sync(~0u, same != 0)) {       // keep the first k - ties of them
+            int before = __popc(same);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(~0u, before, o);
+                if (lane >= o) before += up;
+            }
+            const int total = __shfl_sync(~0u, before, 31);
+            int keep = k - ties - (before - __popc(same));
+#pragma unroll
+            for (int e = 0; e < S::VE; ++e)
+                if (((same >> e) & 1) && keep-- > 0) more |= 1u << e;
+            ties += total;
+        }
+        if (more) {
+            int to = atomicAdd(n_cand, __popc(more));
+#pragma unroll
+            for (int e = 0; e < S::VE; ++e)
+                if ((more >> e) & 1) {
+                    if (to < cap) cand[to] = make_uint2(key[e], t.col + e);
+                    ++to;
+                }
+        }
+        head += count;
+        __syncwarp();
+    };
+    while (true) {
+        int j0 = 0;
+        if (lane == 0) j0 = atomicAdd(next, kBatch);
+        j0 = __shfl_sync(~0u, j0, 0);
+        if (j0 >= n) break;
+        uint32_t v[4 * kBatch], in_row[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            in_row[b] = 0;
+            if (j0 + b < n) in_row[b] = load_run<DT>(v, b, at[j0 + b], lane);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (j0 + b >= n) break;
+            const bool hit = in_row[b] != 0 && order_key(S::max_words(&v[4 * b], 4)) >= bound;
+            const uint32_t who = __ballot_sync(~0u, hit);
+            if (hit)
+                ring[(tail + __popc(who & ((1u << lane) - 1))) % kWaiting] =
+                    Waiting{make_uint4(v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]), at[j0 + b].z + lane * S::VE, in_row[b]};
+            tail += __popc(who);
+            if (tail - head >= 32) take_apart(32);
+        }
+    }
+    if (tail > head) take_apart(tail - head);
+}
+
+// Runs in the order of their largest scores: the best k - j elements of the
+// run at place j (one warp).
+template <int DT>
+__device__ __forceinline__ void collect_in_order(const uint4* at, int n, int k, uint32_t floor_key, uint2* cand, int* n_cand, int lane) {
+    using S = Score<DT>;
+    int count = 0;
+    for (int j = 0; j < n; ++j) {
+        uint32_t v[4], key[S::VE];
+        const uint32_t in_row = load_run<DT>(v, 0, at[j], lane), col = at[j].z + lane * S::VE;
+#pragma unroll
+        for (int e = 0; e < S::VE; ++e) {
+            key[e] = (in_row >> e) & 1 ? order_key(S::value(S::get(v, 0, e))) : 0;
+            if (key[e] < floor_key) key[e] = 0;
+        }
+        for (int left = k - j; left > 0; --left) {
+            uint32_t best = key[0];
+            int e_best = 0;
+#pragma unroll
+            for (int e = 1; e < S::VE; ++e)
+                if (key[e] > best) {
+                    best = key[e];
+                    e_best = e;
+                }
+            const uint32_t top = warp_max_u32(best);
+            if (top == 0) break;
+            if (lane == __ffs(__ballot_sync(~0u, best == top)) - 1) {
+                cand[count] = make_uint2(top, col + e_best);
+#pragma unroll
+                for (int e = 0; e < S::VE; ++e)
+                    if (e == e_best) key[e] = 0;
+            }
+            __syncwarp();
+            count++;
+        }
+    }
+    if (lane == 0) *n_cand = count;
+    __syncwarp();
+}
+
+// Calls put(rank, entry) for the best k of a list of (key, column) (one warp).
+template <class Put>
+__device__ __forceinline__ void rank_list(const uint2* list, int n, int k, int lane, Put put) {
+    constexpr int kEach = 4;
+    for (int i = lane; i < n; i += 32 * kEach) {
+        uint2 mine[kEach];
+        uint64_t whole[kEach];      // key, then the lower column first
+        int rank[kEach];
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            mine[q] = i + 32 * q < n ? list[i + 32 * q] : make_uint2(0, 0);
+            whole[q] = (uint64_t)mine[q].x << 32 | ~mine[q].y;
+            rank[q] = 0;
+        }
+#pragma unroll 4
+        for (int o = 0; o < n; ++o) {
+            const uint2 c = list[o];
+            const uint64_t other = (uint64_t)c.x << 32 | ~c.y;
+#pragma unroll
+            for (int q = 0; q < kEach; ++q) rank[q] += other > whole[q];
+        }
+#pragma unroll
+        for (int q = 0; q < kEach; ++q)
+            if (i + 32 * q < n && rank[q] < k) put(rank[q], mine[q]);
+    }
+}
+
+// The top k of a row from its runs' keys, by the row warp of the cluster's
+// first CTA while the stream is in the next row: it picks the runs, publishes
+// them and begins to read them again; the stream's warps, when they are
+// through with their row, take what is left.
+constexpr int kMaxPicked = 192;
+struct TopShared {
+    uint4 at[kMaxPicked];           // the picked runs
+    Waiting ring[kScoreWarps + 1][kWaiting];
+    uint32_t picked[kMaxPicked];
+    uint32_t bound;
+    int n_picked, n_cand, next;
+    uint32_t published;             // the row's number here + 1
+};
+template <int DT>
+__device__ __forceinline__ void help(const ScoreParams& P, TopShared& T, uint2* cand, int warp, int lane) {
+    collect<DT>(T.at, T.n_picked, P.top_k, T.bound, &T.next, T.ring[warp], cand, &T.n_cand, lane);
+}
+
+// Calls of their own: inlined, their registers crowd the stream's.
+template <int DT>
+__device__ __forceinline__ void locate(const ScoreParams& P, uint64_t row, TopShared& T, int n, int lane) {
+    for (int i = lane; i < n; i += 32) T.at[i] = locate_run<DT>(P, row, T.picked[i]);
+    __syncwarp();
+}
+// Picks a row's runs and publishes them as number `count`; false where they overflow.
+template <int DT>
+__device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, uint32_t count, const uint32_t* keys, uint32_t runs, uint2* cand,
+                                       TopShared& T, int lane) {
+    using S = Score<DT>;
+    const int k = P.top_k;
+    uint32_t bound = kth_bound([&](uint32_t i) { return keys[i]; }, runs, k, lane);
+    // the runs that reach it: all those above, the first k of those at it
+    int m = 0, ties = 0;
+    const uint32_t below = (1u << lane) - 1;
+    for (uint32_t i0 = lane; i0 - lane < runs; i0 += 128) {
+        uint32_t key[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) key[q] = i0 + 32 * q < runs ? keys[i0 + 32 * q] : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t same = __ballot_sync(~0u, key[q] == bound && key[q] != 0);
+            const bool take = key[q] > bound || (((same >> lane) & 1) && ties + __popc(same & below) < k);
+            const uint32_t who = __ballot_sync(~0u, take);
+            const int to = m + __popc(who & below);
+            if (take && to < kMaxPicked) T.picked[to] = i0 + 32 * q;
+            m += __popc(who);
+            ties += __popc(same);
+        }
+    }
+    __syncwarp();
+    const bool fits = m <= kMaxPicked;
+    if (fits) locate<DT>(P, row, T, m, lane);
+    if (bound == 0 && fits && m > k) {      // places without a score left too few groups: without them
+        bound = kth_bound([&](uint32_t i) { return keys[T.picked[i]]; }, (uint32_t)m, k, lane);
+    } else if (bound == 0 && fits) {
+        // fewer runs than k: a bound from the lanes' largest scores in them
+        uint32_t* lanes = reinterpret_cast<uint32_t*>(cand);
+        for (int j0 = 0; j0 < m; j0 += 4) {
+            uint32_t v[16], in_row[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (j0 + b < m) in_row[b] = load_run<DT>(v, b, T.at[j0 + b], lane);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (j0 + b < m) lanes[(j0 + b) * 32 + lane] = in_row[b] ? order_key(S::max_words(&v[4 * b], 4)) : 0;
+        }
+        __syncwarp();
+        bound = kth_bound([&](uint32_t i) { return lanes[i]; }, (uint32_t)m * 32, k, lane);
+    }
+    __syncwarp();
+    if (lane == 0) {
+        T.n_cand = T.next = 0;
+        T.n_picked = fits ? m : 0;
+        T.bound = bound;
+        __threadfence_block();
+        *reinterpret_cast<volatile uint32_t*>(&T.published) = count + 1;
+    }
+    __syncwarp();
+    return fits;
+}
+// The candidates are complete: the runs one by one where they overflowed.
+template <int DT>
+__device__ __noinline__ void mend_candidates(const ScoreParams& P, uint64_t row, uint32_t* keys, uint32_t runs, uint2* cand, TopShared& T,
+                                             int lane) {
+    uint32_t floor_key;
+    const int r = select_runs(keys, runs, P.top_k, T.picked, floor_key, lane);
+    locate<DT>(P, row, T, r, lane);
+    collect_in_order<DT>(T.at, r, P.top_k, floor_key, cand, &T.n_cand, lane);
+}
+__device__ __noinline__ void put_top(const ScoreParams& P, uint64_t row, const uint2* cand, int n, const Stat& all, const Final& f, int lane) {
+    const int k = P.top_k;
+    const float scale = P.scale;
+    long long* const top_ids = P.top_ids ? P.top_ids + row * k : nullptr;
+    float* const top_logprob = P.top_logprob ? P.top_logprob + row * k : nullptr;
+    rank_list(cand, n, k, lane, [&](int rank, uint2 c) {
+        if (top_ids) top_ids[rank] = c.y;
+        if (top_logprob) top_logprob[rank] = log_prob(key_value(c.x), all, f, scale);
+    });
+    __syncwarp();
+}
 
 template <int DT, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const __grid_constant__ ScoreParams P) {
+__global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_constant__ ScoreParams P) {
     using S = Score<DT>;
-    constexpr int kRuns = kSbRuns;
-    extern __shared__ uint32_t top_smem[];
-    // every warp's statistics, by row parity; the cluster's first CTA joins them
-    __shared__ Stat part[2][kMaxScoreCluster * kScoreWarps];
-    __shared__ uint2 peer_top[2][TOP ? kMaxScoreCluster * MR_MAX_TOP : 1];
-    __shared__ int peer_count[2][kMaxScoreCluster];
-    __shared__ int n_cand, n_sel;
-    __shared__ float row_m, row_logs;
+    extern __shared__ __align__(16) uint32_t top_smem[];
+    __shared__ Stat part[2][kMaxScoreCluster * kScoreWarps];       // read by the cluster's first CTA
+    __shared__ int row_out[2];      // the row is left out
+    TopShared& top = *reinterpret_cast<TopShared*>(top_smem);       // TOP: then two rows' keys, then the candidates
+    static_assert(sizeof(TopShared) <= kTopSharedBytes, "score_top_smem counts them");
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int C = P.csize, crank = C > 1 ? (int)cluster_rank() : 0;
     const uint32_t nsb = P.sb0[P.W];
     const uint32_t sb_lo = (uint32_t)((uint64_t)nsb * crank / C), sb_hi = (uint32_t)((uint64_t)nsb * (crank + 1) / C);
+    const uint64_t stride = gridDim.x / C;
+    uint64_t row = blockIdx.x / C;
     const int k = P.top_k;
-    const uint32_t runs = (sb_hi - sb_lo) * kRuns;
-    uint32_t* keys = top_smem;
-    uint32_t* sel = keys + (((nsb + C - 1) / C) * kRuns);
-    uint2* cand = reinterpret_cast<uint2*>(sel + ((k + 2) & ~1));
+    const uint32_t runs = nsb * kSbRuns;
+    uint32_t* const keys = top_smem + kTopSharedBytes / 4;
+    uint2* const cand = reinterpret_cast<uint2*>(keys + 2 * runs);
+    if (C > 1) cluster_arrive();        // every CTA of the cluster has started: waited for before the first store to a peer
     pdl_enter();
 
-    int parity = 0;
-    for (uint64_t row = blockIdx.x / C; row < P.rows; row += gridDim.x / C) {
-        const long long id = P.ids ? P.ids[row] : 0;
-        if (id < 0) {       // left out: nothing of it is read
-            if (crank == 0) {
-                if (threadIdx.x == 0) {
-                    if (P.logprob) P.logprob[row] = 0.0f;
-                    if (ENT) P.entropy[row] = 0.0f;
-                    if (P.stats) {
-                        P.stats[2 * row] = neg_inf();
-                        P.stats[2 * row + 1] = 0.0f;
-                    }
-                }
-                if (TOP)
-                    for (int i = threadIdx.x; i < k; i += kThreads) {
-                        if (P.top_ids) P.top_ids[row * k + i] = -1;
-                        if (P.top_logprob) P.top_logprob[row * k + i] = neg_inf();
-                    }
-            }
-            continue;
-        }
-        float x_id = quiet_nan();
-        if (crank == 0 && P.ids && id < (long long)P.vocab) x_id = S::load_one(score_at<DT>(P, row, (uint32_t)id));
-
-        // ---- the stream ----
-        Stat a{neg_inf(), 0.0f, 0.0f};
+    if (warp < kScoreWarps) {
+        // ================= the stream =================
+        uint32_t w[16];
         Walk<DT> walk;
-        uint32_t sb = sb_lo + warp;
-        uint32_t w[16], nx[16];
-        uint32_t p0 = 0;
         ShardRow sr{};
-        if (sb < sb_hi) {
-            walk.seek(P, row, sb);
+        uint32_t p0 = 0;
+        const uint32_t first = sb_lo + warp;
+        auto fetch = [&](uint32_t (&to)[16], uint64_t r, uint32_t sb) {
+            walk.seek(P, r, sb);
             sr = walk.sr;
             p0 = walk.place(sb);
-            load_superblock<DT>(w, sr, p0, lane);
-        }
-        while (sb < sb_hi) {
-            const uint32_t next = sb + kScoreWarps;
-            const ShardRow now = sr;
-            const uint32_t now_p0 = p0;
-            if (next < sb_hi) {
-                walk.seek(P, row, next);
-                sr = walk.sr;
-                p0 = walk.place(next);
-                load_superblock<DT>(nx, sr, p0, lane);
+            load_superblock<DT>(to, sr, p0, lane);
+        };
+        if (row < P.rows && first < sb_hi) fetch(w, row, first);
+        bool waited = C == 1, last_out = true;
+        int parity = 0;
+        uint32_t count = 0;     // this CTA's rows so far
+        const uint32_t keys_at = TOP ? (C > 1 ? peer_address(keys, 0) : (uint32_t)__cvta_generic_to_shared(keys)) : 0;
+        for (; row < P.rows; row += stride, parity ^= 1) {
+            bar_sync(kRowReady + parity);
+            const bool out = row_out[parity];
+            if (TOP && !waited) {       // the keys of the row before last have been used
+                cluster_wait();
+                waited = true;
             }
-            accumulate<DT, ENT>(a, w, P.scale);
-            if (TOP) {
-#pragma unroll
-                for (int j = 0; j < kRuns; ++j) {
-                    uint32_t key = warp_max_u32(order_key(S::max_words(&w[4 * j], 4)));
-                    // a run with no place of the row in it has no score
-                    const uint32_t rp = now_p0 + j * 32 * S::VE;
-                    if (rp + 32 * S::VE <= now.lo || rp >= now.hi) key = 0;
-                    if (lane == 0) keys[(sb - sb_lo) * kRuns + j] = key;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = nx[i];
-            sb = next;
-        }
-        a = warp_join<ENT>(a);
-
-        // ---- the top k of this CTA's part ----
-        if (TOP) {
-            if (threadIdx.x == 0) n_cand = 0;
-            __syncthreads();
-            if (warp == 0) {
-                uint32_t best = 0, at = 0;      // this lane's best run left
-                auto rescan = [&] {
-                    best = 0;
-                    for (uint32_t i = lane; i < runs; i += 32)
-                        if (keys[i] > best) {
-                            best = keys[i];
-                            at = i;
-                        }
-                };
-                rescan();
-                int n = 0;
-                for (; n < k; ++n) {
-                    const uint32_t top = warp_max_u32(best);
-                    if (top == 0) break;
-                    const uint32_t first = warp_min_u32(best == top ? at : ~0u);
-                    if (best == top && at == first) {
-                        sel[n] = first;
-                        keys[first] = 0;
-                        rescan();
-                    }
-                    if (lane == 0 && n == k - 1) sel[k] = top;     // the k-th run's largest
-                }
-                if (lane == 0) {
-                    n_sel = n;
-                    if (n < k) sel[k] = 1;      // fewer runs than k: every score counts
-                }
-            }
-            __syncthreads();
-            const int n = n_sel;
-            const uint32_t floor_key = sel[k];
-            for (int j = warp; j < n; j += kScoreWarps) {
-                const uint32_t run = sel[j], s = sb_lo + run / kRuns;
-                Walk<DT> at;
-                at.seek(P, row, s);
-                const uint32_t p = at.place(s) + ((run % kRuns) * 32 + lane) * S::VE;
-                const uint32_t col = P.col0[at.r] + p - at.sr.lo;
-                uint32_t v[4], key[S::VE];
-                load_vector<DT>(v, 0, at.sr, p);
-#pragma unroll
-                for (int e = 0; e < S::VE; ++e) {
-                    key[e] = order_key(S::value(S::get(v, 0, e)));
-                    if (p + e < at.sr.lo || p + e >= at.sr.hi || key[e] < floor_key) key[e] = 0;
-                }
-                for (int left = k - j; left > 0; --left) {
-                    uint32_t best = key[0];
-                    int e_best = 0;
-#pragma unroll
-                    for (int e = 1; e < S::VE; ++e)
-                        if (key[e] > best) {
-                            best = key[e];
-                            e_best = e;
-                        }
-                    const uint32_t top = warp_max_u32(best);
-                    if (top == 0) break;
-                    const uint32_t who = __ballot_sync(~0u, best == top);
-                    if (lane == __ffs(who) - 1) {
-                        cand[atomicAdd(&n_cand, 1)] = make_uint2(top, col + e_best);
-#pragma unroll
-                        for (int e = 0; e < S::VE; ++e)
-                            if (e == e_best) key[e] = 0;
-                    }
-                }
-            }
-        }
-
-        // ---- join ----
-        if (lane == 0) {
-            if (C == 1) {
-                part[parity][warp] = a;
+            Running run = start_running(P.c);
+            const uint64_t next_row = row + stride;
+            if (out) {
+                walk = Walk<DT>{};
+                if (next_row < P.rows && first < sb_hi) fetch(w, next_row, first);
             } else {
-                const uint32_t to = peer_address(&part[parity][crank * kScoreWarps + warp], 0);
-                peer_store(to, __float_as_uint(a.m));
-                peer_store(to + 4, __float_as_uint(a.s));
-                peer_store(to + 8, __float_as_uint(a.u));
-            }
-        }
-        if (TOP && C > 1) {
-            __syncthreads();
-            const int n = n_cand;
-            for (int i = threadIdx.x; i < n; i += kThreads) {
-                const uint2 mine = cand[i];
-                int rank = 0;
-                for (int o = 0; o < n; ++o) rank += before(cand[o], mine);
-                if (rank < k) {
-                    const uint32_t to = peer_address(&peer_top[parity][crank * MR_MAX_TOP + rank], 0);
-                    peer_store(to, mine.x);
-                    peer_store(to + 4, mine.y);
-                }
-            }
-            if (threadIdx.x == 0) peer_store(peer_address(&peer_count[parity][crank], 0), (uint32_t)min(n, k));
-        }
-        if (C == 1) __syncthreads();
-        else cluster_barrier();
-        if (crank == 0) {
-            if (warp == 0) {
-                Stat b{neg_inf(), 0.0f, 0.0f};
-                for (int i = lane; i < C * kScoreWarps; i += 32) {
-                    Stat o = part[parity][i];
-                    const float M = max_nan(b.m, o.m);
-                    rebase<ENT>(b, M);
-                    rebase<ENT>(o, M);
-                    b.s = __fadd_rn(b.s, o.s);
-                    if (ENT) b.u = __fadd_rn(b.u, o.u);
-                }
-                b = warp_join<ENT>(b);
-                if (lane == 0) {
-                    float m, logs;
-                    finish(b, m, logs);
-                    if (P.stats) {
-                        P.stats[2 * row] = m;
-                        P.stats[2 * row + 1] = logs;
+                for (uint32_t sb = first; sb < sb_hi; sb += kScoreWarps) {
+                    uint32_t nx[16];
+                    const ShardRow now = sr;
+                    const uint32_t now_p0 = p0;
+                    if (sb + kScoreWarps < sb_hi) {
+                        fetch(nx, row, sb + kScoreWarps);
+                    } else if (next_row < P.rows) {     // the next row's first, left out or not
+                        walk = Walk<DT>{};
+                        fetch(nx, next_row, first);
                     }
-                    if (P.logprob)
-                        P.logprob[row] = x_id == neg_inf() && m == m ? neg_inf()
-                                                                     : __fadd_rn(__fmaf_rn(x_id, P.scale, -m), -logs);
-                    if (ENT) P.entropy[row] = m == neg_inf() ? 0.0f : __fadd_rn(logs, -__fdiv_rn(b.u, b.s));
+                    accumulate<DT, ENT>(run, w, P.c);
                     if (TOP) {
-                        row_m = m;
-                        row_logs = logs;
+                        uint32_t mine = 0;
+#pragma unroll
+                        for (int j = 0; j < kSbRuns; ++j) {
+                            uint32_t key = warp_max_u32(order_key(S::max_words(&w[4 * j], 4)));
+                            // a run with no place of the row in it has no score
+                            const uint32_t rp = now_p0 + j * 32 * S::VE;
+                            if (rp + 32 * S::VE <= now.lo || rp >= now.hi) key = 0;
+                            if (lane == j) mine = key;
+                        }
+                        if (lane < kSbRuns) peer_store(keys_at + (parity * runs + sb * kSbRuns + lane) * 4, mine);
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = nx[i];
                 }
             }
-            if (TOP) {
-                __syncthreads();
-                const uint2* list = C == 1 ? cand : peer_top[parity];
-                const int slots = C == 1 ? n_cand : C * MR_MAX_TOP;
-                const float m = row_m, logs = row_logs;
-                for (int i = threadIdx.x; i < slots; i += kThreads) {
-                    if (C > 1 && i % MR_MAX_TOP >= peer_count[parity][i / MR_MAX_TOP]) continue;
-                    const uint2 mine = list[i];
-                    int rank = 0;
-                    if (C == 1) {
-                        for (int o = 0; o < slots; ++o) rank += before(list[o], mine);
-                    } else {
-                        for (int c = 0; c < C; ++c)
-                            for (int o = 0; o < peer_count[parity][c]; ++o) rank += before(list[c * MR_MAX_TOP + o], mine);
-                    }
-                    if (rank < k) {
-                        const float x = key_value(mine.x);
-                        if (P.top_ids) P.top_ids[row * k + rank] = mine.y;
-                        if (P.top_logprob)
-                            P.top_logprob[row * k + rank] = x == neg_inf() && m == m ? neg_inf()
-                                                          : __fadd_rn(__fmaf_rn(x, P.scale, -m), -logs);
-                    }
+            Stat a = run.a;
+            if (!out) a = warp_join<ENT>(a, P.c);
+            if (!waited) cluster_wait();
+            if (lane == 0 && !out) {
+                if (C == 1) {
+                    part[parity][warp] = a;
+                } else {
+                    const uint32_t to = peer_address(&part[parity][crank * kScoreWarps + warp], 0);
+                    peer_store(to, __float_as_uint(a.x));
+                    peer_store(to + 4, __float_as_uint(a.s));
+                    peer_store(to + 8, __float_as_uint(a.u));
                 }
-                __syncthreads();        // before the next row takes the lists
+            }
+            __syncwarp();
+            if (C > 1) {
+                cluster_arrive();
+                waited = false;         // for this row's phase: before the next row's stores, or the end
+            } else {
+                bar_arrive(kRowDone + parity);
+            }
+            if (TOP && crank == 0) {
+                if (!last_out) {        // the row before: what its runs' readers have left
+                    if (*reinterpret_cast<volatile uint32_t*>(&top.published) == count) {
+                        __threadfence_block();
+                        help<DT>(P, top, cand, warp, lane);
+                    }
+                    bar_arrive(kRowHelped);
+                }
+                last_out = out;
+                ++count;
             }
         }
-        parity ^= 1;
+        if (TOP && !last_out) {
+            bar_sync(kRowHelp);
+            help<DT>(P, top, cand, warp, lane);
+            bar_arrive(kRowHelped);
+        }
+        if (!waited) cluster_wait();
+        return;
     }
-    if (C > 1) cluster_barrier();       // no CTA leaves while a peer may still write to it
+
+    // ================= the row warp =================
+    auto id_of = [&](uint64_t r) -> long long { return P.ids && r < P.rows ? P.ids[r] : 0; };
+    auto row_ready = [&](uint64_t r, long long id, int par) {
+        if (r < P.rows) {
+            if (lane == 0) row_out[par] = id < 0;
+            bar_arrive(kRowReady + par);
+        }
+    };
+    long long id = id_of(row), id_next = id_of(row + stride);
+    if (TOP && lane == 0) top.published = 0;
+    row_ready(row, id, 0);
+    row_ready(row + stride, id_next, 1);
+    if (C > 1) cluster_wait();
+    int parity = 0;
+    for (uint32_t count = 0; row < P.rows; row += stride, parity ^= 1, ++count) {
+        const bool out = id < 0;
+        const long long id_after = id_of(row + 2 * stride);
+        float x_id = quiet_nan();
+        if (crank == 0 && P.ids && !out && id < (long long)P.vocab) x_id = S::load_one(score_at<DT>(P, row, (uint32_t)id));
+        if (C == 1) {
+            bar_sync(kRowDone + parity);
+        } else {
+            cluster_arrive();
+            cluster_wait();
+        }
+        id = id_next;
+        id_next = id_after;
+        if (crank != 0) {
+            row_ready(row + 2 * stride, id_after, parity);
+            continue;
+        }
+        Stat all{neg_inf(), 0.0f, 0.0f};
+        Final f{neg_inf(), 0.0f, 0.0f};
+        if (!out) all = join_parts<ENT>(part[parity], C * kScoreWarps, lane, P.c);
+        bool fits = true;
+        if (TOP && !out) {
+            fits = pick_runs<DT>(P, row, count, keys + parity * runs, runs, cand, top, lane);
+            if (row + stride >= P.rows) bar_arrive(kRowHelp);      // the last row: the stream has nothing else to do
+        }
+        if (!out) f = finish(all, P.scale);
+        if (lane == 0) {
+            if (P.stats) {
+                P.stats[2 * row] = f.m;
+                P.stats[2 * row + 1] = f.logs;
+            }
+            if (P.logprob) P.logprob[row] = out ? 0.0f : log_prob(x_id, all, f, P.scale);
+            if (ENT) P.entropy[row] = f.m == neg_inf() ? 0.0f : __fmaf_rn(-kLn2, __fdiv_rn(all.u, all.s), f.log_s);
+        }
+        if (TOP && !out) {
+            if (fits) help<DT>(P, top, cand, kScoreWarps, lane);
+            bar_sync(kRowHelped);
+            if (!fits || top.n_cand > score_top_candidates(k)) mend_candidates<DT>(P, row, keys + parity * runs, runs, cand, top, lane);
+        }
+        row_ready(row + 2 * stride, id_after, parity);
+        if (TOP) {
+            if (out) {
+                for (int i = lane; i < k; i += 32) {
+                    if (P.top_ids) P.top_ids[row * k + i] = -1;
+                    if (P.top_logprob) P.top_logprob[row * k + i] = neg_inf();
+                }
+            } else {
+                put_top(P, row, cand, top.n_cand, all, f, lane);
+            }
+        }
+    }
 }
 
 template <int DT, bool ENT>
@@ -299,20 +611,23 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_grad_kernel(const __grid_
         const uint32_t part = (uint32_t)(unit - row * (uint32_t)P.parts);
         const uint32_t sb_lo = part * P.part_sb, sb_hi = min(nsb, sb_lo + P.part_sb);
         const long long id = P.ids ? P.ids[row] : 0;
-        float A = 0.0f, B = 0.0f, m = 0.0f, g_lp = 0.0f;
+        // gradient: 2^(c x - ref) (A + B (c x - ref))
+        float A = 0.0f, B = 0.0f, g_lp = 0.0f;
+        Ref ref{P.c, 0.0f, 0.0f};
         uint32_t id_sb = ~0u, id_place = 0;
         int id_r = 0;
         if (id >= 0) {
-            m = P.stats_in[2 * row];
-            const float logs = P.stats_in[2 * row + 1];
+            const float m = P.stats_in[2 * row], logs = P.stats_in[2 * row + 1];
             g_lp = P.g_row ? P.g_row[row] : 0.0f;
             const float g_h = ENT ? P.g_entropy[row] : 0.0f, h = ENT ? P.entropy_in[row] : 0.0f;
-            if (m == neg_inf()) {
-                m = 0.0f;       // nothing but -inf: every gradient is 0
-            } else {
-                const float f = __fmul_rn(P.scale, expf(-logs));
-                A = -__fmul_rn(f, __fmaf_rn(g_h, __fadd_rn(h, -logs), g_lp));
-                B = -__fmul_rn(f, g_h);
+            if (m != neg_inf()) {       // else nothing but -inf: every gradient is 0
+                const SavedRef k = saved_reference<DT>(m, P.scale, P.c);
+                ref = k.f;
+                // p = 2^(c x - ref) f; log p = ln 2 (c x - ref) + off
+                const float f = __fmul_rn(P.scale, __fmul_rn(expf(__fadd_rn(k.rho, -logs)), undo(ref)));
+                const float off = __fmaf_rn(-kLn2, ref.r, __fadd_rn(k.rho, -logs));
+                A = -__fmul_rn(f, __fmaf_rn(g_h, __fadd_rn(h, off), g_lp));
+                B = -__fmul_rn(f, __fmul_rn(g_h, kLn2));
             }
             if (P.ids) {
                 if (id >= (long long)P.vocab) {
@@ -327,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_grad_kernel(const __grid_
         }
         Walk<DT> walk;
         ShardRow out{};
-        const F2 sc = f2(P.scale, P.scale), off = f2(-m, -m), l2 = f2(kLog2e, kLog2e), a2 = f2(A, A), b2 = f2(B, B);
+        const F2 cc = f2(ref.c, ref.c), off = f2(-ref.ref, -ref.ref), a2 = f2(A, A), b2 = f2(B, B);
         for (uint32_t sb = sb_lo; sb < sb_hi; ++sb) {
             if (walk.seek(P, row, sb)) out = shard_row<DT>(P.g[walk.r], P.ldg[walk.r], row, P.col0[walk.r + 1] - P.col0[walk.r]);
             const uint32_t p0 = walk.place(sb);
@@ -342,25 +657,19 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_grad_kernel(const __grid_
             const bool has_id = sb == id_sb;
             if (has_id) {       // before an in-place store takes the score
                 const float x = S::load_one(walk.sr.base + (uint64_t)id_place * S::kBytes);
-                const float t = fmaxf(__fmaf_rn(x, P.scale, -m), kFarBelow);
-                g_id = x == neg_inf() ? 0.0f
-                                      : __fmaf_rn(ex2(__fmul_rn(t, kLog2e)), __fmaf_rn(B, t, A), __fmul_rn(P.scale, g_lp));
+                const float t = fmaxf(__fmaf_rn(x, ref.c, -ref.ref), kFarBelow);
+                g_id = x == neg_inf() ? 0.0f : __fmaf_rn(ex2(t), __fmaf_rn(B, t, A), __fmul_rn(P.scale, g_lp));
                 __syncwarp();
             }
             if (id >= 0) {
 #pragma unroll
                 for (int i = 0; i < S::kPairs; ++i) {
-                    float x0, x1, e0, e1;
+                    float x0, x1, t0, t1;
                     S::pair(w, i, x0, x1);
-                    F2 t = fma2(f2(x0, x1), sc, off);
-                    unpack(mul2(t, l2), e0, e1);
+                    unpack(fma2(f2(x0, x1), cc, off), t0, t1);
                     F2 f = a2;
-                    if (ENT) {
-                        float t0, t1;
-                        unpack(t, t0, t1);
-                        f = fma2(b2, f2(fmaxf(t0, kFarBelow), fmaxf(t1, kFarBelow)), a2);
-                    }
-                    unpack(mul2(f2(ex2(e0), ex2(e1)), f), x0, x1);
+                    if (ENT) f = fma2(b2, f2(fmaxf(t0, kFarBelow), fmaxf(t1, kFarBelow)), a2);
+                    unpack(mul2(f2(ex2(t0), ex2(t1)), f), x0, x1);
                     S::set_pair(w, i, x0, x1);
                 }
             }
@@ -373,28 +682,17 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_grad_kernel(const __grid_
     }
 }
 
-template <int DT, bool ENT, bool TOP>
-cudaError_t launch(const ScoreParams& P, dim3 grid, size_t smem, cudaStream_t s) {
-    auto* kernel = logprob_kernel<DT, ENT, TOP>;
-    cudaError_t e = cudaSuccess;
-    // 48 KB without the opt-in, static shared memory included (up to 20 KB)
-    if (smem > 28 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && P.csize > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, grid, smem, s, P.csize > 1 ? P.csize : 0, P);
+ScoreKernel variant(int dtype, bool ent, bool top) {
+    if (dtype == MR_BF16)
+        return top ? (ent ? logprob_kernel<MR_BF16, true, true> : logprob_kernel<MR_BF16, false, true>)
+                   : (ent ? logprob_kernel<MR_BF16, true, false> : logprob_kernel<MR_BF16, false, false>);
+    return top ? (ent ? logprob_kernel<MR_FP32, true, true> : logprob_kernel<MR_FP32, false, true>)
+               : (ent ? logprob_kernel<MR_FP32, true, false> : logprob_kernel<MR_FP32, false, false>);
 }
 
 }  // namespace
 
-cudaError_t launch_logprob(const ScoreParams& P, int dtype, dim3 grid, size_t smem, cudaStream_t s) {
-    const bool ent = P.entropy != nullptr, top = P.top_k > 0;
-    if (dtype == MR_BF16) {
-        if (top) return ent ? launch<MR_BF16, true, true>(P, grid, smem, s) : launch<MR_BF16, false, true>(P, grid, smem, s);
-        return ent ? launch<MR_BF16, true, false>(P, grid, smem, s) : launch<MR_BF16, false, false>(P, grid, smem, s);
-    }
-    if (top) return ent ? launch<MR_FP32, true, true>(P, grid, smem, s) : launch<MR_FP32, false, true>(P, grid, smem, s);
-    return ent ? launch<MR_FP32, true, false>(P, grid, smem, s) : launch<MR_FP32, false, false>(P, grid, smem, s);
-}
+ScoreKernel logprob_forward(const ScoreParams& P, int dtype) { return variant(dtype, P.entropy != nullptr, P.top_k > 0); }
 
 cudaError_t launch_logprob_grad(const ScoreParams& P, int dtype, dim3 grid, cudaStream_t s) {
     if (dtype == MR_BF16)

@@ -133,6 +133,7 @@ struct ScoreParams {
     uint32_t vocab;
     float shards_per_col;           // W / V
     float scale;
+    float c;                        // scale * log2(e)
     int csize;                      // CTAs per cluster: a row is cut into this many runs of superblocks
     int parts;                      // gradient kernels: warps per row,
     uint32_t part_sb;               // and superblocks each of them takes
@@ -164,10 +165,19 @@ constexpr int kMaxScoreCluster = 16;
 constexpr uint32_t kSuperblockBytes = 2048;
 constexpr int kSbRuns = 4;                          // 512-byte runs in a superblock
 constexpr size_t kStepRoundBytes = kSuperblockBytes * (kThreads / 32);  // a superblock for every warp of a CTA
-// Shared memory of the top-k path: a key for each 512-byte run of the CTA's
-// part, the selected runs, and the candidates (k - j from the j-th run).
+// Candidates that the top-k path holds: usually a little over k are needed; 9
+// warps may each keep k that equal the bound; the path for crowded scores
+// needs k (k + 1) / 2.
+__host__ __device__ constexpr int score_top_candidates(int k) {
+    return k * (k + 1) / 2 > 12 * k + 128 ? k * (k + 1) / 2 : 12 * k + 128;
+}
+// Shared memory of the top-k path: its fixed part, a key for each 512-byte run
+// of a row (two rows of them), and the candidates (or, before them, 32 k keys
+// of lanes).
+constexpr size_t kTopSharedBytes = 22 * 1024;
 constexpr size_t score_top_smem(uint32_t runs, int k) {
-    return (size_t)runs * 4 + (size_t)(k + 2) * 4 + (size_t)k * (k + 1) / 2 * 8;
+    return kTopSharedBytes + (size_t)runs * 8 +
+           (size_t)(score_top_candidates(k) * 8 > k * 128 ? score_top_candidates(k) * 8 : k * 128);
 }
 
 struct GatherParams {
@@ -280,11 +290,11 @@ __device__ __forceinline__ void pdl_enter() {
 // Launch `k` on `s` with programmatic stream serialisation (when enabled)
 // and, when cluster > 0, as 1-D thread-block clusters of that many CTAs.
 template <class... Exp, class... Act>
-inline cudaError_t launch_kernel(void (*k)(Exp...), dim3 grid, size_t smem, cudaStream_t s, unsigned cluster,
-                                 Act&&... args) {
+inline cudaError_t launch_kernel_of(int threads, void (*k)(Exp...), dim3 grid, size_t smem, cudaStream_t s,
+                                    unsigned cluster, Act&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -304,6 +314,12 @@ inline cudaError_t launch_kernel(void (*k)(Exp...), dim3 grid, size_t smem, cuda
     cfg.attrs = attr;
     cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, k, static_cast<Act&&>(args)...);
+}
+// The same with the block size every other kernel has.
+template <class... Exp, class... Act>
+inline cudaError_t launch_kernel(void (*k)(Exp...), dim3 grid, size_t smem, cudaStream_t s, unsigned cluster,
+                                 Act&&... args) {
+    return launch_kernel_of(kThreads, k, grid, smem, s, cluster, static_cast<Act&&>(args)...);
 }
 
 #define MR_DECLARE_REDUCE(dt, algo) \
@@ -338,8 +354,19 @@ int device_sms();
 int debug_log_level();
 void count_launch();
 void clear_error();
-cudaError_t launch_logprob(const ScoreParams& P, int dtype, dim3 grid, size_t smem, cudaStream_t s);
-cudaError_t launch_distill(const ScoreParams& P, int dtype, bool step, dim3 grid, size_t smem, cudaStream_t s);
+// The forward kernels (kScoreThreads threads, clusters of P.csize).
+using ScoreKernel = void (*)(ScoreParams);
+constexpr int kScoreThreads = kThreads + 32;
+// Lets a forward kernel have clusters of C and that much dynamic shared memory
+// (48 KB without the opt-in, static arrays of up to 21 KB included).
+inline cudaError_t allow_score_kernel(ScoreKernel kernel, int C, size_t smem) {
+    cudaError_t e = cudaSuccess;
+    if (smem > 27 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
+}
+ScoreKernel logprob_forward(const ScoreParams& P, int dtype);
+ScoreKernel distill_forward(int dtype, bool step);
 cudaError_t launch_logprob_grad(const ScoreParams& P, int dtype, dim3 grid, cudaStream_t s);
 cudaError_t launch_distill_grad(const ScoreParams& P, int dtype, dim3 grid, cudaStream_t s);
 cudaError_t launch_allreduce_rmsnorm(const NormParams& P, int dtype, int algo, dim3 grid, size_t smem, cudaStream_t s);

@@ -6,6 +6,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "mr.h"
 #include "mr_internal.h"
@@ -15,6 +16,8 @@ namespace {
 
 using mr::report_error;
 using mr::ScoreParams;
+
+constexpr size_t kMostDynamicSmem = 200 * 1024;     // of a CTA's 227 KB, beside its static arrays
 
 constexpr size_t kMostRows = (size_t)1 << 40, kMostStride = (size_t)1 << 40;
 
@@ -106,6 +109,7 @@ mr_status_t check_scores(Call& c, const void* const* logits, const size_t* ld, v
     P.vocab = (uint32_t)vocab;
     P.shards_per_col = (float)W / (float)vocab;
     P.scale = scale;
+    P.c = (float)((double)scale * 1.4426950408889634);
     const uint32_t sb = mr::kSuperblockBytes / b;       // scores in a superblock
     uint32_t nsb = 0;
     for (int r = 0; r < W; ++r) {
@@ -154,42 +158,86 @@ mr_status_t per_row(Call& c, const T* p, size_t per, const char* name, bool writ
     return MR_OK;
 }
 
+// Clusters of C CTAs of a forward kernel that the current device holds at
+// once.  The answer (the driver's, some 10 us) is kept: it depends on the
+// kernel, C and the shared memory alone.  Asking beats dividing: clusters do
+// not cross the borders between groups of SMs, and 114 clusters of 4 where
+// 110 fit left the last four to a second wave (loss and gradient of 1140 rows
+// 1.5 times as long).
+int resident_clusters(mr::ScoreKernel kernel, int C, size_t smem) {
+    struct Known {
+        mr::ScoreKernel kernel;
+        size_t smem;
+        int C, dev, n;
+    };
+    static Known known[256];
+    static int count = 0;
+    static std::mutex mutex;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lock(mutex);
+    for (int i = 0; i < count; ++i)
+        if (known[i].kernel == kernel && known[i].smem == smem && known[i].C == C && known[i].dev == dev) return known[i].n;
+    int n = 0;
+    cudaError_t e = mr::allow_score_kernel(kernel, C, smem);
+    if (e == cudaSuccess && C == 1) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, mr::kScoreThreads, smem);
+        n *= mr::device_sms();
+    } else if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)C, 1, 1);
+        cfg.blockDim = dim3(mr::kScoreThreads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)C;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return 0;       // not kept: the launch will say what is wrong
+    }
+    if (count < 256) known[count++] = {kernel, smem, C, dev, n};
+    return n;
+}
+
+struct Plan {
+    int C, clusters;
+    size_t smem;
+};
 // CTAs per row (a cluster), from the modelled time of the whole call: rounds
 // of rows over the resident clusters, each a CTA's part of a row at its share
 // of the bandwidth and a fixed cost of the row's start and join.
-int plan_cluster(const Call& c, size_t (*smem)(const Call&, int), int most_resident, int* resident, double passes) {
-    const double sms = mr::device_sms();
-    int best = 1;
+Plan plan_forward(const Call& c, mr::ScoreKernel kernel, size_t (*smem)(const Call&, int), double passes, double fixed_us,
+                  double join_us) {
+    Plan best{0, 1, 0};
     double best_us = 1e300;
     for (int C = 1; C <= mr::kMaxScoreCluster; C *= 2) {
         if (C > 1 && (uint32_t)C * mr::kThreads / 32 > c.nsb + 7) break;        // a superblock for every warp
         const size_t bytes = smem(c, C);
-        if (bytes > 200 * 1024) continue;
-        const int r = std::min<int>(most_resident, (int)((227 * 1024) / (bytes + 24 * 1024)));
-        const double slots = sms * std::max(1, r), clusters = std::max(1.0, floor(slots / C));
+        if (bytes > kMostDynamicSmem) continue;
+        const int clusters = resident_clusters(kernel, C, bytes);
+        if (clusters < 1) continue;
         const double rounds = ceil((double)c.rows / clusters);
-        const double active = std::min(slots, (double)c.rows * C);
+        const double active = std::min<double>(clusters, c.rows) * C;
         const double gbs = std::min(45.0, 6600.0 / active);
-        const double us = rounds * ((double)c.nsb * mr::kSuperblockBytes * passes / C / (gbs * 1e3) + (C == 1 ? 1.0 : 2.0));
+        const double us = rounds * ((double)c.nsb * mr::kSuperblockBytes * passes / C / (gbs * 1e3) + fixed_us + (C == 1 ? 0.0 : join_us));
         if (us < best_us) {
             best_us = us;
-            best = C;
-            *resident = std::max(1, r);
+            best = {C, clusters, bytes};
         }
     }
     return best;
 }
 
 size_t plain_smem(const Call&, int) { return 0; }
-size_t top_smem(const Call& c, int C) { return mr::score_top_smem((c.nsb + C - 1) / C * mr::kSbRuns, c.P.top_k); }
+size_t top_smem(const Call& c, int) { return mr::score_top_smem(c.nsb * mr::kSbRuns, c.P.top_k); }
 size_t step_smem(const Call& c, int C) {
     const uint32_t rounds = ((c.nsb + C - 1) / C + mr::kThreads / 32 - 1) / (mr::kThreads / 32);
     return (size_t)rounds * mr::kStepRoundBytes;
-}
-
-dim3 forward_grid(const Call& c, int C, int resident) {
-    const size_t clusters = std::max<size_t>(1, (size_t)mr::device_sms() * resident / C);
-    return dim3((unsigned)(std::min(c.rows, clusters) * C), 1, 1);
 }
 
 // Warps per row of an elementwise kernel, and the grid.
@@ -232,24 +280,26 @@ mr_status_t check_teacher(Call& c, int K, const long long* ids, const float* val
     return st;
 }
 
+mr_status_t run_forward(Call& c, mr::ScoreKernel kernel, const Plan& plan, void* stream) {
+    c.P.csize = plan.C;
+    const dim3 grid((unsigned)(std::min<size_t>(c.rows, plan.clusters) * plan.C), 1, 1);
+    cudaError_t e = mr::allow_score_kernel(kernel, plan.C, plan.smem);
+    if (e == cudaSuccess)
+        e = mr::launch_kernel_of(mr::kScoreThreads, kernel, grid, plan.smem, (cudaStream_t)stream, plan.C > 1 ? plan.C : 0, c.P);
+    return launched(c, e, grid, plan.smem);
+}
+
 mr_status_t run_distill(Call& c, bool step, void* stream) {
-    size_t smem = 0;
-    int resident = 1;
-    if (step) {
-        c.P.csize = plan_cluster(c, step_smem, 3, &resident, 2.0);
-        smem = step_smem(c, c.P.csize);
-        c.P.cache_rounds = (uint32_t)(smem / mr::kStepRoundBytes);
-        if (smem > 200 * 1024) {        // a row too long for sixteen CTAs: the rest is read again
-            c.P.cache_rounds = 4;
-            smem = 4 * mr::kStepRoundBytes;
-            resident = 2;
-            c.P.csize = mr::kMaxScoreCluster;
-        }
-    } else {
-        c.P.csize = plan_cluster(c, plain_smem, 3, &resident, 1.0);
+    const mr::ScoreKernel kernel = mr::distill_forward(c.dtype, step);
+    Plan plan = plan_forward(c, kernel, step ? step_smem : plain_smem, step ? 2.0 : 1.0, 1.0, 1.0);
+    if (plan.C == 0) {
+        // no GPU to ask, or a row too long for sixteen CTAs' shared memory:
+        // what does not fit is read again
+        plan = {step ? mr::kMaxScoreCluster : 1, 1, step ? 4 * mr::kStepRoundBytes : 0};
+        plan.clusters = std::max(1, resident_clusters(kernel, plan.C, plan.smem));
     }
-    const dim3 grid = forward_grid(c, c.P.csize, resident);
-    return launched(c, mr::launch_distill(c.P, c.dtype, step, grid, smem, (cudaStream_t)stream), grid, smem);
+    c.P.cache_rounds = (uint32_t)(plan.smem / mr::kStepRoundBytes);
+    return run_forward(c, kernel, plan, stream);
 }
 
 }  // namespace
@@ -286,11 +336,10 @@ mr_status_t mr_logprob(const void* const* logits, const size_t* ld, int W, size_
     c.P.stats = stats;
     c.P.top_ids = top_ids;
     c.P.top_logprob = top_logprob;
-    int resident = 1;
-    c.P.csize = plan_cluster(c, top_k ? top_smem : plain_smem, 3, &resident, 1.0);
-    const size_t smem = top_k ? top_smem(c, c.P.csize) : 0;
-    const dim3 grid = forward_grid(c, c.P.csize, resident);
-    return launched(c, mr::launch_logprob(c.P, dtype, grid, smem, (cudaStream_t)stream), grid, smem);
+    const mr::ScoreKernel kernel = mr::logprob_forward(c.P, dtype);
+    Plan plan = plan_forward(c, kernel, top_k ? top_smem : plain_smem, 1.0, 1.0, 1.0);
+    if (plan.C == 0) plan = {1, 1, top_k ? top_smem(c, 1) : 0};       // no GPU to ask: the launch will fail
+    return run_forward(c, kernel, plan, stream);
 }
 
 mr_status_t mr_logprob_grad(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,

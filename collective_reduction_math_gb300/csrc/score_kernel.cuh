@@ -12,13 +12,20 @@
 // 512 consecutive bytes.  A superblock that reaches over either end of the
 // shard row takes the element-wise loads, which read nothing outside it.
 //
-// Scores are y = scale * x.  A thread keeps a running maximum m and the sums
-//     s = sum exp(y - m),   u = sum exp(y - m) * (y - m)
-// of what it has seen, both in fp32 (y - m as one fused multiply-add, the
-// exponential by the 2^x instruction, relative error 2^-22); a new maximum
-// rescales both.  Threads join as  M = max m,  s = sum s_i e^(m_i - M).  NaN
-// and +inf live in m (the maximum passes NaN on), and m = -inf stands for
-// "nothing but -inf so far", where the sums stay 0.
+// Scores are y = scale * x.  A thread keeps the largest score x_m it has seen
+// and, with c = scale * log2(e), the sums
+//     s = sum 2^(c (x - x_m)),   u = sum 2^(c (x - x_m)) * c (x - x_m)
+// in fp32 (the exponential by the 2^x instruction, relative error 2^-22); a
+// new maximum rescales both.  Threads join as  X = max x_m,
+// s = sum s_i 2^(c (x_i - X)).  One fused multiply-add makes an exponent,
+// c x - R with R = c x_m rounded: what R lost, r = c x_m - R, is the same for
+// every term, so 2^-r goes onto a superblock's sum and not onto its terms.
+// Where |c x_m| reaches 2^31 (masks of the type's lowest value) two different
+// scores are over 2^8 apart in the exponent and the smaller one's term is 0:
+// any c that keeps them 2^7 apart gives the same sums, and the power of two
+// that does so neither rounds nor overflows.
+// NaN and +inf live in x_m (the maximum passes NaN on), and x_m = -inf stands
+// for "nothing but -inf so far", where the sums stay 0.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -28,13 +35,12 @@
 
 namespace mr {
 
-constexpr float kLog2e = 1.4426950408889634f;
-// Differences y - m are taken no lower where they are a factor: e^d is 0 long
-// before, and 0 * -inf (a mask) or an overflowing product (a mask of the
-// type's lowest value) would be NaN.
+// Exponents are taken no lower where they are a factor: 2^d is 0 long before,
+// and 0 * -inf (a mask) or an overflowing product (a mask of the type's lowest
+// value) would be NaN.
 constexpr float kFarBelow = -1e4f;
 constexpr int kSbVectors = kSbRuns;         // 16-byte vectors per lane and superblock
-constexpr int kScoreWarps = kThreads / 32;
+constexpr int kScoreWarps = kThreads / 32;     // the warps that stream
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
@@ -113,6 +119,7 @@ struct Score<MR_FP32> {
     static __device__ __forceinline__ uint32_t load_bits(const char* a) { return *reinterpret_cast<const volatile uint32_t*>(a); }
     static __device__ __forceinline__ void store_bits(char* a, uint32_t v) { *reinterpret_cast<volatile uint32_t*>(a) = v; }
     static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
+    static __device__ __forceinline__ void mask_one(char* a) { *reinterpret_cast<volatile uint32_t*>(a) = 0xff800000u; }
 };
 template <>
 struct Score<MR_BF16> {
@@ -151,6 +158,7 @@ struct Score<MR_BF16> {
     static __device__ __forceinline__ uint32_t load_bits(const char* a) { return *reinterpret_cast<const volatile uint16_t*>(a); }
     static __device__ __forceinline__ void store_bits(char* a, uint32_t v) { *reinterpret_cast<volatile uint16_t*>(a) = (uint16_t)v; }
     static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
+    static __device__ __forceinline__ void mask_one(char* a) { *reinterpret_cast<volatile uint16_t*>(a) = 0xff80u; }
 };
 
 // ---- where a row's shard lies ----
@@ -270,83 +278,81 @@ __device__ __forceinline__ const char* score_at(const ScoreParams& P, uint64_t r
 
 // ---- running softmax statistics ----
 struct Stat {
-    float m, s, u;
+    float x, s, u;
 };
+constexpr float kLn2 = 0.69314718055994531f;
 
-// Raises the running maximum to at least y (NaN included) and rescales.
-template <bool ENT>
-__device__ __forceinline__ void raise(Stat& a, float y) {
-    if (!(y <= a.m)) {
-        if (a.m != neg_inf()) {
-            const float d = fmaxf(__fadd_rn(a.m, -y), kFarBelow);
-            const float f = ex2(__fmul_rn(d, kLog2e));
-            if (ENT) a.u = __fmul_rn(__fmaf_rn(a.s, d, a.u), f);
-            a.s = __fmul_rn(a.s, f);
-        }
-        a.m = y;
+// The reference that exponents are made against: c x - ref, off by r for every x.
+struct Ref {
+    float c, ref, r;
+};
+__device__ __forceinline__ Ref reference(float x, float c) {
+    Ref f{c, __fmul_rn(x, c), 0.0f};
+    if (x == neg_inf()) {
+        f.ref = 0.0f;
+        return f;
     }
+    if (!(fabsf(f.ref) < 2147483648.0f)) {
+        const uint32_t e = (__float_as_uint(x) >> 23) & 255;      // 2^(30 - exponent of x)
+        f.c = __uint_as_float(min(284u - e, 254u) << 23);
+        f.ref = __fmul_rn(x, f.c);
+    }
+    f.r = __fmaf_rn(x, f.c, -f.ref);
+    return f;
+}
+__device__ __forceinline__ float undo(const Ref& f) { return ex2(-f.r); }
+
+// A statistic against another maximum X >= x.
+template <bool ENT>
+__device__ __forceinline__ void rebase(Stat& a, float X, float c) {
+    if (a.x == neg_inf()) {
+        a.s = a.u = 0.0f;
+    } else {
+        const float d = fmaxf(__fmul_rn(__fadd_rn(a.x, -X), c), kFarBelow);
+        const float f = ex2(d);
+        if (ENT) a.u = __fmul_rn(__fmaf_rn(a.s, d, a.u), f);
+        a.s = __fmul_rn(a.s, f);
+    }
+    a.x = X;
 }
 
-// One superblock into a thread's statistics.
+// A thread's running state.
+struct Running {
+    Stat a;
+    Ref f;
+};
+__device__ __forceinline__ Running start_running(float c) { return {{neg_inf(), 0.0f, 0.0f}, {c, 0.0f, 0.0f}}; }
+
+// One superblock into a thread's state.
 template <int DT, bool ENT>
-__device__ __forceinline__ void accumulate(Stat& a, const uint32_t (&w)[16], float scale) {
+__device__ __forceinline__ void accumulate(Running& t, const uint32_t (&w)[16], float c) {
     using S = Score<DT>;
-    raise<ENT>(a, __fmul_rn(S::max_words(w, 16), scale));
-    const float ref = a.m == neg_inf() ? 0.0f : a.m;
-    const F2 sc = f2(scale, scale), off = f2(-ref, -ref), l2 = f2(kLog2e, kLog2e);
+    const float top = S::max_words(w, 16);
+    if (!(top <= t.a.x)) {      // a new maximum, or NaN
+        rebase<ENT>(t.a, top, c);
+        t.f = reference(top, c);
+    }
+    const F2 cc = f2(t.f.c, t.f.c), off = f2(-t.f.ref, -t.f.ref);
     F2 s = f2(0.0f, 0.0f), u = s;
 #pragma unroll
     for (int i = 0; i < S::kPairs; ++i) {
-        float x0, x1;
+        float x0, x1, t0, t1;
         S::pair(w, i, x0, x1);
-        const F2 t = fma2(f2(x0, x1), sc, off);
-        float e0, e1;
-        unpack(mul2(t, l2), e0, e1);
-        const F2 e = f2(ex2(e0), ex2(e1));
+        unpack(fma2(f2(x0, x1), cc, off), t0, t1);
+        const F2 e = f2(ex2(t0), ex2(t1));
         s = add2(s, e);
-        if (ENT) {
-            float t0, t1;
-            unpack(t, t0, t1);
-            u = fma2(e, f2(fmaxf(t0, kFarBelow), fmaxf(t1, kFarBelow)), u);
-        }
+        if (ENT) u = fma2(e, f2(fmaxf(t0, kFarBelow), fmaxf(t1, kFarBelow)), u);
     }
     float p, q;
     unpack(s, p, q);
-    a.s = __fadd_rn(a.s, __fadd_rn(p, q));
+    const float sum = __fadd_rn(p, q), k = undo(t.f);
+    t.a.s = __fmaf_rn(sum, k, t.a.s);
     if (ENT) {
         unpack(u, p, q);
-        a.u = __fadd_rn(a.u, __fadd_rn(p, q));
+        t.a.u = __fmaf_rn(__fmaf_rn(-t.f.r, sum, __fadd_rn(p, q)), k, t.a.u);
     }
 }
 
-// A statistic against another maximum M >= m.
-template <bool ENT>
-__device__ __forceinline__ void rebase(Stat& a, float M) {
-    if (a.m == neg_inf()) {
-        a.s = a.u = 0.0f;
-    } else {
-        const float d = fmaxf(__fadd_rn(a.m, -M), kFarBelow);
-        const float f = expf(d);
-        if (ENT) a.u = a.s == 0.0f ? 0.0f : __fmul_rn(__fmaf_rn(a.s, d, a.u), f);
-        a.s = __fmul_rn(a.s, f);
-    }
-    a.m = M;
-}
-
-// Joins the statistics of a warp's lanes; every lane gets the result.
-template <bool ENT>
-__device__ __forceinline__ Stat warp_join(Stat a) {
-    float M = a.m;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = max_nan(M, __shfl_xor_sync(~0u, M, o));
-    rebase<ENT>(a, M);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        a.s = __fadd_rn(a.s, __shfl_xor_sync(~0u, a.s, o));
-        if (ENT) a.u = __fadd_rn(a.u, __shfl_xor_sync(~0u, a.u, o));
-    }
-    return a;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(~0u, v, o));
@@ -357,23 +363,109 @@ __device__ __forceinline__ float warp_max_nan(float v) {
     for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, o));
     return v;
 }
-
-// A row's final pair: the largest scaled score and the log of the sum of
-// exponentials relative to it; (-inf, 0) for a row of nothing but -inf, NaN
-// for both where a NaN or +inf was seen.
-__device__ __forceinline__ void finish(const Stat& a, float& m, float& logs) {
-    if (a.m == neg_inf()) {
-        m = a.m;
-        logs = 0.0f;
-    } else if (!(a.m < __int_as_float(0x7f800000))) {
-        m = logs = quiet_nan();
-    } else {
-        m = a.m;
-        logs = logf(a.s);
+// Joins the statistics of a warp's lanes; every lane gets the result.
+template <bool ENT>
+__device__ __forceinline__ Stat warp_join(Stat a, float c) {
+    rebase<ENT>(a, warp_max_nan(a.x), c);
+    a.s = warp_sum(a.s);
+    if (ENT) a.u = warp_sum(a.u);
+    return a;
+}
+// Joins the statistics of a row's warps (one warp; every lane gets the result).
+template <bool ENT>
+__device__ __forceinline__ Stat join_parts(const Stat* part, int n, int lane, float c) {
+    constexpr int kEach = kMaxScoreCluster * kScoreWarps / 32;
+    Stat o[kEach];
+    float X = neg_inf();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        o[i] = lane + 32 * i < n ? part[lane + 32 * i] : Stat{neg_inf(), 0.0f, 0.0f};
+        X = max_nan(X, o[i].x);
     }
+    X = warp_max_nan(X);
+    Stat b{X, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        rebase<ENT>(o[i], X, c);
+        b.s = __fadd_rn(b.s, o[i].s);
+        if (ENT) b.u = __fadd_rn(b.u, o[i].u);
+    }
+    b.s = warp_sum(b.s);
+    if (ENT) b.u = warp_sum(b.u);
+    return b;
 }
 
-// ---- thread-block clusters ----
+// What m = scale * x lost in its rounding; 0 where a whole unit and more is
+// lost (a score of the type's lowest value): y is an fp32 number there.
+__device__ __forceinline__ float rounding_of(float x, float scale, float m) {
+    const float rho = __fmaf_rn(x, scale, -m);
+    return fabsf(rho) < 1.0f ? rho : m == m ? 0.0f : m;
+}
+
+// A row's final values: the largest scaled score m, the log of the sum of
+// exponentials relative to it (what the caller sees), and log s (relative to
+// the unrounded scale * x); (-inf, 0, 0) for a row of nothing but -inf, NaN
+// where a NaN or +inf was seen.
+struct Final {
+    float m, logs, log_s;
+};
+__device__ __forceinline__ Final finish(const Stat& a, float scale) {
+    Final f;
+    f.m = __fmul_rn(a.x, scale);
+    if (f.m == neg_inf()) {
+        f.logs = f.log_s = 0.0f;
+    } else if (!(f.m < __int_as_float(0x7f800000))) {
+        f.m = f.logs = f.log_s = quiet_nan();
+    } else {
+        f.log_s = logf(a.s);
+        f.logs = __fadd_rn(f.log_s, rounding_of(a.x, scale, f.m));
+    }
+    return f;
+}
+// log p of a score: -inf for a masked one, NaN in a row that has NaN.
+__device__ __forceinline__ float log_prob(float x, const Stat& a, const Final& f, float scale) {
+    if (f.m != f.m) return f.m;
+    if (x == neg_inf() || f.m == neg_inf()) return neg_inf();
+    return __fmaf_rn(__fadd_rn(x, -a.x), scale, -f.log_s);
+}
+
+// The reference of saved statistics: the largest score x_m again from
+// m = scale * x_m rounded, so that y - m = scale (x - x_m) + rho.  For bf16
+// scores the quotient rounds to x_m itself.  For fp32 it may be off by a step,
+// which rho makes good but for scores so large that a step is whole units:
+// there the farther of the scores that round to m is taken, which finds a
+// mask of the type's lowest value.
+struct SavedRef {
+    Ref f;
+    float x, rho;
+};
+template <int DT>
+__device__ __forceinline__ SavedRef saved_reference(float m, float scale, float c) {
+    SavedRef k;
+    k.x = m;
+    k.rho = 0.0f;
+    if (m != neg_inf()) {
+        k.x = __fdiv_rn(m, scale);
+        if (DT == MR_BF16) {
+            uint32_t w;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(w) : "f"(k.x));
+            k.x = __uint_as_float(w << 16);
+        } else if (fabsf(m) > 1e30f) {
+            const float lowest = __int_as_float(0xff7fffff);
+            k.x = fmaxf(k.x, lowest);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float next = __uint_as_float(__float_as_uint(k.x) + 1);
+                if (k.x != lowest && __fmul_rn(next, scale) == m) k.x = next;
+            }
+        }
+        k.rho = rounding_of(k.x, scale, m);
+    }
+    k.f = reference(k.x, c);
+    return k;
+}
+
+// ---- thread-block clusters and barriers inside a CTA ----
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -387,9 +479,24 @@ __device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
 __device__ __forceinline__ void peer_store(uint32_t a, uint32_t v) {
     asm volatile("st.shared::cluster.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// The forward kernels' CTAs: 8 warps that stream a row's scores and one warp
+// that does everything else of it.  That warp fetches the next rows' ids and
+// lists ahead of the stream, and joins the statistics of a row while the
+// stream is in the next one, so the stream never waits for a chain of small
+// loads.  They meet at named barriers; what passes through shared memory is
+// double-buffered by the row's parity:
+//   kRowReady + parity   the row warp has set a row up (the first two before it
+//                        begins, row i+2 when it has joined row i); the stream
+//                        waits before it starts the row
+//   kRowDone + parity    the stream's warps have left their results of row i;
+//                        the row warp waits before it joins them
+// So the stream is at most one row ahead and no buffer of row i is still in
+// use when row i+2 begins.
+enum { kRowReady = 1, kRowDone = 3, kRowStep = 5, kRowHelp = 6, kRowHelped = 7 };     // 0 is __syncthreads
+__device__ __forceinline__ void bar_sync(int id) { asm volatile("barrier.cta.sync %0, %1;" :: "r"(id), "n"(kScoreThreads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id) { asm volatile("barrier.cta.arrive %0, %1;" :: "r"(id), "n"(kScoreThreads) : "memory"); }
 
 }  // namespace mr

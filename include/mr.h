@@ -273,7 +273,7 @@ mr_status_t mr_reduce_scatter_ex(const void* const* send, void* const* recv, int
  * library's own.
  */
 #define MR_MAX_TOP 64               /* top alternatives per row */
-#define MR_MAX_TOP_VOCAB 4194304    /* columns of a row with top_k > 0 */
+#define MR_MAX_TOP_VOCAB 2097152    /* columns of a row with top_k > 0 */
 #define MR_MAX_TEACHER 128          /* teacher entries per row */
 
 /*

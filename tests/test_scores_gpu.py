@@ -114,6 +114,7 @@ def _check_forward(x, ids, scale, k, o, what):
     T = x.shape[0]
     for t in range(T):
         lp, h, stats, top, top_lp = ref.logprob_row(x[t], None if ids is None else int(ids[t]), scale, k)
+        top_lp = [v if v >= -3.4028235e38 or v != v else -np.inf for v in top_lp]      # below fp32's range
         spread = abs(stats[1]) + 1 if np.isfinite(stats[1]) else 1.0
         w = f"{what} row {t}"
         if ids is not None:
@@ -216,6 +217,75 @@ def test_top_k_where_it_lies(mr, order):
         o = _forward(mr, rows, np.array([0, V - 1]), 1.0, 64)
         for t in range(2):
             assert o["top"][t].tolist() == ref.logprob_row(xs[t].double().numpy(), 0, 1.0, 64)[3], (order, dtype)
+
+
+@pytest.mark.parametrize("T", [3, 1000])        # one row a cluster, and several
+@pytest.mark.parametrize("k", [1, 20, 64])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_top_k_ties_and_masks(mr, dtype, k, T):
+    """Few places left by a mask, equal scores in floods, scores crowded in a run."""
+    V = 9001
+    x = _scores(61, T, V, dtype).float()
+    x[0] = float("-inf")
+    x[0, [5, 4000, 9000]] = 1.0
+    x[1] = 2.0
+    x[2] = (x[2] * 2).round() / 2
+    if T > 3:
+        x[-1, :300] += 50.0
+        x[-2] = float("-inf")
+        x[-3, 100:] = float("-inf")
+        x[-4] = 0.0
+        x[-4, ::7] = 1.0
+    x = x.to(_dt(dtype))
+    rows = Rows(2, T, V, dtype, 0, 0, x)
+    o = _forward(mr, rows, np.zeros(T, np.int64), 1.0, k)
+    for t in {0, 1, 2, T - 1, T - 2, T - 3, T - 4} & set(range(T)):
+        want = ref.logprob_row(x[t].double().numpy(), 0, 1.0, k)
+        assert o["top"][t].tolist() == want[3], t
+        _close(o["top_lp"][t].cpu().numpy(), want[4], REL + 4 * U * 128, f"row {t}")
+
+
+@pytest.mark.parametrize("scale", [0.7, 3.0])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_lowest_values_at_a_scale(mr, dtype, scale):
+    """Rows of the type's lowest value, whose scaled scores round by whole
+    units or overflow to -inf."""
+    import torch
+    V, T = 1500, 4
+    low = torch.finfo(_dt(dtype)).min
+    x = _scores(71, T, V, dtype).float()
+    x[0] = low
+    x[1] = low
+    x[1, 77] = 1.0
+    x[2, ::2] = low
+    x = x.to(_dt(dtype))
+    rows, out = Rows(2, T, V, dtype, 0, 0, x), Rows(2, T, V, dtype)
+    ids = np.array([3, 77, 1, 2])
+    o = _forward(mr, rows, ids, scale, 3)
+    sc = float(np.float32(scale))
+    y_low = float(np.float32(np.float64(x[0, 0].item()) * sc)) if abs(x[0, 0].item()) * sc < 3.4028235e38 else -np.inf
+    if y_low == -np.inf:        # a masked row in fp32
+        assert o["stats"][0].tolist() == [-np.inf, 0.0] and o["lp"][0].item() == -np.inf and o["h"][0].item() == 0
+    else:
+        _close(o["stats"][0].cpu().numpy(), [y_low, np.log(V)], [0.0, REL])
+        _close(o["lp"][0].item(), -np.log(V), REL)
+        _close(o["h"][0].item(), np.log(V), 2 * REL * 8)
+    assert o["top"][0].tolist() == [0, 1, 2]
+    _check_forward(x[1:].double().numpy(), ids[1:], sc, 3, {n: v[1:] for n, v in o.items()}, "lowest")
+    g = torch.ones(T, device="cuda")
+    mr.mr_logprob_grad(rows.views, torch.from_numpy(ids).cuda(), o["stats"], out.views, g_logprob=g, scale=scale)
+    torch.cuda.synchronize()
+    got = out.host()
+    if y_low == -np.inf:
+        want = np.zeros(V)
+        want[3] = 0.0 if got[0, 3] == 0 else sc      # the place itself is finite: either reading is a number
+    else:
+        want = np.full(V, -sc / V)
+        want[3] += sc
+    _close(got[0], want, HALF_STEP[dtype] * np.abs(want) + 2 * REL * sc / V + 4 * U * (np.arange(V) == 3))
+    for t in (1, 2, 3):
+        w = ref.logprob_grad_row(x[t].double().numpy(), int(ids[t]), sc, 1.0, 0.0)
+        _close(got[t], w, _prob_tol(w, np.abs(w) + 4 * U / REL * sc * (np.arange(V) == ids[t]), dtype))
 
 
 def _stats(x, scale, ids=None):
