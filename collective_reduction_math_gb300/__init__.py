@@ -304,35 +304,45 @@ def _score_rows(tensors, name):
     if not tensors:
         raise ValueError(f"{name}: empty list of rank buffers")
     W, t0 = len(tensors), tensors[0]
-    rows, vocab = t0.shape[0], 0
-    ptrs, lds = (ctypes.c_void_p * W)(), (ctypes.c_size_t * W)()
+    rows, dtype = t0.shape[0], t0.dtype
+    ptrs, lds, vocab = [], [], 0
     for r, t in enumerate(tensors):
-        if t.dim() != 2 or not t.is_cuda or t.dtype != t0.dtype or t.shape[0] != rows:
+        shape = t.shape
+        if len(shape) != 2 or not t.is_cuda or t.dtype is not dtype or shape[0] != rows:
             raise ValueError(f"{name}: rank buffers must be 2-D CUDA tensors [rows, columns] of one dtype")
-        n = t.shape[1]
+        n = shape[1]
         ld, step = t.stride()
         if (step != 1 and n > 1) or (ld < n and rows > 1):
             raise ValueError(f"{name}[{r}]: the columns of a row must lie beside each other and rows must not overlap")
-        ptrs[r] = t.data_ptr()
-        lds[r] = ld if ld > n else n
+        ptrs.append(t.data_ptr())
+        lds.append(ld if ld > n else n)
         vocab += n
-    for r, t in enumerate(tensors if W > 1 else ()):
-        if t.shape[1] != (r + 1) * vocab // W - r * vocab // W:
-            raise ValueError(f"{name}[{r}]: {t.shape[1]} columns, but rank {r} of {W} holds columns "
-                             f"[{r * vocab // W}, {(r + 1) * vocab // W}) of {vocab}")
-    return ptrs, lds, rows, vocab, _dtype_code(t0)
+    if W > 1:
+        for r, t in enumerate(tensors):
+            if t.shape[1] != (r + 1) * vocab // W - r * vocab // W:
+                raise ValueError(f"{name}[{r}]: {t.shape[1]} columns, but rank {r} of {W} holds columns "
+                                 f"[{r * vocab // W}, {(r + 1) * vocab // W}) of {vocab}")
+    return (ctypes.c_void_p * W)(*ptrs), (ctypes.c_size_t * W)(*lds), rows, vocab, _dtype_code(t0)
 
 
-def _row_ptr(t, name, rows, per, integer=False):
-    """The address of a per-row array (None stays None)."""
+def _row_ptr(t, name, n, dtype):
+    """The address of a per-row array of n elements (None stays None)."""
     if t is None:
         return None
-    import torch
-    if t.dtype is not (torch.int64 if integer else torch.float32) or not t.is_cuda or not t.is_contiguous() \
-            or t.numel() != rows * per:
-        raise ValueError(f"{name}: a contiguous CUDA tensor of {'int64' if integer else 'float32'} with "
-                         f"{rows} x {per} elements is needed")
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype} with {n} elements is needed")
     return t.data_ptr()
+
+
+def _score_stream(stream, t):
+    """As _stream, by torch's direct lookup where it has one: these calls are short, and
+    torch.cuda.current_stream() builds an object for each (3 us of a 12 us call on GB300's host)."""
+    if stream is None:
+        import torch
+        direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if direct is not None:
+            return direct(t.get_device())
+    return _stream(stream)
 
 
 def _grad_rows(logits, grad, rows, vocab, code):
@@ -350,15 +360,13 @@ def mr_logprob(logits, ids=None, scale=1.0, logprob=None, entropy=None, stats=No
     Outputs, each optional: logprob, entropy [T] fp32; stats [T, 2] fp32 (for
     mr_logprob_grad); top_ids [T, k] int64 and top_logprob [T, k] fp32.  y =
     scale * logits."""
+    from torch import float32, int64
     xp, ld, rows, vocab, code = _score_rows(logits, "logits")
-    k = 0
-    for t in (top_ids, top_logprob):
-        if t is not None:
-            k = t.shape[-1]
-    st = load().mr_logprob(xp, ld, len(logits), rows, vocab, code, scale, _row_ptr(ids, "ids", rows, 1, True), k,
-                           _row_ptr(logprob, "logprob", rows, 1), _row_ptr(entropy, "entropy", rows, 1),
-                           _row_ptr(stats, "stats", rows, 2), _row_ptr(top_ids, "top_ids", rows, k, True),
-                           _row_ptr(top_logprob, "top_logprob", rows, k), _stream(stream))
+    k = top_ids.shape[-1] if top_ids is not None else top_logprob.shape[-1] if top_logprob is not None else 0
+    st = load().mr_logprob(xp, ld, len(logits), rows, vocab, code, scale, _row_ptr(ids, "ids", rows, int64), k,
+                           _row_ptr(logprob, "logprob", rows, float32), _row_ptr(entropy, "entropy", rows, float32),
+                           _row_ptr(stats, "stats", 2 * rows, float32), _row_ptr(top_ids, "top_ids", k * rows, int64),
+                           _row_ptr(top_logprob, "top_logprob", k * rows, float32), _score_stream(stream, logits[0]))
     if st:
         _raise(st)
 
@@ -367,19 +375,23 @@ def mr_logprob_grad(logits, ids, stats, grad, g_logprob=None, entropy=None, g_en
     """Gradient of g_logprob . logprob + g_entropy . entropy with respect to
     the scores, into ``grad`` (W rank buffers; may be ``logits``).  stats and
     entropy are mr_logprob's outputs."""
+    from torch import float32, int64
     xp, ld, rows, vocab, code = _score_rows(logits, "logits")
     gp, gl = _grad_rows(logits, grad, rows, vocab, code)
-    st = load().mr_logprob_grad(xp, ld, len(logits), rows, vocab, code, scale, _row_ptr(ids, "ids", rows, 1, True),
-                                _row_ptr(stats, "stats", rows, 2), _row_ptr(entropy, "entropy", rows, 1),
-                                _row_ptr(g_logprob, "g_logprob", rows, 1), _row_ptr(g_entropy, "g_entropy", rows, 1),
-                                gp, gl, _stream(stream))
+    st = load().mr_logprob_grad(xp, ld, len(logits), rows, vocab, code, scale, _row_ptr(ids, "ids", rows, int64),
+                                _row_ptr(stats, "stats", 2 * rows, float32), _row_ptr(entropy, "entropy", rows, float32),
+                                _row_ptr(g_logprob, "g_logprob", rows, float32),
+                                _row_ptr(g_entropy, "g_entropy", rows, float32), gp, gl, _score_stream(stream, logits[0]))
     if st:
         _raise(st)
 
 
 def _teacher(teacher_ids, teacher_val, rows, mode, teacher_scale):
-    k = teacher_ids.shape[-1] if teacher_ids.dim() == 2 else 0
-    return (k, _row_ptr(teacher_ids, "teacher_ids", rows, k, True), _row_ptr(teacher_val, "teacher_val", rows, k),
+    from torch import float32, int64
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids: a [rows, K] tensor is needed")
+    k = teacher_ids.shape[1]
+    return (k, _row_ptr(teacher_ids, "teacher_ids", k * rows, int64), _row_ptr(teacher_val, "teacher_val", k * rows, float32),
             _code(DISTILL_MODES, mode, "mode"), teacher_scale)
 
 
@@ -390,10 +402,12 @@ def mr_distill_topk(logits, teacher_ids, teacher_val, loss=None, stats=None, mod
     takes logits and renormalises them over the list, 'tail' takes log
     probabilities and treats the remaining mass as one more outcome.  stats
     [T, 4] is what mr_distill_topk_grad takes."""
+    from torch import float32
     xp, ld, rows, vocab, code = _score_rows(logits, "logits")
     st = load().mr_distill_topk(xp, ld, len(logits), rows, vocab, code, scale,
                                 *_teacher(teacher_ids, teacher_val, rows, mode, teacher_scale),
-                                _row_ptr(loss, "loss", rows, 1), _row_ptr(stats, "stats", rows, 4), _stream(stream))
+                                _row_ptr(loss, "loss", rows, float32), _row_ptr(stats, "stats", 4 * rows, float32),
+                                _score_stream(stream, logits[0]))
     if st:
         _raise(st)
 
@@ -402,12 +416,13 @@ def mr_distill_topk_grad(logits, teacher_ids, teacher_val, stats, g_loss, grad, 
                          teacher_scale=1.0, stream=None):
     """Gradient of g_loss . loss with respect to the scores, into ``grad`` (W
     rank buffers; may be ``logits``)."""
+    from torch import float32
     xp, ld, rows, vocab, code = _score_rows(logits, "logits")
     gp, gl = _grad_rows(logits, grad, rows, vocab, code)
     st = load().mr_distill_topk_grad(xp, ld, len(logits), rows, vocab, code, scale,
                                      *_teacher(teacher_ids, teacher_val, rows, mode, teacher_scale),
-                                     _row_ptr(stats, "stats", rows, 4), _row_ptr(g_loss, "g_loss", rows, 1), gp, gl,
-                                     _stream(stream))
+                                     _row_ptr(stats, "stats", 4 * rows, float32), _row_ptr(g_loss, "g_loss", rows, float32),
+                                     gp, gl, _score_stream(stream, logits[0]))
     if st:
         _raise(st)
 
@@ -416,12 +431,13 @@ def mr_distill_topk_step(logits, teacher_ids, teacher_val, weight, loss, grad, m
                          teacher_scale=1.0, stream=None):
     """Loss [T] (unweighted; may be None) and the gradient of weight . loss in
     one kernel, reading the scores once (``grad`` may be ``logits``)."""
+    from torch import float32
     xp, ld, rows, vocab, code = _score_rows(logits, "logits")
     gp, gl = _grad_rows(logits, grad, rows, vocab, code)
     st = load().mr_distill_topk_step(xp, ld, len(logits), rows, vocab, code, scale,
                                      *_teacher(teacher_ids, teacher_val, rows, mode, teacher_scale),
-                                     _row_ptr(weight, "weight", rows, 1), _row_ptr(loss, "loss", rows, 1), gp, gl,
-                                     _stream(stream))
+                                     _row_ptr(weight, "weight", rows, float32), _row_ptr(loss, "loss", rows, float32), gp, gl,
+                                     _score_stream(stream, logits[0]))
     if st:
         _raise(st)
 

@@ -129,35 +129,42 @@ __device__ __forceinline__ void teacher_mass(Teacher& t, const List& L, const Sc
     }
 }
 
-// Takes the listed places of superblock sb out of its words: where there are
-// any (one vote), through the warp's 2 KiB of shared memory.  Selecting them
-// in registers, 32 tests a lane, cost as much as the superblock's sum.
+// The rounds (every `step`-th superblock from `first`, up to `end`) in which an
+// entry of the list lies, as bits round mod 32.
 template <int DT>
-__device__ __forceinline__ void mask_listed(uint32_t (&w)[16], const List& L, uint32_t sb, uint4* bounce, int lane) {
+__device__ __forceinline__ uint32_t rounds_with_entries(const List& L, uint32_t first, uint32_t end, uint32_t step) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kListRegs; ++i) {
+        const uint32_t sb = L.place[i] >> Score<DT>::kLogSb, d = sb - first;
+        if (sb >= first && sb < end && d % step == 0) bits |= 1u << ((d / step) & 31);
+    }
+    return __reduce_or_sync(~0u, bits);
+}
+// Takes the listed places of superblock sb out of its block in shared memory,
+// whose copies are there.
+template <int DT>
+__device__ __forceinline__ void mask_listed(uint4* block, const List& L, uint32_t sb) {
     using S = Score<DT>;
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kListRegs; ++i) any |= (L.place[i] >> S::kLogSb) == sb;
-    if (!__any_sync(~0u, any)) return;
-#pragma unroll
-    for (int j = 0; j < kSbVectors; ++j) bounce[j * 32 + lane] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kListRegs; ++i)
         if ((L.place[i] >> S::kLogSb) == sb)
-            S::mask_one(reinterpret_cast<char*>(bounce) + (size_t)(L.place[i] & ((1u << S::kLogSb) - 1)) * S::kBytes);
+            S::mask_one(reinterpret_cast<char*>(block) + (size_t)(L.place[i] & ((1u << S::kLogSb) - 1)) * S::kBytes);
     __syncwarp();
+}
+// The same for words in registers, through a block of the warp's: picking
+// them out in registers, 32 tests a lane, costs as much as the sum.
+template <int DT>
+__device__ __forceinline__ void mask_listed(uint32_t (&w)[16], const List& L, uint32_t sb, uint4* block, int lane) {
 #pragma unroll
-    for (int j = 0; j < kSbVectors; ++j) {
-        const uint4 v = bounce[j * 32 + lane];
-        w[4 * j] = v.x;
-        w[4 * j + 1] = v.y;
-        w[4 * j + 2] = v.z;
-        w[4 * j + 3] = v.w;
-    }
+    for (int j = 0; j < kSbVectors; ++j) block[j * 32 + lane] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    mask_listed<DT>(block, L, sb);
+    read_block(w, block, lane);
 }
 
-// The same for rows too long for the cache, which leave no shared memory.
+// And in registers alone, for the superblocks of a row that is too long for
+// its cache, which leaves no shared memory.
 template <int DT>
 __device__ __forceinline__ void mask_listed_in_registers(uint32_t (&w)[16], const List& L, uint32_t sb, int lane) {
     using S = Score<DT>;
@@ -171,13 +178,11 @@ __device__ __forceinline__ void mask_listed_in_registers(uint32_t (&w)[16], cons
             if ((int)((p >> S::kLogVe) & 31) == lane) mine |= 1u << ((p >> (S::kLogVe + 5)) * S::VE + (p & (S::VE - 1)));
         }
     }
-    if (mine) {
 #pragma unroll
-        for (int j = 0; j < kSbVectors; ++j)
+    for (int j = 0; j < kSbVectors; ++j)
 #pragma unroll
-            for (int e = 0; e < S::VE; ++e)
-                if ((mine >> (j * S::VE + e)) & 1) S::put(w, j, e, S::kBytes == 2 ? S::kFill & 0xffffu : S::kFill);
-    }
+        for (int e = 0; e < S::VE; ++e)
+            if ((mine >> (j * S::VE + e)) & 1) S::put(w, j, e, S::kBytes == 2 ? S::kFill & 0xffffu : S::kFill);
 }
 
 // What the gradient outside the list needs: coef * 2^(c x - ref).
@@ -200,58 +205,17 @@ __device__ __forceinline__ void rest_gradient(uint32_t (&w)[16], const Coef& k) 
     }
 }
 
-__device__ __forceinline__ void copy16(uint32_t to, const char* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
-}
-// One superblock of a row into the CTA's cache (slots of 16 bytes that only
-// this thread touches): whole vectors by asynchronous copies, the row's ends
-// element by element.
-template <int DT>
-__device__ __forceinline__ void cache_superblock(uint4* slot, const ShardRow& sr, uint32_t p0, int lane) {
-    using S = Score<DT>;
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
-    const char* from = sr.base + ((uint64_t)p0 + (uint32_t)lane * S::VE) * S::kBytes;
-    if (p0 >= sr.lo && p0 + (1u << S::kLogSb) <= sr.hi) {
-#pragma unroll
-        for (int j = 0; j < kSbVectors; ++j) copy16(to + j * kThreads * 16, from + j * 512);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kSbVectors; ++j) {
-            const uint32_t p = p0 + (uint32_t)(j * 32 + lane) * S::VE;
-            if (p >= sr.lo && p + S::VE <= sr.hi) {
-                copy16(to + j * kThreads * 16, from + j * 512);
-            } else {
-                uint32_t v[4];
-                load_vector<DT>(v, 0, sr, p);
-                slot[j * kThreads] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// This thread's copies are there.
-__device__ __forceinline__ void cache_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void from_cache(uint32_t (&w)[16], const uint4* slot) {
-#pragma unroll
-    for (int j = 0; j < kSbVectors; ++j) {
-        const uint4 v = slot[j * kThreads];
-        w[4 * j] = v.x;
-        w[4 * j + 1] = v.y;
-        w[4 * j + 2] = v.z;
-        w[4 * j + 3] = v.w;
-    }
-}
-
 template <int DT, bool STEP>
 __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_constant__ ScoreParams P) {
     using S = Score<DT>;
-    extern __shared__ uint4 cache[];        // STEP: this CTA's part of a row, [round][vector][thread]
-    __shared__ Stat part[2][kMaxScoreCluster * kScoreWarps];
+    extern __shared__ uint4 smem[];         // STEP: this CTA's part of a row, [round][warp] blocks
+    __shared__ uint4 bounce[STEP ? 1 : kScoreWarps][STEP ? 1 : kSbVectors * 32];      // a block of each warp
+    __shared__ LaneStats stats[2];
+    __shared__ Stat part[2][kMaxScoreCluster];
     __shared__ uint32_t s_place[2][MR_MAX_TEACHER];
     __shared__ int row_out[2];              // the row is left out
     __shared__ float s_grad[MR_MAX_TEACHER];        // STEP: the listed places' gradients
     __shared__ Coef s_coef;
-    __shared__ uint4 bounce[STEP ? 1 : kScoreWarps][STEP ? 1 : kSbVectors * 32];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int C = P.csize, crank = C > 1 ? (int)cluster_rank() : 0;
@@ -265,141 +229,111 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
 
     if (warp < kScoreWarps) {
         // ================= the stream =================
+        constexpr int kBlock = kSbVectors * 32;
         uint32_t w[16];
-        Walk<DT> walk;
-        const uint32_t first = sb_lo + warp;
-        const uint32_t my_rounds = first < sb_hi ? (sb_hi - first + kScoreWarps - 1) / kScoreWarps : 0;
-        const uint32_t cached = STEP ? min(my_rounds, P.cache_rounds) : 0;
-        uint4* const slots = cache + threadIdx.x;
-        auto fetch = [&](uint32_t (&to)[16], uint64_t r, uint32_t sb) {
-            walk.seek(P, r, sb);
-            load_superblock<DT>(to, walk.sr, walk.place(sb), lane);
-        };
-        if (row < P.rows && my_rounds) {
-            if constexpr (STEP) {
-                for (uint32_t i = 0; i < cached; ++i) {
-                    walk.seek(P, row, first + i * kScoreWarps);
-                    cache_superblock<DT>(slots + i * kSbVectors * kThreads, walk.sr, walk.place(first + i * kScoreWarps), lane);
+        Feed<DT> feed;          // without STEP
+        uint32_t ahead_runs = 0;
+        Walk<DT> walk;          // STEP: this row, and the next one's copies
+        auto block_of = [&](uint32_t round) { return smem + (round * kScoreWarps + warp) * kBlock; };
+        auto rounds_of = [&](uint32_t first) { return first < sb_hi ? (sb_hi - first + kScoreWarps - 1) / kScoreWarps : 0; };
+        if constexpr (STEP) {
+            const uint32_t first = first_superblock(sb_lo, warp, 0);
+            if (row < P.rows)
+                for (uint32_t i = 0; i < min(rounds_of(first), P.cache_rounds); ++i) {
+                    walk.seek(P, row, first + i * kScoreWarps, lane);
+                    begin_copy<DT>(block_of(i), P, row, walk, first + i * kScoreWarps, lane);
                 }
-            } else {
-                fetch(w, row, first);
-            }
+            copies_commit();
+        } else {
+            ahead_runs = feed.template start<false>(w, P, sb_lo, sb_hi, row, stride, warp, lane);
         }
         bool waited = C == 1;
         int parity = 0;
-        for (; row < P.rows; row += stride, parity ^= 1) {
+        for (uint32_t count = 0; row < P.rows; row += stride, parity ^= 1, ++count) {
             bar_sync(kRowReady + parity);
             const bool out = row_out[parity];
+            const uint32_t first = first_superblock(sb_lo, warp, count);
             List L;
 #pragma unroll
             for (int i = 0; i < kListRegs; ++i) L.place[i] = i < regs ? s_place[parity][lane + 32 * i] : kNoPlace;
-            const uint64_t next_row = row + stride;
+            const uint32_t entries = out ? 0 : rounds_with_entries<DT>(L, first, sb_hi, kScoreWarps);
+            const uint32_t rounds = rounds_of(first), cached = STEP ? min(rounds, P.cache_rounds) : 0;
             Running run = start_running(P.c);
             if constexpr (!STEP) {
                 if (out) {
-                    walk = Walk<DT>{};
-                    if (next_row < P.rows && my_rounds) fetch(w, next_row, first);
+                    ahead_runs = feed.template drop<false>(w, ahead_runs, P, count, warp, lane);
                 } else {
-                    for (uint32_t sb = first; sb < sb_hi; sb += kScoreWarps) {
-                        uint32_t nx[16];
-                        if (sb + kScoreWarps < sb_hi) {
-                            fetch(nx, row, sb + kScoreWarps);
-                        } else if (next_row < P.rows) {     // the next row's first, left out or not
-                            walk = Walk<DT>{};
-                            fetch(nx, next_row, first);
-                        }
-                        mask_listed<DT>(w, L, sb, bounce[warp], lane);
-                        accumulate<DT, false>(run, w, P.c);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = nx[i];
-                    }
+                    ahead_runs = feed.template each<false>(w, ahead_runs, P, first, warp, lane, [&](uint32_t (&x)[16], uint32_t sb, uint32_t) {
+                        if ((entries >> (((sb - first) / kScoreWarps) & 31)) & 1) mask_listed<DT>(x, L, sb, bounce[warp], lane);
+                        accumulate<DT, false>(run, x, S::template max_words<16>(x), P.c);
+                    });
                 }
-            } else if (!out) {
-                // this row's copies are there; the listed places of this warp's superblocks leave the cache
-                cache_wait();
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kListRegs; ++i) {
-                    const uint32_t sb = L.place[i] >> S::kLogSb, round = (sb - first) / kScoreWarps;
-                    if (sb >= first && (sb - first) % kScoreWarps == 0 && round < cached) {
-                        const uint32_t at = L.place[i] & ((1u << S::kLogSb) - 1);      // vector, lane and element in it
-                        char* slot = reinterpret_cast<char*>(
-                            cache + ((round * kSbVectors + (at >> (S::kLogVe + 5))) * kThreads + warp * 32 + ((at >> S::kLogVe) & 31)));
-                        S::mask_one(slot + (at & (S::VE - 1)) * S::kBytes);
-                    }
-                }
-                __syncwarp();
-                for (uint32_t i = 0; i < cached; ++i) {
-                    from_cache(w, slots + i * kSbVectors * kThreads);
-                    accumulate<DT, false>(run, w, P.c);
-                }
-                walk = Walk<DT>{};
-                for (uint32_t i = cached; i < my_rounds; ++i) {     // a row longer than the cache
-                    const uint32_t sb = first + i * kScoreWarps;
-                    fetch(w, row, sb);
-                    mask_listed_in_registers<DT>(w, L, sb, lane);
-                    accumulate<DT, false>(run, w, P.c);
-                }
-            }
-            Stat a = run.a;
-            if (!out) a = warp_join<false>(a, P.c);
-            if (!waited) cluster_wait();
-            waited = true;
-            if (!out) {
-                if (C == 1) {
-                    if (lane == 0) part[parity][warp] = a;
-                } else if (lane < (STEP ? C : 1)) {
-                    const uint32_t to = peer_address(&part[parity][crank * kScoreWarps + warp], lane);
-                    peer_store(to, __float_as_uint(a.x));
-                    peer_store(to + 4, __float_as_uint(a.s));
-                }
-            }
-            if (C > 1) {
-                __syncwarp();
-                cluster_arrive();
-                waited = false;     // for this row's phase: before the next row's store, or the end
             } else {
-                bar_arrive(kRowDone + parity);
+                copies_wait();          // this row's copies are there
+                if (!out) {
+                    for (uint32_t i = 0; i < cached; ++i) {
+                        if ((entries >> (i & 31)) & 1) mask_listed<DT>(block_of(i), L, first + i * kScoreWarps);
+                        read_block(w, block_of(i), lane);
+                        accumulate<DT, false>(run, w, S::template max_words<16>(w), P.c);
+                    }
+                    walk = Walk<DT>{};
+                    for (uint32_t i = cached; i < rounds; ++i) {        // a row longer than the cache
+                        const uint32_t sb = first + i * kScoreWarps;
+                        walk.seek(P, row, sb, lane);
+                        load_superblock<DT>(w, P, row, walk, sb, lane);
+                        if ((entries >> (i & 31)) & 1) mask_listed_in_registers<DT>(w, L, sb, lane);
+                        accumulate<DT, false>(run, w, S::template max_words<16>(w), P.c);
+                    }
+                }
+            }
+            if (!out) stats[parity].template put<false>(run.a);
+            bar_arrive(kRowDone + parity);
+            if (C > 1) {
+                if (!waited) cluster_wait();
+                cluster_arrive();
+                waited = false;     // for this row's phase: before the next one, or the end
             }
             if constexpr (STEP) {
                 Coef coef{P.c, 0.0f, 0.0f};
-                if (!waited) cluster_wait();
-                waited = true;
                 bar_sync(kRowStep);
                 if (!out) coef = s_coef;
                 Walk<DT> ahead;
                 walk = Walk<DT>{};
-                ShardRow to{};
-                uint32_t sb = first;
-                if (out) cache_wait();      // its copies, before the next row's into the same slots
-                for (uint32_t i = 0; i < my_rounds; ++i, sb += kScoreWarps) {
-                    if (walk.seek(P, row, sb)) to = shard_row<DT>(P.g[walk.r], P.ldg[walk.r], row, P.col0[walk.r + 1] - P.col0[walk.r]);
-                    const uint32_t p0 = walk.place(sb);
-                    if (out) {
+                Output<DT> to;
+                // the next row's copies go into the blocks as they empty
+                const uint64_t next_row = row + stride;
+                const uint32_t next_first = first_superblock(sb_lo, warp, count + 1);
+                const uint32_t next_cached = next_row < P.rows ? min(rounds_of(next_first), P.cache_rounds) : 0;
+                for (uint32_t i = 0; i < max(rounds, next_cached); ++i) {
+                    const uint32_t sb = first + i * kScoreWarps;
+                    if (i < rounds) {
+                        if (walk.seek(P, row, sb, lane)) to.follow(P, row, walk, lane);
+                        if (out) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = 0;
-                    } else {
-                        if (i < cached) from_cache(w, slots + i * kSbVectors * kThreads);
-                        else load_superblock<DT>(w, walk.sr, p0, lane);
-                        rest_gradient<DT>(w, coef);
+                            for (int e = 0; e < 16; ++e) w[e] = 0;
+                        } else {
+                            if (i < cached) read_block(w, block_of(i), lane);
+                            else load_superblock<DT>(w, P, row, walk, sb, lane);
+                            rest_gradient<DT>(w, coef);
+                        }
                     }
-                    if (i < cached && next_row < P.rows) {      // the slot is free: the next row's copy into it
-                        ahead.seek(P, next_row, sb);
-                        cache_superblock<DT>(slots + i * kSbVectors * kThreads, ahead.sr, ahead.place(sb), lane);
+                    if (i < next_cached) {
+                        const uint32_t next_sb = next_first + i * kScoreWarps;
+                        ahead.seek(P, next_row, next_sb, lane);
+                        begin_copy<DT>(block_of(i), P, next_row, ahead, next_sb, lane);
                     }
-                    store_superblock<DT>(w, walk.sr, to, p0, lane);
-#pragma unroll
-                    for (int e = 0; e < kListRegs; ++e) {
-                        if (e >= regs) break;
-                        const bool mine = (L.place[e] >> S::kLogSb) == sb;
-                        if (__any_sync(~0u, mine)) {        // after the vector stores of every lane
+                    if (i < rounds) {
+                        to.store(w, P, row, walk, sb, lane);
+                        if ((entries >> (i & 31)) & 1) {        // after the vector stores of every lane
                             __syncwarp();
-                            if (mine)
-                                S::store_one(to.base + (uint64_t)(L.place[e] - (walk.sb_lo << S::kLogSb) - walk.sr.lo + to.lo) * S::kBytes,
-                                             s_grad[lane + 32 * e]);
+#pragma unroll
+                            for (int e = 0; e < kListRegs; ++e)
+                                if ((L.place[e] >> S::kLogSb) == sb)
+                                    S::store_one(Output<DT>::element(P, row, walk.r, L.place[e] - (P.sb0[walk.r] << S::kLogSb)), s_grad[lane + 32 * e]);
                         }
                     }
                 }
+                copies_commit();
             }
         }
         if (!waited) cluster_wait();
@@ -455,11 +389,15 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                 l.s = warp_sum(l.s);
             }
         }
-        if (C == 1) {
-            bar_sync(kRowDone + parity);
-        } else {
+        bar_sync(kRowDone + parity);
+        Stat b{neg_inf(), 0.0f, 0.0f};
+        if (!out) b = stats[parity].template join<false>(lane, P.c);
+        if (C > 1) {
+            if (!out && lane < (STEP ? C : 1)) push_stat<false>(part[parity], crank, lane, b);
+            __syncwarp();
             cluster_arrive();
             cluster_wait();
+            if (joins && !out) b = join_cluster<false>(part[parity], C, lane, P.c);
         }
         if (!joins) continue;
         if (out) {
@@ -473,7 +411,6 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             if (STEP) bar_arrive(kRowStep);
             continue;
         }
-        const Stat b = join_parts<false>(part[parity], C * kScoreWarps, lane, P.c);
         Stat all{max_nan(b.x, l.x), 0.0f, 0.0f};
         {
             Stat r = b;
@@ -551,46 +488,42 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
                                                   __fmul_rn(expf(__fadd_rn(k.rho, -logs_rest)), undo(k.f)))};
             }
         }
+        const uint32_t entries = rounds_with_entries<DT>(L, sb_lo, sb_hi, 1);
         Walk<DT> walk;
-        ShardRow out{};
+        Output<DT> out;
         for (uint32_t sb = sb_lo; sb < sb_hi; ++sb) {
-            if (walk.seek(P, row, sb)) out = shard_row<DT>(P.g[walk.r], P.ldg[walk.r], row, P.col0[walk.r + 1] - P.col0[walk.r]);
-            const uint32_t p0 = walk.place(sb);
+            if (walk.seek(P, row, sb, lane)) out.follow(P, row, walk, lane);
             uint32_t w[16];
             if (!L.some) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = 0;
-                store_superblock<DT>(w, walk.sr, out, p0, lane);
+                out.store(w, P, row, walk, sb, lane);
                 continue;
             }
-            load_superblock<DT>(w, walk.sr, p0, lane);
+            load_superblock<DT>(w, P, row, walk, sb, lane);
             // the listed places' gradients, from their scores before an in-place store takes them
+            const bool any = (entries >> ((sb - sb_lo) & 31)) & 1;
             float listed[kListRegs];
-            bool any = false;
+            if (any) {
 #pragma unroll
-            for (int i = 0; i < kListRegs; ++i) {
-                if (i >= regs) break;
-                const bool mine = (L.place[i] >> S::kLogSb) == sb;
-                any |= mine;
-                if (mine) {
-                    const float x = S::load_one(walk.sr.base + (uint64_t)(L.place[i] - (walk.sb_lo << S::kLogSb)) * S::kBytes);
-                    const float logp = __fadd_rn(__fmaf_rn(x, P.scale, -m), -logs);
-                    listed[i] = x == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(expf(logp), t.Q, -t.q[i]));
+                for (int i = 0; i < kListRegs; ++i) {
+                    listed[i] = 0.0f;
+                    if ((L.place[i] >> S::kLogSb) == sb) {
+                        const float x = S::load_one(walk.shard(P, row).base + (uint64_t)(L.place[i] - (P.sb0[walk.r] << S::kLogSb)) * S::kBytes);
+                        const float logp = __fadd_rn(__fmaf_rn(x, P.scale, -m), -logs);
+                        if (x != neg_inf()) listed[i] = __fmul_rn(g, __fmaf_rn(expf(logp), t.Q, -t.q[i]));
+                    }
                 }
+                __syncwarp();
             }
-            any = __any_sync(~0u, any);
-            if (any) __syncwarp();
             rest_gradient<DT>(w, coef);
-            store_superblock<DT>(w, walk.sr, out, p0, lane);
+            out.store(w, P, row, walk, sb, lane);
             if (any) {
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < kListRegs; ++i) {
-                    if (i >= regs) break;
+                for (int i = 0; i < kListRegs; ++i)
                     if ((L.place[i] >> S::kLogSb) == sb)
-                        S::store_one(out.base + (uint64_t)(L.place[i] - (walk.sb_lo << S::kLogSb) - walk.sr.lo + out.lo) * S::kBytes,
-                                     listed[i]);
-                }
+                        S::store_one(Output<DT>::element(P, row, walk.r, L.place[i] - (P.sb0[walk.r] << S::kLogSb)), listed[i]);
             }
         }
     }

@@ -128,12 +128,13 @@ template <int DT>
 __device__ __forceinline__ uint4 locate_run(const ScoreParams& P, uint64_t row, uint32_t run) {
     using S = Score<DT>;
     Walk<DT> at;
-    at.seek(P, row, run / kSbRuns);
-    const uint32_t place = at.place(run / kSbRuns) + (run % kSbRuns) * 32 * S::VE;
-    const uint64_t a = reinterpret_cast<uint64_t>(at.sr.base) + (uint64_t)place * S::kBytes;
-    const uint32_t lo = place < at.sr.lo ? at.sr.lo - place : 0;
-    const uint32_t hi = place < at.sr.hi ? min(at.sr.hi - place, 32u * S::VE) : 0;
-    return make_uint4((uint32_t)a, (uint32_t)(a >> 32), P.col0[at.r] + place - at.sr.lo, lo | hi << 16);
+    at.seek(P, row, run / kSbRuns, 0);
+    const ShardRow sr = at.shard(P, row);
+    const uint32_t place = at.place(P, run / kSbRuns) + (run % kSbRuns) * 32 * S::VE;
+    const uint64_t a = reinterpret_cast<uint64_t>(sr.base) + (uint64_t)place * S::kBytes;
+    const uint32_t lo = place < sr.lo ? sr.lo - place : 0;
+    const uint32_t hi = place < sr.hi ? min(sr.hi - place, 32u * S::VE) : 0;
+    return make_uint4((uint32_t)a, (uint32_t)(a >> 32), P.col0[at.r] + place - sr.lo, lo | hi << 16);
 }
 // A lane's vector of a run; returns which of its places are in the row (-inf elsewhere).
 template <int DT, int N>
@@ -157,22 +158,18 @@ __device__ __forceinline__ uint32_t load_run(uint32_t (&w)[N], int j, uint4 run,
     return in_row;
 }
 
-// Vectors that reach the bound, waiting for a full warp of them (a ring of 64
-// for each warp).
-struct Waiting {
-    uint4 v;
-    uint32_t col, in_row;
-};
+// Vectors that reach the bound wait for a full warp of them in a ring of 64
+// for each warp, as (run << 5 | lane).
 constexpr int kWaiting = 64;
 
 // Takes batches of the n runs of `at` (in column order; `next` counts what the
 // CTA's warps have taken): appends every score above `bound` and, of those
 // equal to it, the first k that this warp meets.  Counts past the list's end
 // are not stored.  A run has a score or two that reach the bound: its lanes
-// only leave the vectors that do in the ring, and 32 of those are taken apart
-// at a time, a lane each.
+// only note the vectors that do, and 32 of those are taken apart at a time, a
+// lane each.
 template <int DT>
-__device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t bound, int* next, Waiting* ring, uint2* cand,
+__device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t bound, int* next, uint32_t* ring, uint2* cand,
                                         int* n_cand, int lane) {
     using S = Score<DT>;
     constexpr int kBatch = 4;       // runs in flight
@@ -180,14 +177,17 @@ __device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t 
     int ties = 0, head = 0, tail = 0;
     auto take_apart = [&](int count) {
         __syncwarp();
-        const bool mine = lane < count;
-        Waiting t = ring[(head + lane) % kWaiting];
-        if (!mine) t.in_row = 0;
-        const uint32_t v[4] = {t.v.x, t.v.y, t.v.z, t.v.w};
+        uint32_t v[4], in_row = 0, col = 0;
+        if (lane < count) {
+            const uint32_t t = ring[(head + lane) % kWaiting];
+            const uint4 run = at[t >> 5];
+            in_row = load_run<DT>(v, 0, run, t & 31);
+            col = run.z + (t & 31) * S::VE;
+        }
         uint32_t more = 0, same = 0, key[S::VE];
 #pragma unroll
         for (int e = 0; e < S::VE; ++e) {
-            key[e] = (t.in_row >> e) & 1 ? order_key(S::value(S::get(v, 0, e))) : 0;
+            key[e] = (in_row >> e) & 1 ? order_key(S::value(S::get(v, 0, e))) : 0;
             more |= (uint32_t)(key[e] > bound) << e;
             same |= (uint32_t)(key[e] == bound && key[e] != 0) << e;
         }
@@ -210,7 +210,7 @@ __device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t 
 #pragma unroll
             for (int e = 0; e < S::VE; ++e)
                 if ((more >> e) & 1) {
-                    if (to < cap) cand[to] = make_uint2(key[e], t.col + e);
+                    if (to < cap) cand[to] = make_uint2(key[e], col + e);
                     ++to;
                 }
         }
@@ -231,11 +231,9 @@ __device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t 
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (j0 + b >= n) break;
-            const bool hit = in_row[b] != 0 && order_key(S::max_words(&v[4 * b], 4)) >= bound;
+            const bool hit = in_row[b] != 0 && order_key(S::template max_words<4>(&v[4 * b])) >= bound;
             const uint32_t who = __ballot_sync(~0u, hit);
-            if (hit)
-                ring[(tail + __popc(who & ((1u << lane) - 1))) % kWaiting] =
-                    Waiting{make_uint4(v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]), at[j0 + b].z + lane * S::VE, in_row[b]};
+            if (hit) ring[(tail + __popc(who & ((1u << lane) - 1))) % kWaiting] = (uint32_t)(j0 + b) << 5 | lane;
             tail += __popc(who);
             if (tail - head >= 32) take_apart(32);
         }
@@ -316,7 +314,7 @@ __device__ __forceinline__ void rank_list(const uint2* list, int n, int k, int l
 constexpr int kMaxPicked = 192;
 struct TopShared {
     uint4 at[kMaxPicked];           // the picked runs
-    Waiting ring[kScoreWarps + 1][kWaiting];
+    uint32_t ring[kScoreWarps + 1][kWaiting];
     uint32_t picked[kMaxPicked];
     uint32_t bound;
     int n_picked, n_cand, next;
@@ -373,7 +371,7 @@ __device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, uint3
                 if (j0 + b < m) in_row[b] = load_run<DT>(v, b, T.at[j0 + b], lane);
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                if (j0 + b < m) lanes[(j0 + b) * 32 + lane] = in_row[b] ? order_key(S::max_words(&v[4 * b], 4)) : 0;
+                if (j0 + b < m) lanes[(j0 + b) * 32 + lane] = in_row[b] ? order_key(S::template max_words<4>(&v[4 * b])) : 0;
         }
         __syncwarp();
         bound = kth_bound([&](uint32_t i) { return lanes[i]; }, (uint32_t)m * 32, k, lane);
@@ -413,10 +411,11 @@ __device__ __noinline__ void put_top(const ScoreParams& P, uint64_t row, const u
 template <int DT, bool ENT, bool TOP>
 __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_constant__ ScoreParams P) {
     using S = Score<DT>;
-    extern __shared__ __align__(16) uint32_t top_smem[];
-    __shared__ Stat part[2][kMaxScoreCluster * kScoreWarps];       // read by the cluster's first CTA
+    extern __shared__ __align__(16) uint32_t top_smem[];     // TOP: its fixed part, two rows' keys, the candidates
+    __shared__ LaneStats stats[2];
+    __shared__ Stat part[2][kMaxScoreCluster];      // the CTAs' statistics, in the cluster's first CTA
     __shared__ int row_out[2];      // the row is left out
-    TopShared& top = *reinterpret_cast<TopShared*>(top_smem);       // TOP: then two rows' keys, then the candidates
+    TopShared& top = *reinterpret_cast<TopShared*>(top_smem);
     static_assert(sizeof(TopShared) <= kTopSharedBytes, "score_top_smem counts them");
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -435,17 +434,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
     if (warp < kScoreWarps) {
         // ================= the stream =================
         uint32_t w[16];
-        Walk<DT> walk;
-        ShardRow sr{};
-        uint32_t p0 = 0;
-        const uint32_t first = sb_lo + warp;
-        auto fetch = [&](uint32_t (&to)[16], uint64_t r, uint32_t sb) {
-            walk.seek(P, r, sb);
-            sr = walk.sr;
-            p0 = walk.place(sb);
-            load_superblock<DT>(to, sr, p0, lane);
-        };
-        if (row < P.rows && first < sb_hi) fetch(w, row, first);
+        Feed<DT> feed;
+        uint32_t ahead = feed.template start<TOP>(w, P, sb_lo, sb_hi, row, stride, warp, lane);
         bool waited = C == 1, last_out = true;
         int parity = 0;
         uint32_t count = 0;     // this CTA's rows so far
@@ -458,57 +448,33 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
                 waited = true;
             }
             Running run = start_running(P.c);
-            const uint64_t next_row = row + stride;
+            const uint32_t first = first_superblock(sb_lo, warp, count);
             if (out) {
-                walk = Walk<DT>{};
-                if (next_row < P.rows && first < sb_hi) fetch(w, next_row, first);
+                ahead = feed.template drop<TOP>(w, ahead, P, count, warp, lane);
             } else {
-                for (uint32_t sb = first; sb < sb_hi; sb += kScoreWarps) {
-                    uint32_t nx[16];
-                    const ShardRow now = sr;
-                    const uint32_t now_p0 = p0;
-                    if (sb + kScoreWarps < sb_hi) {
-                        fetch(nx, row, sb + kScoreWarps);
-                    } else if (next_row < P.rows) {     // the next row's first, left out or not
-                        walk = Walk<DT>{};
-                        fetch(nx, next_row, first);
-                    }
-                    accumulate<DT, ENT>(run, w, P.c);
-                    if (TOP) {
-                        uint32_t mine = 0;
+                ahead = feed.template each<TOP>(w, ahead, P, first, warp, lane, [&](const uint32_t (&x)[16], uint32_t sb, uint32_t with_scores) {
+                    if constexpr (TOP) {
+                        float top[kSbRuns], mine = quiet_nan();
 #pragma unroll
                         for (int j = 0; j < kSbRuns; ++j) {
-                            uint32_t key = warp_max_u32(order_key(S::max_words(&w[4 * j], 4)));
-                            // a run with no place of the row in it has no score
-                            const uint32_t rp = now_p0 + j * 32 * S::VE;
-                            if (rp + 32 * S::VE <= now.lo || rp >= now.hi) key = 0;
-                            if (lane == j) mine = key;
+                            top[j] = S::template max_words<4>(&x[4 * j]);
+                            const float most = redux_max_nan(top[j]);
+                            if (lane == j) mine = most;
                         }
-                        if (lane < kSbRuns) peer_store(keys_at + (parity * runs + sb * kSbRuns + lane) * 4, mine);
+                        if (lane < kSbRuns)
+                            peer_store(keys_at + (parity * runs + sb * kSbRuns + lane) * 4, lane < with_scores ? order_key(mine) : 0);
+                        accumulate<DT, ENT>(run, x, max_nan(max_nan(top[0], top[1]), max_nan(top[2], top[3])), P.c);
+                    } else {
+                        accumulate<DT, ENT>(run, x, S::template max_words<16>(x), P.c);
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = nx[i];
-                }
+                });
             }
-            Stat a = run.a;
-            if (!out) a = warp_join<ENT>(a, P.c);
-            if (!waited) cluster_wait();
-            if (lane == 0 && !out) {
-                if (C == 1) {
-                    part[parity][warp] = a;
-                } else {
-                    const uint32_t to = peer_address(&part[parity][crank * kScoreWarps + warp], 0);
-                    peer_store(to, __float_as_uint(a.x));
-                    peer_store(to + 4, __float_as_uint(a.s));
-                    peer_store(to + 8, __float_as_uint(a.u));
-                }
-            }
-            __syncwarp();
+            if (!out) stats[parity].template put<ENT>(run.a);
+            bar_arrive(kRowDone + parity);
             if (C > 1) {
+                if (!waited) cluster_wait();
                 cluster_arrive();
-                waited = false;         // for this row's phase: before the next row's stores, or the end
-            } else {
-                bar_arrive(kRowDone + parity);
+                waited = false;         // for this row's phase: before the next one, or the end
             }
             if (TOP && crank == 0) {
                 if (!last_out) {        // the row before: what its runs' readers have left
@@ -519,8 +485,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
                     bar_arrive(kRowHelped);
                 }
                 last_out = out;
-                ++count;
             }
+            ++count;
         }
         if (TOP && !last_out) {
             bar_sync(kRowHelp);
@@ -550,21 +516,22 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
         const long long id_after = id_of(row + 2 * stride);
         float x_id = quiet_nan();
         if (crank == 0 && P.ids && !out && id < (long long)P.vocab) x_id = S::load_one(score_at<DT>(P, row, (uint32_t)id));
-        if (C == 1) {
-            bar_sync(kRowDone + parity);
-        } else {
-            cluster_arrive();
-            cluster_wait();
-        }
+        bar_sync(kRowDone + parity);
         id = id_next;
         id_next = id_after;
-        if (crank != 0) {
-            row_ready(row + 2 * stride, id_after, parity);
-            continue;
-        }
         Stat all{neg_inf(), 0.0f, 0.0f};
+        if (!out) all = stats[parity].template join<ENT>(lane, P.c);
+        if (C > 1) {
+            if (lane == 0 && !out) push_stat<ENT>(part[parity], crank, 0, all);
+            cluster_arrive();
+            cluster_wait();
+            if (crank != 0) {
+                row_ready(row + 2 * stride, id_after, parity);
+                continue;
+            }
+            if (!out) all = join_cluster<ENT>(part[parity], C, lane, P.c);
+        }
         Final f{neg_inf(), 0.0f, 0.0f};
-        if (!out) all = join_parts<ENT>(part[parity], C * kScoreWarps, lane, P.c);
         bool fits = true;
         if (TOP && !out) {
             fits = pick_runs<DT>(P, row, count, keys + parity * runs, runs, cand, top, lane);
@@ -641,22 +608,21 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_grad_kernel(const __grid_
             }
         }
         Walk<DT> walk;
-        ShardRow out{};
+        Output<DT> out;
         const F2 cc = f2(ref.c, ref.c), off = f2(-ref.ref, -ref.ref), a2 = f2(A, A), b2 = f2(B, B);
         for (uint32_t sb = sb_lo; sb < sb_hi; ++sb) {
-            if (walk.seek(P, row, sb)) out = shard_row<DT>(P.g[walk.r], P.ldg[walk.r], row, P.col0[walk.r + 1] - P.col0[walk.r]);
-            const uint32_t p0 = walk.place(sb);
+            if (walk.seek(P, row, sb, lane)) out.follow(P, row, walk, lane);
             uint32_t w[16];
             if (id < 0) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = 0;
             } else {
-                load_superblock<DT>(w, walk.sr, p0, lane);
+                load_superblock<DT>(w, P, row, walk, sb, lane);
             }
             float g_id = 0.0f;
             const bool has_id = sb == id_sb;
             if (has_id) {       // before an in-place store takes the score
-                const float x = S::load_one(walk.sr.base + (uint64_t)id_place * S::kBytes);
+                const float x = S::load_one(score_at<DT>(P, row, (uint32_t)id));
                 const float t = fmaxf(__fmaf_rn(x, ref.c, -ref.ref), kFarBelow);
                 g_id = x == neg_inf() ? 0.0f : __fmaf_rn(ex2(t), __fmaf_rn(B, t, A), __fmul_rn(P.scale, g_lp));
                 __syncwarp();
@@ -673,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_grad_kernel(const __grid_
                     S::set_pair(w, i, x0, x1);
                 }
             }
-            store_superblock<DT>(w, walk.sr, out, p0, lane);
+            out.store(w, P, row, walk, sb, lane);
             if (has_id) {
                 __syncwarp();
-                if (lane == 0) S::store_one(out.base + (uint64_t)(id_place - walk.sr.lo + out.lo) * S::kBytes, g_id);
+                if (lane == 0) S::store_one(Output<DT>::element(P, row, id_r, id_place), g_id);
             }
         }
     }

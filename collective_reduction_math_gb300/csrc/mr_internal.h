@@ -174,7 +174,7 @@ __host__ __device__ constexpr int score_top_candidates(int k) {
 // Shared memory of the top-k path: its fixed part, a key for each 512-byte run
 // of a row (two rows of them), and the candidates (or, before them, 32 k keys
 // of lanes).
-constexpr size_t kTopSharedBytes = 22 * 1024;
+constexpr size_t kTopSharedBytes = 7 * 1024;
 constexpr size_t score_top_smem(uint32_t runs, int k) {
     return kTopSharedBytes + (size_t)runs * 8 +
            (size_t)(score_top_candidates(k) * 8 > k * 128 ? score_top_candidates(k) * 8 : k * 128);

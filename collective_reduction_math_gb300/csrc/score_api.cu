@@ -19,7 +19,8 @@ using mr::ScoreParams;
 
 constexpr size_t kMostDynamicSmem = 200 * 1024;     // of a CTA's 227 KB, beside its static arrays
 
-constexpr size_t kMostRows = (size_t)1 << 40, kMostStride = (size_t)1 << 40;
+constexpr float kLeastScale = 5.421010862427522e-20f;       // 2^-64
+constexpr size_t kMostRows = (size_t)1 << 36, kMostStride = (size_t)1 << 40;
 
 // A byte range of the call, or (ld > 0) rows of `width` bytes every `ld` bytes from lo.
 struct Span {
@@ -97,8 +98,9 @@ mr_status_t check_scores(Call& c, const void* const* logits, const size_t* ld, v
     if (!logits || (with_grad && !grad)) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: logits or grad pointer array is NULL", w);
     if (vocab < 1 || vocab >= ((size_t)1 << 31))
         return report_error(MR_ERR_INVALID_ARGUMENT, "%s: vocab = %zu is outside [1, 2^31)", w, vocab);
-    if (rows > kMostRows) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: rows = %zu is more than 2^40", w, rows);
-    if (!(scale > 0.0f) || !isfinite(scale)) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: scale must be positive and finite", w);
+    if (rows > kMostRows) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: rows = %zu is more than 2^36", w, rows);
+    if (!(scale >= kLeastScale && scale <= 1.0f / kLeastScale))
+        return report_error(MR_ERR_INVALID_ARGUMENT, "%s: scale must lie in [2^-64, 2^64]", w);
     ScoreParams& P = c.P;
     const size_t b = dtype == MR_BF16 ? 2 : 4;
     c.dtype = dtype;
@@ -164,7 +166,7 @@ mr_status_t per_row(Call& c, const T* p, size_t per, const char* name, bool writ
 // not cross the borders between groups of SMs, and 114 clusters of 4 where
 // 110 fit left the last four to a second wave (loss and gradient of 1140 rows
 // 1.5 times as long).
-int resident_clusters(mr::ScoreKernel kernel, int C, size_t smem) {
+int resident_clusters(int dev, mr::ScoreKernel kernel, int C, size_t smem) {
     struct Known {
         mr::ScoreKernel kernel;
         size_t smem;
@@ -173,8 +175,6 @@ int resident_clusters(mr::ScoreKernel kernel, int C, size_t smem) {
     static Known known[256];
     static int count = 0;
     static std::mutex mutex;
-    int dev = 0;
-    cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lock(mutex);
     for (int i = 0; i < count; ++i)
         if (known[i].kernel == kernel && known[i].smem == smem && known[i].C == C && known[i].dev == dev) return known[i].n;
@@ -208,36 +208,57 @@ struct Plan {
     int C, clusters;
     size_t smem;
 };
+// What a forward kernel takes of shared memory at a cluster size, and the
+// share of the row that it reads twice from beyond it; false: no such choice.
+using Needs = bool (*)(const Call&, int C, int choice, size_t* smem, double* again);
+
 // CTAs per row (a cluster), from the modelled time of the whole call: rounds
 // of rows over the resident clusters, each a CTA's part of a row at its share
 // of the bandwidth and a fixed cost of the row's start and join.
-Plan plan_forward(const Call& c, mr::ScoreKernel kernel, size_t (*smem)(const Call&, int), double passes, double fixed_us,
-                  double join_us) {
+Plan plan_forward(const Call& c, mr::ScoreKernel kernel, Needs needs, double passes, double fixed_us, double join_us) {
     Plan best{0, 1, 0};
     double best_us = 1e300;
+    int dev = 0;
+    cudaGetDevice(&dev);
     for (int C = 1; C <= mr::kMaxScoreCluster; C *= 2) {
         if (C > 1 && (uint32_t)C * mr::kThreads / 32 > c.nsb + 7) break;        // a superblock for every warp
-        const size_t bytes = smem(c, C);
-        if (bytes > kMostDynamicSmem) continue;
-        const int clusters = resident_clusters(kernel, C, bytes);
-        if (clusters < 1) continue;
-        const double rounds = ceil((double)c.rows / clusters);
-        const double active = std::min<double>(clusters, c.rows) * C;
-        const double gbs = std::min(45.0, 6600.0 / active);
-        const double us = rounds * ((double)c.nsb * mr::kSuperblockBytes * passes / C / (gbs * 1e3) + fixed_us + (C == 1 ? 0.0 : join_us));
-        if (us < best_us) {
-            best_us = us;
-            best = {C, clusters, bytes};
+        size_t bytes = 0;
+        double again = 0.0;
+        for (int choice = 0; needs(c, C, choice, &bytes, &again); ++choice) {
+            if (bytes > kMostDynamicSmem) continue;
+            const int clusters = resident_clusters(dev, kernel, C, bytes);
+            if (clusters < 1) continue;
+            const double rounds = ceil((double)c.rows / clusters);
+            const double active = std::min<double>(clusters, c.rows) * C;
+            const double gbs = std::min(45.0, 6600.0 / active);
+            const double us = rounds * ((double)c.nsb * mr::kSuperblockBytes * (passes + again) / C / (gbs * 1e3) + fixed_us +
+                                        (C == 1 ? 0.0 : join_us));
+            if (us < best_us) {
+                best_us = us;
+                best = {C, clusters, bytes};
+            }
         }
     }
     return best;
 }
 
-size_t plain_smem(const Call&, int) { return 0; }
-size_t top_smem(const Call& c, int) { return mr::score_top_smem(c.nsb * mr::kSbRuns, c.P.top_k); }
-size_t step_smem(const Call& c, int C) {
-    const uint32_t rounds = ((c.nsb + C - 1) / C + mr::kThreads / 32 - 1) / (mr::kThreads / 32);
-    return (size_t)rounds * mr::kStepRoundBytes;
+bool plain_needs(const Call&, int, int choice, size_t* smem, double*) {
+    *smem = 0;
+    return choice == 0;
+}
+bool top_needs(const Call& c, int, int choice, size_t* smem, double*) {
+    *smem = mr::score_top_smem(c.nsb * mr::kSbRuns, c.P.top_k);
+    return choice == 0;
+}
+// The CTA's part of a row, or all but its last round, which may hold a
+// superblock or two and keep a third CTA off the SM.
+bool step_needs(const Call& c, int C, int choice, size_t* smem, double* again) {
+    const uint32_t warps = mr::kThreads / 32, part = (c.nsb + C - 1) / C;
+    const uint32_t rounds = (part + warps - 1) / warps, kept = rounds - (uint32_t)choice;
+    if (choice > 1 || kept < 1) return false;
+    *smem = kept * mr::kStepRoundBytes;
+    *again = part > kept * warps ? (double)(part - kept * warps) / part : 0.0;
+    return true;
 }
 
 // Warps per row of an elementwise kernel, and the grid.
@@ -291,12 +312,14 @@ mr_status_t run_forward(Call& c, mr::ScoreKernel kernel, const Plan& plan, void*
 
 mr_status_t run_distill(Call& c, bool step, void* stream) {
     const mr::ScoreKernel kernel = mr::distill_forward(c.dtype, step);
-    Plan plan = plan_forward(c, kernel, step ? step_smem : plain_smem, step ? 2.0 : 1.0, 1.0, 1.0);
+    Plan plan = plan_forward(c, kernel, step ? step_needs : plain_needs, step ? 2.0 : 1.0, 1.0, 1.0);
     if (plan.C == 0) {
         // no GPU to ask, or a row too long for sixteen CTAs' shared memory:
         // what does not fit is read again
         plan = {step ? mr::kMaxScoreCluster : 1, 1, step ? 4 * mr::kStepRoundBytes : 0};
-        plan.clusters = std::max(1, resident_clusters(kernel, plan.C, plan.smem));
+        int dev = 0;
+        cudaGetDevice(&dev);
+        plan.clusters = std::max(1, resident_clusters(dev, kernel, plan.C, plan.smem));
     }
     c.P.cache_rounds = (uint32_t)(plan.smem / mr::kStepRoundBytes);
     return run_forward(c, kernel, plan, stream);
@@ -337,8 +360,8 @@ mr_status_t mr_logprob(const void* const* logits, const size_t* ld, int W, size_
     c.P.top_ids = top_ids;
     c.P.top_logprob = top_logprob;
     const mr::ScoreKernel kernel = mr::logprob_forward(c.P, dtype);
-    Plan plan = plan_forward(c, kernel, top_k ? top_smem : plain_smem, 1.0, 1.0, 1.0);
-    if (plan.C == 0) plan = {1, 1, top_k ? top_smem(c, 1) : 0};       // no GPU to ask: the launch will fail
+    Plan plan = plan_forward(c, kernel, top_k ? top_needs : plain_needs, 1.0, 1.0, 1.0);
+    if (plan.C == 0) plan = {1, 1, top_k ? mr::score_top_smem(c.nsb * mr::kSbRuns, top_k) : 0};       // no GPU to ask: the launch will fail
     return run_forward(c, kernel, plan, stream);
 }
 

@@ -77,6 +77,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// The largest of a warp's values, NaN above all.
+__device__ __forceinline__ float redux_max_nan(float v) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -103,11 +109,20 @@ struct Score<MR_FP32> {
         w[2 * i] = __float_as_uint(a);
         w[2 * i + 1] = __float_as_uint(b);
     }
-    static __device__ __forceinline__ float max_words(const uint32_t* w, int n) {
-        float m = __uint_as_float(w[0]);
+    template <int N>
+    static __device__ __forceinline__ float max_words(const uint32_t* w) {
+        float m[4];
 #pragma unroll
-        for (int i = 1; i < n; ++i) m = max_nan(m, __uint_as_float(w[i]));
-        return m;
+        for (int i = 0; i < 4; ++i) m[i] = __uint_as_float(w[i]);
+#pragma unroll
+        for (int i = 4; i < N; ++i) m[i % 4] = max_nan(m[i % 4], __uint_as_float(w[i]));
+        return max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+    }
+    // The least score that still counts, and a pair of scores no lower than it.
+    static __device__ __forceinline__ uint32_t floor_word(float x) { return __float_as_uint(x); }
+    static __device__ __forceinline__ void floored_pair(const uint32_t (&w)[16], int i, uint32_t least, float& a, float& b) {
+        a = fmaxf(__uint_as_float(w[2 * i]), __uint_as_float(least));
+        b = fmaxf(__uint_as_float(w[2 * i + 1]), __uint_as_float(least));
     }
     static __device__ __forceinline__ float load_one(const char* a) { return *reinterpret_cast<const volatile float*>(a); }
     static __device__ __forceinline__ void store_one(char* a, float v) { *reinterpret_cast<volatile float*>(a) = v; }
@@ -132,11 +147,26 @@ struct Score<MR_BF16> {
     static __device__ __forceinline__ void set_pair(uint32_t (&w)[16], int i, float a, float b) {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
     }
-    static __device__ __forceinline__ float max_words(const uint32_t* w, int n) {
-        uint32_t m = w[0];
+    template <int N>
+    static __device__ __forceinline__ float max_words(const uint32_t* w) {
+        uint32_t m[4];
 #pragma unroll
-        for (int i = 1; i < n; ++i) m = max_nan_bf16x2(m, w[i]);
-        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+        for (int i = 0; i < 4; ++i) m[i] = w[i];
+#pragma unroll
+        for (int i = 4; i < N; ++i) m[i % 4] = max_nan_bf16x2(m[i % 4], w[i]);
+        const uint32_t k = max_nan_bf16x2(max_nan_bf16x2(m[0], m[1]), max_nan_bf16x2(m[2], m[3]));
+        return max_nan(__uint_as_float(k << 16), __uint_as_float(k & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t floor_word(float x) {
+        uint32_t w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(w) : "f"(x));
+        return w;
+    }
+    static __device__ __forceinline__ void floored_pair(const uint32_t (&w)[16], int i, uint32_t least, float& a, float& b) {
+        uint32_t m;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w[i]), "r"(least));
+        a = __uint_as_float(m << 16);
+        b = __uint_as_float(m & 0xffff0000u);
     }
     static __device__ __forceinline__ float load_one(const char* a) {
         return __uint_as_float((uint32_t)*reinterpret_cast<const volatile uint16_t*>(a) << 16);
@@ -201,65 +231,230 @@ __device__ __forceinline__ void load_vector(uint32_t (&w)[N], int j, const Shard
     }
 }
 
-// The superblock at places [p0, p0 + kSb) of a shard row; -inf outside it.
-template <int DT>
-__device__ __forceinline__ void load_superblock(uint32_t (&w)[16], const ShardRow& sr, uint32_t p0, int lane) {
-    using S = Score<DT>;
-    if (p0 >= sr.lo && p0 + (1u << S::kLogSb) <= sr.hi) {
-        const char* a = sr.base + ((uint64_t)p0 + (uint32_t)lane * S::VE) * S::kBytes;
-#pragma unroll
-        for (int j = 0; j < kSbVectors; ++j) load16(&w[4 * j], a + j * 512);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kSbVectors; ++j) load_vector<DT>(w, j, sr, p0 + (uint32_t)(j * 32 + lane) * S::VE);
-    }
-}
-
-// Stores the superblock's words at the same places of the output's shard row
-// (`out` starts its row at the same column; its own distance to a 16-byte
-// boundary may differ, and then every element is stored by itself).
-template <int DT>
-__device__ __forceinline__ void store_superblock(const uint32_t (&w)[16], const ShardRow& in, const ShardRow& out, uint32_t p0, int lane) {
-    using S = Score<DT>;
-    if (in.lo == out.lo && p0 >= in.lo && p0 + (1u << S::kLogSb) <= in.hi) {
-        char* a = out.base + ((uint64_t)p0 + (uint32_t)lane * S::VE) * S::kBytes;
-#pragma unroll
-        for (int j = 0; j < kSbVectors; ++j) store16(a + j * 512, &w[4 * j]);
-    } else {
-        char* row = out.base + (int64_t)((int)out.lo - (int)in.lo) * S::kBytes;    // place 0 of `in`, in the output
-#pragma unroll
-        for (int j = 0; j < kSbVectors; ++j) {
-            const uint32_t p = p0 + (uint32_t)(j * 32 + lane) * S::VE;
-            if (in.lo == out.lo && p >= in.lo && p + S::VE <= in.hi) {
-                store16(row + (uint64_t)p * S::kBytes, &w[4 * j]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < S::VE; ++e)
-                    if (p + e >= in.lo && p + e < in.hi) S::store_bits(row + (uint64_t)(p + e) * S::kBytes, S::get(w, j, e));
-            }
-        }
-    }
-}
-
 // ---- the walk over a row's superblocks (ordinals count through the shards) ----
+// Few registers: what only the ends of a shard row need is worked out there.
 template <int DT>
 struct Walk {
-    int r = -1;                 // current shard
-    uint32_t sb_lo = 0, sb_hi = 0;
-    ShardRow sr{};
+    int r = -1;                     // current shard,
+    uint32_t sb_hi = 0;             // the end of its superblocks,
+    uint32_t in_lo = 0, in_n = 0;   // and those that lie in its row from end to end
+    const char* at = nullptr;       // superblock sb's vector of this lane is at at + sb * kSuperblockBytes
+    __device__ __forceinline__ ShardRow shard(const ScoreParams& P, uint64_t row) const {
+        return shard_row<DT>(P.x[r], P.ld[r], row, P.col0[r + 1] - P.col0[r]);
+    }
     // Moves to the shard of superblock sb (ascending within a row).
-    __device__ __forceinline__ bool seek(const ScoreParams& P, uint64_t row, uint32_t sb) {
+    __device__ __forceinline__ bool seek(const ScoreParams& P, uint64_t row, uint32_t sb, int lane) {
         if (sb < sb_hi) return false;
         do {
             ++r;
             sb_hi = P.sb0[r + 1];
         } while (sb >= sb_hi);
-        sb_lo = P.sb0[r];
-        sr = shard_row<DT>(P.x[r], P.ld[r], row, P.col0[r + 1] - P.col0[r]);
+        const uint32_t sb_lo = P.sb0[r];
+        const ShardRow sr = shard(P, row);
+        in_lo = sb_lo + (sr.lo != 0);
+        const uint32_t whole = sr.hi >> Score<DT>::kLogSb;      // from the shard's first on
+        in_n = whole > (sr.lo != 0) ? whole - (sr.lo != 0) : 0;
+        at = sr.base + lane * 16 - (int64_t)sb_lo * kSuperblockBytes;
         return true;
     }
-    __device__ __forceinline__ uint32_t place(uint32_t sb) const { return (sb - sb_lo) << Score<DT>::kLogSb; }
+    __device__ __forceinline__ uint32_t place(const ScoreParams& P, uint32_t sb) const { return (sb - P.sb0[r]) << Score<DT>::kLogSb; }
+    __device__ __forceinline__ bool inside(uint32_t sb) const { return sb - in_lo < in_n; }
+    __device__ __forceinline__ const char* address(uint32_t sb) const { return at + (uint64_t)sb * kSuperblockBytes; }
+    // How many of the superblock's runs hold a place of the row.
+    __device__ __forceinline__ uint32_t runs(const ScoreParams& P, uint64_t row, uint32_t sb) const {
+        using S = Score<DT>;
+        if (inside(sb)) return kSbRuns;
+        const uint32_t p0 = place(P, sb), hi = shard(P, row).hi;
+        return p0 >= hi ? 0 : min((hi - p0 + 32 * S::VE - 1) / (32 * S::VE), (uint32_t)kSbRuns);
+    }
 };
+
+// The superblock the walk stands at; -inf outside the row.
+template <int DT>
+__device__ __forceinline__ void load_superblock(uint32_t (&w)[16], const ScoreParams& P, uint64_t row, const Walk<DT>& walk, uint32_t sb,
+                                                int lane) {
+    using S = Score<DT>;
+    if (walk.inside(sb)) {
+        const char* a = walk.address(sb);
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) load16(&w[4 * j], a + j * 512);
+    } else {
+        const ShardRow sr = walk.shard(P, row);
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) load_vector<DT>(w, j, sr, walk.place(P, sb) + (uint32_t)(j * 32 + lane) * S::VE);
+    }
+}
+
+// The gradients' buffer of the shard the walk stands at.
+template <int DT>
+struct Output {
+    char* at = nullptr;         // as the walk's, where both rows start at the same distance from a 16-byte boundary
+    bool alike = false;
+    __device__ __forceinline__ static ShardRow shard(const ScoreParams& P, uint64_t row, int r) {
+        return shard_row<DT>(P.g[r], P.ldg[r], row, P.col0[r + 1] - P.col0[r]);
+    }
+    __device__ __forceinline__ void follow(const ScoreParams& P, uint64_t row, const Walk<DT>& walk, int lane) {
+        const ShardRow sr = shard(P, row, walk.r);
+        alike = sr.lo == walk.shard(P, row).lo;
+        at = sr.base + lane * 16 - (int64_t)P.sb0[walk.r] * kSuperblockBytes;
+    }
+    // the element at a place of the walk's shard row
+    __device__ __forceinline__ static char* element(const ScoreParams& P, uint64_t row, int r, uint32_t place) {
+        const uint32_t lo = shard_row<DT>(P.x[r], P.ld[r], row, 0).lo;
+        return static_cast<char*>(P.g[r]) + (row * P.ldg[r] + (place - lo)) * Score<DT>::kBytes;
+    }
+    // Stores a superblock's words; element by element at the row's ends, and
+    // everywhere where the two rows are not alike.
+    __device__ __forceinline__ void store(const uint32_t (&w)[16], const ScoreParams& P, uint64_t row, const Walk<DT>& walk, uint32_t sb,
+                                          int lane) const {
+        using S = Score<DT>;
+        if (alike && walk.inside(sb)) {
+            char* a = at + (uint64_t)sb * kSuperblockBytes;
+#pragma unroll
+            for (int j = 0; j < kSbVectors; ++j) store16(a + j * 512, &w[4 * j]);
+        } else {
+            const ShardRow in = walk.shard(P, row), out = shard(P, row, walk.r);
+            char* const place0 = out.base + ((int64_t)out.lo - in.lo) * S::kBytes;
+#pragma unroll
+            for (int j = 0; j < kSbVectors; ++j) {
+                const uint32_t p = walk.place(P, sb) + (uint32_t)(j * 32 + lane) * S::VE;
+                if (alike && p >= in.lo && p + S::VE <= in.hi) {
+                    store16(place0 + (uint64_t)p * S::kBytes, &w[4 * j]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < S::VE; ++e)
+                        if (p + e >= in.lo && p + e < in.hi) S::store_bits(place0 + (uint64_t)(p + e) * S::kBytes, S::get(w, j, e));
+                }
+            }
+        }
+    }
+};
+
+// Which superblocks of its CTA's part [sb_lo, sb_hi) a warp takes of the
+// CTA's count-th row: every 8th, from a start that moves on by one a row, so
+// that the odd ones do not always fall to the same warps.
+__device__ __forceinline__ uint32_t first_superblock(uint32_t sb_lo, int warp, uint32_t count) {
+    return sb_lo + ((warp + count) & (kScoreWarps - 1));
+}
+
+// A warp's loads over all its rows, one superblock ahead of what it works on
+// and through the ends of rows.  (Three ahead, through shared memory, was
+// slower: 8192 x 131072 bf16 361 us against 352, and 189 against 169 for the
+// distillation loss of half of it: the kernels are bound by their
+// instructions as much as by memory.)
+template <int DT>
+struct Feed {
+    uint32_t sb_lo, sb_hi;
+    uint64_t row0, stride;      // the CTA's rows
+    uint32_t count, rows;       // of the next superblock to load, and how many there are
+    uint32_t sb;
+    Walk<DT> walk;
+
+    __device__ __forceinline__ uint64_t row() const { return row0 + count * stride; }
+    __device__ __forceinline__ void next_row(int warp) {
+        do {
+            ++count;
+            sb = first_superblock(sb_lo, warp, count);
+        } while (count < rows && sb >= sb_hi);
+        walk = Walk<DT>{};
+    }
+    // Loads the next superblock.  RUNS: returns how many of its runs hold a place of the row.
+    template <bool RUNS>
+    __device__ __forceinline__ uint32_t load(uint32_t (&w)[16], const ScoreParams& P, int warp, int lane) {
+        if (count >= rows) return 0;
+        walk.seek(P, row(), sb, lane);
+        load_superblock<DT>(w, P, row(), walk, sb, lane);
+        const uint32_t runs = RUNS ? walk.runs(P, row(), sb) : 0;
+        sb += kScoreWarps;
+        if (sb >= sb_hi) next_row(warp);
+        return runs;
+    }
+    template <bool RUNS>
+    __device__ __forceinline__ uint32_t start(uint32_t (&w)[16], const ScoreParams& P, uint32_t lo, uint32_t hi, uint64_t first_row,
+                                              uint64_t row_stride, int warp, int lane) {
+        sb_lo = lo;
+        sb_hi = hi;
+        row0 = first_row;
+        stride = row_stride;
+        rows = first_row < P.rows ? (uint32_t)((P.rows - first_row + row_stride - 1) / row_stride) : 0;
+        count = 0;
+        sb = first_superblock(lo, warp, 0);
+        if (sb >= sb_hi && rows) next_row(warp);
+        return load<RUNS>(w, P, warp, lane);
+    }
+    // Drops the count-th row, which is left out and whose first superblock (if it has one) is in w.
+    template <bool RUNS>
+    __device__ __forceinline__ uint32_t drop(uint32_t (&w)[16], uint32_t runs, const ScoreParams& P, uint32_t of, int warp, int lane) {
+        if (count == of) next_row(warp);
+        return first_superblock(sb_lo, warp, of) < sb_hi ? load<RUNS>(w, P, warp, lane) : runs;
+    }
+    // Gives work(w, sb, runs) a row's superblocks; on entry and on return w
+    // holds the next one.  Two in turn, so that none is moved between registers.
+    template <bool RUNS, class Work>
+    __device__ __forceinline__ uint32_t each(uint32_t (&w)[16], uint32_t runs, const ScoreParams& P, uint32_t first, int warp, int lane,
+                                             Work work) {
+        for (uint32_t s = first; s < sb_hi; s += 2 * kScoreWarps) {
+            uint32_t x[16];
+            const uint32_t more = load<RUNS>(x, P, warp, lane);
+            work(w, s, runs);
+            if (s + kScoreWarps < sb_hi) {
+                runs = load<RUNS>(w, P, warp, lane);
+                work(x, s + kScoreWarps, more);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = x[i];
+                runs = more;
+            }
+        }
+        return runs;
+    }
+};
+
+// ---- superblocks in shared memory ----
+// A warp's superblock takes 2 KiB, in the order of its places: vector j of
+// lane l at 16-byte slot 32 j + l.  Each lane copies and reads back its own
+// slots, so no barrier is needed; another lane's slot may be touched between
+// two __syncwarp once its copy is there.
+__device__ __forceinline__ void copy16(uint32_t to, const char* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// Begins to copy the superblock the walk stands at: whole vectors
+// asynchronously, the row's ends element by element, -inf outside the row.
+template <int DT>
+__device__ __forceinline__ void begin_copy(uint4* block, const ScoreParams& P, uint64_t row, const Walk<DT>& walk, uint32_t sb, int lane) {
+    using S = Score<DT>;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(block + lane);
+    const char* from = walk.address(sb);
+    if (walk.inside(sb)) {
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) copy16(to + j * 512, from + j * 512);
+    } else {
+        const ShardRow sr = walk.shard(P, row);
+#pragma unroll
+        for (int j = 0; j < kSbVectors; ++j) {
+            const uint32_t p = walk.place(P, sb) + (uint32_t)(j * 32 + lane) * S::VE;
+            if (p >= sr.lo && p + S::VE <= sr.hi) {
+                copy16(to + j * 512, from + j * 512);
+            } else {
+                uint32_t v[4];
+                load_vector<DT>(v, 0, sr, p);
+                block[j * 32 + lane] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    }
+}
+__device__ __forceinline__ void read_block(uint32_t (&w)[16], const uint4* block, int lane) {
+#pragma unroll
+    for (int j = 0; j < kSbVectors; ++j) {
+        const uint4 v = block[j * 32 + lane];
+        w[4 * j] = v.x;
+        w[4 * j + 1] = v.y;
+        w[4 * j + 2] = v.z;
+        w[4 * j + 3] = v.w;
+    }
+}
 
 // The shard that holds column c (an fp32 estimate and a short walk).
 __device__ __forceinline__ int shard_of(const ScoreParams& P, uint32_t c) {
@@ -276,11 +471,30 @@ __device__ __forceinline__ const char* score_at(const ScoreParams& P, uint64_t r
     return static_cast<const char*>(P.x[r]) + (row * P.ld[r] + (c - P.col0[r])) * Score<DT>::kBytes;
 }
 
+// ---- thread-block clusters ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void peer_store(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // ---- running softmax statistics ----
 struct Stat {
     float x, s, u;
 };
 constexpr float kLn2 = 0.69314718055994531f;
+
+constexpr float kFlatRef = 2147483648.0f;
 
 // The reference that exponents are made against: c x - ref, off by r for every x.
 struct Ref {
@@ -292,7 +506,7 @@ __device__ __forceinline__ Ref reference(float x, float c) {
         f.ref = 0.0f;
         return f;
     }
-    if (!(fabsf(f.ref) < 2147483648.0f)) {
+    if (!(fabsf(f.ref) < kFlatRef)) {
         const uint32_t e = (__float_as_uint(x) >> 23) & 255;      // 2^(30 - exponent of x)
         f.c = __uint_as_float(min(284u - e, 254u) << 23);
         f.ref = __fmul_rn(x, f.c);
@@ -316,32 +530,44 @@ __device__ __forceinline__ void rebase(Stat& a, float X, float c) {
     a.x = X;
 }
 
-// A thread's running state.
+// A thread's running state.  For the entropy, scores are taken no lower than
+// `least`, some 1000 below the maximum in the exponent: their terms are 0 all
+// the same, and 0 * -inf (a mask) would be NaN.  One instruction a pair of
+// bf16 scores; on the exponents it takes two.  `flat`: the reference is so
+// large that every term is 1 or 0 and u gets nothing.
 struct Running {
     Stat a;
     Ref f;
+    uint32_t least;
+    bool flat;
 };
-__device__ __forceinline__ Running start_running(float c) { return {{neg_inf(), 0.0f, 0.0f}, {c, 0.0f, 0.0f}}; }
+__device__ __forceinline__ Running start_running(float c) { return {{neg_inf(), 0.0f, 0.0f}, {c, 0.0f, 0.0f}, 0xff7fff7fu, true}; }
 
-// One superblock into a thread's state.
+// One superblock, whose largest score (of this lane's) is `top`, into a thread's state.
 template <int DT, bool ENT>
-__device__ __forceinline__ void accumulate(Running& t, const uint32_t (&w)[16], float c) {
+__device__ __forceinline__ void accumulate(Running& t, const uint32_t (&w)[16], float top, float c) {
     using S = Score<DT>;
-    const float top = S::max_words(w, 16);
     if (!(top <= t.a.x)) {      // a new maximum, or NaN
         rebase<ENT>(t.a, top, c);
         t.f = reference(top, c);
+        if (ENT) {
+            t.flat = !(fabsf(__fmul_rn(top, c)) < kFlatRef);
+            // 1000 in the exponent or, for the rounding to the type, 1/64 of the maximum
+            t.least = S::floor_word(__fadd_rn(top, -fmaxf(__fdiv_rn(1000.0f, c), fabsf(top) * 0.015625f)));
+        }
     }
     const F2 cc = f2(t.f.c, t.f.c), off = f2(-t.f.ref, -t.f.ref);
     F2 s = f2(0.0f, 0.0f), u = s;
 #pragma unroll
     for (int i = 0; i < S::kPairs; ++i) {
         float x0, x1, t0, t1;
-        S::pair(w, i, x0, x1);
-        unpack(fma2(f2(x0, x1), cc, off), t0, t1);
+        if (ENT) S::floored_pair(w, i, t.least, x0, x1);
+        else S::pair(w, i, x0, x1);
+        const F2 x = fma2(f2(x0, x1), cc, off);
+        unpack(x, t0, t1);
         const F2 e = f2(ex2(t0), ex2(t1));
         s = add2(s, e);
-        if (ENT) u = fma2(e, f2(fmaxf(t0, kFarBelow), fmaxf(t1, kFarBelow)), u);
+        if (ENT) u = fma2(e, x, u);
     }
     float p, q;
     unpack(s, p, q);
@@ -349,7 +575,8 @@ __device__ __forceinline__ void accumulate(Running& t, const uint32_t (&w)[16], 
     t.a.s = __fmaf_rn(sum, k, t.a.s);
     if (ENT) {
         unpack(u, p, q);
-        t.a.u = __fmaf_rn(__fmaf_rn(-t.f.r, sum, __fadd_rn(p, q)), k, t.a.u);
+        const float more = __fmul_rn(__fmaf_rn(-t.f.r, sum, __fadd_rn(p, q)), k);
+        if (!t.flat) t.a.u = __fadd_rn(t.a.u, more);
     }
 }
 
@@ -363,25 +590,12 @@ __device__ __forceinline__ float warp_max_nan(float v) {
     for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, o));
     return v;
 }
-// Joins the statistics of a warp's lanes; every lane gets the result.
-template <bool ENT>
-__device__ __forceinline__ Stat warp_join(Stat a, float c) {
-    rebase<ENT>(a, warp_max_nan(a.x), c);
-    a.s = warp_sum(a.s);
-    if (ENT) a.u = warp_sum(a.u);
-    return a;
-}
-// Joins the statistics of a row's warps (one warp; every lane gets the result).
-template <bool ENT>
-__device__ __forceinline__ Stat join_parts(const Stat* part, int n, int lane, float c) {
-    constexpr int kEach = kMaxScoreCluster * kScoreWarps / 32;
-    Stat o[kEach];
-    float X = neg_inf();
+// Joins `each` statistics of every lane of a warp; all lanes get the result.
+template <bool ENT, int kEach>
+__device__ __forceinline__ Stat warp_join(Stat (&o)[kEach], float c) {
+    float X = o[0].x;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        o[i] = lane + 32 * i < n ? part[lane + 32 * i] : Stat{neg_inf(), 0.0f, 0.0f};
-        X = max_nan(X, o[i].x);
-    }
+    for (int i = 1; i < kEach; ++i) X = max_nan(X, o[i].x);
     X = warp_max_nan(X);
     Stat b{X, 0.0f, 0.0f};
 #pragma unroll
@@ -393,6 +607,38 @@ __device__ __forceinline__ Stat join_parts(const Stat* part, int n, int lane, fl
     b.s = warp_sum(b.s);
     if (ENT) b.u = warp_sum(b.u);
     return b;
+}
+// The stream's threads leave their statistics of a row here, and the row warp
+// joins them: a join in every warp first is three times the instructions and
+// keeps the stream waiting for its shuffles.
+struct LaneStats {
+    float x[kThreads], s[kThreads], u[kThreads];
+    template <bool ENT>
+    __device__ __forceinline__ void put(const Stat& a) {
+        x[threadIdx.x] = a.x;
+        s[threadIdx.x] = a.s;
+        if (ENT) u[threadIdx.x] = a.u;
+    }
+    template <bool ENT>
+    __device__ __forceinline__ Stat join(int lane, float c) const {
+        Stat o[kScoreWarps];
+#pragma unroll
+        for (int i = 0; i < kScoreWarps; ++i) o[i] = {x[32 * i + lane], s[32 * i + lane], ENT ? u[32 * i + lane] : 0.0f};
+        return warp_join<ENT>(o, c);
+    }
+};
+// The cluster's CTAs' statistics, pushed by their row warps.
+template <bool ENT>
+__device__ __forceinline__ Stat join_cluster(const Stat* part, int C, int lane, float c) {
+    Stat o[1] = {lane < C ? part[lane] : Stat{neg_inf(), 0.0f, 0.0f}};
+    return warp_join<ENT>(o, c);
+}
+template <bool ENT>
+__device__ __forceinline__ void push_stat(Stat* part, int crank, int to_rank, const Stat& a) {
+    const uint32_t to = peer_address(&part[crank], to_rank);
+    peer_store(to, __float_as_uint(a.x));
+    peer_store(to + 4, __float_as_uint(a.s));
+    if (ENT) peer_store(to + 8, __float_as_uint(a.u));
 }
 
 // What m = scale * x lost in its rounding; 0 where a whole unit and more is
@@ -465,23 +711,7 @@ __device__ __forceinline__ SavedRef saved_reference(float m, float scale, float 
     return k;
 }
 
-// ---- thread-block clusters and barriers inside a CTA ----
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void peer_store(uint32_t a, uint32_t v) {
-    asm volatile("st.shared::cluster.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
+// ---- barriers inside a CTA ----
 // The forward kernels' CTAs: 8 warps that stream a row's scores and one warp
 // that does everything else of it.  That warp fetches the next rows' ids and
 // lists ahead of the stream, and joins the statistics of a row while the

@@ -258,7 +258,7 @@ mr_status_t mr_reduce_scatter_ex(const void* const* send, void* const* recv, int
  *     A rank with no column (vocab < W) is never looked at.
  *   dtype: MR_FP32 or MR_BF16 (MR_INT32 returns MR_ERR_UNSUPPORTED);
  *     1 <= vocab < 2^31; rows == 0 is a no-op.
- *   y = scale * x (scale positive and finite: 1 / temperature), in fp32; all
+ *   y = scale * x (1 / temperature, in [2^-64, 2^64]), in fp32; all
  *     sums are fp32 over a fixed split of the row, the same on every run;
  *     results in dtype are rounded once.
  *   -inf is a masked place: it has no part in any sum and gradient 0.  A row
