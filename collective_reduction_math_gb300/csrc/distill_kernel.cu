@@ -28,61 +28,66 @@ namespace {
 constexpr int kListRegs = MR_MAX_TEACHER / 32;
 constexpr uint32_t kNoPlace = ~0u;     // past every superblock: a row has fewer than 2^32 - 2^10 places
 
-// A warp's copy of a row's list: entry k = lane + 32 i.
+// A warp's copy of a row's list: entry k = lane + 32 i, in the first `regs` of
+// the four registers.  Every instruction here is one of the warp that the
+// stream waits for, or of a unit of the gradient's: what a list shorter than
+// 97 entries does not need is skipped, and what two steps share is kept.
 struct List {
     uint32_t place[kListRegs];      // in units of scores, counted through the row's superblocks; kNoPlace if absent
     float v[kListRegs];             // the teacher's value; -inf if absent, NaN for a column past the vocabulary
     bool some;                      // any entry at all
 };
+template <class F>
+__device__ __forceinline__ void each_reg(int regs, F f) {
+#pragma unroll
+    for (int i = 0; i < kListRegs; ++i)
+        if (i < regs) f(i);
+}
 
 // The list as it lies in memory.
 struct RawList {
     long long id[kListRegs];
     float v[kListRegs];
 };
-__device__ __forceinline__ void load_raw(RawList& R, const ScoreParams& P, uint64_t row, int lane) {
-#pragma unroll
-    for (int i = 0; i < kListRegs; ++i) {
-        const int k = lane + 32 * i;
+__device__ __forceinline__ void load_raw(RawList& R, const ScoreParams& P, uint64_t row, int regs, int lane) {
+    const long long* ids = P.t_ids + row * P.K + lane;
+    const float* val = P.t_val + row * P.K + lane;
+    each_reg(regs, [&](int i) {
         R.id[i] = -1;
         R.v[i] = neg_inf();
-        if (k < P.K) {
-            R.id[i] = P.t_ids[row * P.K + k];
-            R.v[i] = P.t_val[row * P.K + k];
+        if (lane + 32 * i < P.K) {
+            R.id[i] = ids[32 * i];
+            R.v[i] = val[32 * i];
         }
-    }
+    });
 }
-template <int DT>
-__device__ __forceinline__ void place_list(List& L, const RawList& R, const ScoreParams& P, uint64_t row, int regs) {
+// Places, values, and by entry(i, score's address, rank, column of the rank)
+// whatever else is to be had of an entry.
+template <int DT, class Entry>
+__device__ __forceinline__ void place_list(List& L, const RawList& R, const ScoreParams& P, uint64_t row, int regs, Entry entry) {
     using S = Score<DT>;
     bool some = false;
 #pragma unroll
     for (int i = 0; i < kListRegs; ++i) {
         L.place[i] = kNoPlace;
         L.v[i] = neg_inf();
-        const long long id = i < regs ? R.id[i] : -1;
-        if (id >= 0) {
+    }
+    each_reg(regs, [&](int i) {
+        if (R.id[i] >= 0) {
             some = true;
-            L.v[i] = id < (long long)P.vocab ? R.v[i] : quiet_nan();
-            if (id < (long long)P.vocab) {
-                const int r = shard_of(P, (uint32_t)id);
-                const ShardRow sr = shard_row<DT>(P.x[r], P.ld[r], row, 0);
-                L.place[i] = (P.sb0[r] << S::kLogSb) + ((uint32_t)id - P.col0[r] + sr.lo);
+            L.v[i] = quiet_nan();
+            if (R.id[i] < (long long)P.vocab) {
+                const uint32_t id = (uint32_t)R.id[i];
+                const int r = shard_of(P, id);
+                const uint32_t column = id - P.col0[r];
+                const uintptr_t start = reinterpret_cast<uintptr_t>(P.x[r]) + row * P.ld[r] * S::kBytes;
+                L.v[i] = R.v[i];
+                L.place[i] = (P.sb0[r] << S::kLogSb) + column + (uint32_t)(start & 15) / S::kBytes;
+                entry(i, reinterpret_cast<const char*>(start + (uint64_t)column * S::kBytes), r, column);
             }
         }
-    }
+    });
     L.some = __any_sync(~0u, some);
-}
-
-// The score at a place.
-template <int DT>
-__device__ __forceinline__ float listed_score(const ScoreParams& P, uint64_t row, uint32_t place) {
-    using S = Score<DT>;
-    int r = 0;
-    const uint32_t sb = place >> S::kLogSb;
-    while (sb >= P.sb0[r + 1]) ++r;
-    const ShardRow sr = shard_row<DT>(P.x[r], P.ld[r], row, 0);
-    return S::load_one(sr.base + (uint64_t)(place - (P.sb0[r] << S::kLogSb)) * S::kBytes);
 }
 
 // The teacher's side of a row.
@@ -90,42 +95,39 @@ struct Teacher {
     float q[kListRegs], logq[kListRegs];
     float q_rest, Q;
 };
-__device__ __forceinline__ void teacher_mass(Teacher& t, const List& L, const ScoreParams& P) {
+__device__ __forceinline__ void teacher_mass(Teacher& t, const List& L, const ScoreParams& P, int regs) {
     float total = 0.0f;
     if (P.tail) {
-#pragma unroll
-        for (int i = 0; i < kListRegs; ++i) {
+        each_reg(regs, [&](int i) {
             t.logq[i] = L.v[i];
-            t.q[i] = expf(L.v[i]);
+            t.q[i] = exp_near(L.v[i]);
             total = __fadd_rn(total, t.q[i]);
-        }
+        });
         const float rest = __fadd_rn(1.0f, -warp_sum(total));
         t.q_rest = rest < 0.0f ? 0.0f : rest;
         t.Q = rest < 0.0f ? __fadd_rn(1.0f, -rest) : rest == rest ? 1.0f : rest;
     } else {
         float m = neg_inf();
-#pragma unroll
-        for (int i = 0; i < kListRegs; ++i) {
+        each_reg(regs, [&](int i) {
             t.logq[i] = __fmul_rn(L.v[i], P.teacher_scale);
             m = max_nan(m, t.logq[i]);
-        }
-        m = warp_max_nan(m);
+        });
+        m = redux_max_nan(m);
         const float ref = m == neg_inf() ? 0.0f : m;
-#pragma unroll
-        for (int i = 0; i < kListRegs; ++i) {
+        each_reg(regs, [&](int i) {
             t.logq[i] = __fadd_rn(t.logq[i], -ref);
-            t.q[i] = expf(t.logq[i]);
+            t.q[i] = exp_near(t.logq[i]);
             total = __fadd_rn(total, t.q[i]);
-        }
+        });
         total = warp_sum(total);
-        const float log_total = m == neg_inf() ? 0.0f : logf(total);
-#pragma unroll
-        for (int i = 0; i < kListRegs; ++i) {
+        const bool none = m == neg_inf();
+        const float log_total = none ? 0.0f : logf(total), inv = none ? 0.0f : reciprocal(total);
+        each_reg(regs, [&](int i) {
             t.logq[i] = __fadd_rn(t.logq[i], -log_total);
-            t.q[i] = m == neg_inf() ? 0.0f : __fdiv_rn(t.q[i], total);
-        }
+            t.q[i] = __fmul_rn(t.q[i], inv);
+        });
         t.q_rest = 0.0f;
-        t.Q = m == neg_inf() ? 0.0f : m == m ? 1.0f : m;
+        t.Q = none ? 0.0f : m == m ? 1.0f : m;
     }
 }
 
@@ -210,11 +212,15 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
     using S = Score<DT>;
     extern __shared__ uint4 smem[];         // STEP: this CTA's part of a row, [round][warp] blocks
     __shared__ uint4 bounce[STEP ? 1 : kScoreWarps][STEP ? 1 : kSbVectors * 32];      // a block of each warp
-    __shared__ LaneStats stats[2];
-    __shared__ Stat part[2][kMaxScoreCluster];
+    __shared__ Stat part[2][kMaxScoreCluster];      // the CTAs' statistics
+    __shared__ LaneStats stats[STEP ? 1 : 2];       // from these threads',
+    __shared__ Stat warp_part[2][kScoreWarps];      // or for STEP from these warps'
+    __shared__ float2 step_part[2][kMaxScoreCluster];       // STEP: the CTAs', as x and s,
+    __shared__ uint64_t step_bar[2];                        // and the barriers that count them
     __shared__ uint32_t s_place[2][MR_MAX_TEACHER];
     __shared__ int row_out[2];              // the row is left out
-    __shared__ float s_grad[MR_MAX_TEACHER];        // STEP: the listed places' gradients
+    __shared__ uint32_t s_mask[2][STEP ? MR_MAX_TEACHER : 1];       // STEP: where the entries lie in the cache,
+    __shared__ char* s_out[2][STEP ? MR_MAX_TEACHER : 1];           // and in the gradients of this CTA's part
     __shared__ Coef s_coef;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -224,6 +230,10 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
     const uint64_t stride = gridDim.x / C;
     uint64_t row = blockIdx.x / C;
     const int regs = (P.K + 31) / 32;
+    if (STEP && C > 1 && threadIdx.x == 0) {
+        counted_init(&step_bar[0]);
+        counted_init(&step_bar[1]);
+    }
     if (C > 1) cluster_arrive();        // every CTA of the cluster has started: waited for before the first store to a peer
     pdl_enter();
 
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
         auto block_of = [&](uint32_t round) { return smem + (round * kScoreWarps + warp) * kBlock; };
         auto rounds_of = [&](uint32_t first) { return first < sb_hi ? (sb_hi - first + kScoreWarps - 1) / kScoreWarps : 0; };
         if constexpr (STEP) {
-            const uint32_t first = first_superblock(sb_lo, warp, 0);
+            const uint32_t first = sb_lo + warp;
             if (row < P.rows)
                 for (uint32_t i = 0; i < min(rounds_of(first), P.cache_rounds); ++i) {
                     walk.seek(P, row, first + i * kScoreWarps, lane);
@@ -252,17 +262,20 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
         for (uint32_t count = 0; row < P.rows; row += stride, parity ^= 1, ++count) {
             bar_sync(kRowReady + parity);
             const bool out = row_out[parity];
-            const uint32_t first = first_superblock(sb_lo, warp, count);
+            const uint32_t first = STEP ? sb_lo + warp : first_superblock(sb_lo, warp, count);
             List L;
+            auto take_list = [&] {
 #pragma unroll
-            for (int i = 0; i < kListRegs; ++i) L.place[i] = i < regs ? s_place[parity][lane + 32 * i] : kNoPlace;
-            const uint32_t entries = out ? 0 : rounds_with_entries<DT>(L, first, sb_hi, kScoreWarps);
+                for (int i = 0; i < kListRegs; ++i) L.place[i] = i < regs ? s_place[parity][lane + 32 * i] : kNoPlace;
+            };
             const uint32_t rounds = rounds_of(first), cached = STEP ? min(rounds, P.cache_rounds) : 0;
             Running run = start_running(P.c);
             if constexpr (!STEP) {
                 if (out) {
                     ahead_runs = feed.template drop<false>(w, ahead_runs, P, count, warp, lane);
                 } else {
+                    take_list();
+                    const uint32_t entries = rounds_with_entries<DT>(L, first, sb_hi, kScoreWarps);
                     ahead_runs = feed.template each<false>(w, ahead_runs, P, first, warp, lane, [&](uint32_t (&x)[16], uint32_t sb, uint32_t) {
                         if ((entries >> (((sb - first) / kScoreWarps) & 31)) & 1) mask_listed<DT>(x, L, sb, bounce[warp], lane);
                         accumulate<DT, false>(run, x, S::template max_words<16>(x), P.c);
@@ -271,103 +284,140 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             } else {
                 copies_wait();          // this row's copies are there
                 if (!out) {
+                    // the listed places in this warp's blocks leave the sums
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kListRegs; ++i)
+                        if (i < regs) {
+                            const uint32_t at = s_mask[parity][lane + 32 * i];
+                            if (at >> 28 == (uint32_t)warp) S::mask_one(reinterpret_cast<char*>(smem) + (at & 0xfffffffu));
+                        }
+                    __syncwarp();
                     for (uint32_t i = 0; i < cached; ++i) {
-                        if ((entries >> (i & 31)) & 1) mask_listed<DT>(block_of(i), L, first + i * kScoreWarps);
                         read_block(w, block_of(i), lane);
                         accumulate<DT, false>(run, w, S::template max_words<16>(w), P.c);
                     }
-                    walk = Walk<DT>{};
-                    for (uint32_t i = cached; i < rounds; ++i) {        // a row longer than the cache
-                        const uint32_t sb = first + i * kScoreWarps;
-                        walk.seek(P, row, sb, lane);
-                        load_superblock<DT>(w, P, row, walk, sb, lane);
-                        if ((entries >> (i & 31)) & 1) mask_listed_in_registers<DT>(w, L, sb, lane);
-                        accumulate<DT, false>(run, w, S::template max_words<16>(w), P.c);
+                    if (cached < rounds) {      // a row longer than the cache
+                        take_list();
+                        const uint32_t entries = rounds_with_entries<DT>(L, first, sb_hi, kScoreWarps);
+                        walk = Walk<DT>{};
+                        for (uint32_t i = cached; i < rounds; ++i) {
+                            const uint32_t sb = first + i * kScoreWarps;
+                            walk.seek(P, row, sb, lane);
+                            load_superblock<DT>(w, P, row, walk, sb, lane);
+                            if ((entries >> (i & 31)) & 1) mask_listed_in_registers<DT>(w, L, sb, lane);
+                            accumulate<DT, false>(run, w, S::template max_words<16>(w), P.c);
+                        }
                     }
                 }
             }
-            if (!out) stats[parity].template put<false>(run.a);
+            if (!out) {
+                if constexpr (STEP) {
+                    const Stat a = warp_join<false>(run.a, P.c);
+                    if (lane == 0) warp_part[parity][warp] = a;
+                } else {
+                    stats[parity].template put<false>(run.a);
+                }
+            }
             bar_arrive(kRowDone + parity);
-            if (C > 1) {
+            if (!STEP && C > 1) {
                 if (!waited) cluster_wait();
-                cluster_arrive();
+                cluster_arrive_relaxed();
                 waited = false;     // for this row's phase: before the next one, or the end
             }
             if constexpr (STEP) {
                 Coef coef{P.c, 0.0f, 0.0f};
                 bar_sync(kRowStep);
                 if (!out) coef = s_coef;
+                // The next row's copies go into the blocks as they empty.
                 Walk<DT> ahead;
                 walk = Walk<DT>{};
                 Output<DT> to;
-                // the next row's copies go into the blocks as they empty
                 const uint64_t next_row = row + stride;
-                const uint32_t next_first = first_superblock(sb_lo, warp, count + 1);
-                const uint32_t next_cached = next_row < P.rows ? min(rounds_of(next_first), P.cache_rounds) : 0;
-                for (uint32_t i = 0; i < max(rounds, next_cached); ++i) {
-                    const uint32_t sb = first + i * kScoreWarps;
-                    if (i < rounds) {
-                        if (walk.seek(P, row, sb, lane)) to.follow(P, row, walk, lane);
-                        if (out) {
+                const bool more = next_row < P.rows;
+                uint32_t sb = first;
+                for (uint32_t i = 0; i < rounds; ++i, sb += kScoreWarps) {
+                    if (walk.seek(P, row, sb, lane)) to.follow(P, row, walk, lane);
+                    if (out) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = 0;
-                        } else {
-                            if (i < cached) read_block(w, block_of(i), lane);
-                            else load_superblock<DT>(w, P, row, walk, sb, lane);
-                            rest_gradient<DT>(w, coef);
-                        }
+                        for (int e = 0; e < 16; ++e) w[e] = 0;
+                    } else {
+                        if (i < cached) read_block(w, block_of(i), lane);
+                        else load_superblock<DT>(w, P, row, walk, sb, lane);
+                        rest_gradient<DT>(w, coef);
                     }
-                    if (i < next_cached) {
-                        const uint32_t next_sb = next_first + i * kScoreWarps;
-                        ahead.seek(P, next_row, next_sb, lane);
-                        begin_copy<DT>(block_of(i), P, next_row, ahead, next_sb, lane);
+                    if (more && i < cached) {
+                        ahead.seek(P, next_row, sb, lane);
+                        begin_copy<DT>(block_of(i), P, next_row, ahead, sb, lane);
                     }
-                    if (i < rounds) {
-                        to.store(w, P, row, walk, sb, lane);
-                        if ((entries >> (i & 31)) & 1) {        // after the vector stores of every lane
-                            __syncwarp();
-#pragma unroll
-                            for (int e = 0; e < kListRegs; ++e)
-                                if ((L.place[e] >> S::kLogSb) == sb)
-                                    S::store_one(Output<DT>::element(P, row, walk.r, L.place[e] - (P.sb0[walk.r] << S::kLogSb)), s_grad[lane + 32 * e]);
-                        }
-                    }
+                    to.store(w, P, row, walk, sb, lane);
                 }
                 copies_commit();
             }
         }
+        if (STEP) bar_arrive(kRowHelped);       // the last row's vector stores are done
         if (!waited) cluster_wait();
+        if (STEP && C > 1) {        // no CTA leaves while a peer may send to it
+            cluster_arrive_relaxed();
+            cluster_wait();
+        }
         return;
     }
 
     // ================= the row warp =================
     const bool joins = STEP || crank == 0;
     RawList raw;        // the list after the one in `cur` / `next`
-    List cur, next;
+    List cur{}, next{};
     float x[kListRegs], x_next[kListRegs];
-    // Sets a row up: places for the stream, then the listed scores.
-    auto set_up = [&](uint64_t r, int par) {
-        place_list<DT>(next, raw, P, r, regs);
+    // STEP: the last row's listed gradients of this CTA's part, stored when the
+    // stream's vector stores of that row are done
+    char* listed_at[kListRegs];
+    float listed[kListRegs];
 #pragma unroll
-        for (int i = 0; i < kListRegs; ++i)
-            if (i < regs) s_place[par][lane + 32 * i] = next.place[i];
+    for (int i = 0; i < kListRegs; ++i) {
+        listed[i] = 0.0f;
+        listed_at[i] = nullptr;
+        x_next[i] = neg_inf();
+    }
+    auto store_listed = [&] {
+        each_reg(regs, [&](int i) {
+            if (listed_at[i]) S::store_one(listed_at[i], listed[i]);
+            listed_at[i] = nullptr;
+        });
+    };
+    // Sets a row up: places for the stream, and the listed scores.
+    auto set_up = [&](uint64_t r, int par) {
+        each_reg(regs, [&](int i) {
+            x_next[i] = neg_inf();
+            if (STEP) s_out[par][lane + 32 * i] = nullptr;
+        });
+        place_list<DT>(next, raw, P, r, regs, [&](int i, const char* score, int rank, uint32_t column) {
+            if (joins) x_next[i] = S::load_one(score);
+            if (STEP) {
+                const uint32_t sb = next.place[i] >> S::kLogSb;
+                if (sb >= sb_lo && sb < sb_hi)
+                    s_out[par][lane + 32 * i] = static_cast<char*>(P.g[rank]) + (r * P.ldg[rank] + column) * S::kBytes;
+            }
+        });
+        each_reg(regs, [&](int i) {
+            if (STEP) {
+                const uint32_t sb = next.place[i] >> S::kLogSb, d = sb - sb_lo;
+                s_mask[par][lane + 32 * i] = sb >= sb_lo && sb < sb_hi && d / kScoreWarps < P.cache_rounds
+                    ? (d % kScoreWarps) << 28 | (d * kSuperblockBytes + (next.place[i] & ((1u << S::kLogSb) - 1)) * S::kBytes) : ~0u;
+            }
+            if (!STEP || P.cache_rounds * kScoreWarps < sb_hi - sb_lo) s_place[par][lane + 32 * i] = next.place[i];
+        });
         if (lane == 0) row_out[par] = !next.some;
         bar_arrive(kRowReady + par);
-        if (r + stride < P.rows) load_raw(raw, P, r + stride, lane);
-        if (joins) {
-#pragma unroll
-            for (int i = 0; i < kListRegs; ++i) {
-                x_next[i] = neg_inf();
-                if (next.place[i] != kNoPlace) x_next[i] = listed_score<DT>(P, r, next.place[i]);
-            }
-        }
+        if (r + stride < P.rows) load_raw(raw, P, r + stride, regs, lane);
     };
     if (row < P.rows) {
-        load_raw(raw, P, row, lane);
+        load_raw(raw, P, row, regs, lane);
         set_up(row, 0);
     }
     if (C > 1) cluster_wait();
     int parity = 0;
+    uint32_t turn = 0;      // of the two counted barriers
     for (; row < P.rows; row += stride, parity ^= 1) {
         cur = next;
 #pragma unroll
@@ -379,25 +429,39 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
         float g = 0.0f;
         if (joins && !out) {
             if (STEP) g = __fmul_rn(P.scale, P.g_row[row]);
-            teacher_mass(t, cur, P);
-#pragma unroll
-            for (int i = 0; i < kListRegs; ++i) l.x = max_nan(l.x, x[i]);
-            l.x = warp_max_nan(l.x);
+            teacher_mass(t, cur, P, regs);
+            each_reg(regs, [&](int i) { l.x = max_nan(l.x, x[i]); });
+            l.x = redux_max_nan(l.x);
             if (l.x != neg_inf()) {
-#pragma unroll
-                for (int i = 0; i < kListRegs; ++i) l.s = __fadd_rn(l.s, ex2(__fmul_rn(__fadd_rn(x[i], -l.x), P.c)));
+                each_reg(regs, [&](int i) { l.s = __fadd_rn(l.s, ex2(__fmul_rn(__fadd_rn(x[i], -l.x), P.c))); });
                 l.s = warp_sum(l.s);
             }
         }
         bar_sync(kRowDone + parity);
         Stat b{neg_inf(), 0.0f, 0.0f};
-        if (!out) b = stats[parity].template join<false>(lane, P.c);
-        if (C > 1) {
-            if (!out && lane < (STEP ? C : 1)) push_stat<false>(part[parity], crank, lane, b);
+        if (!out) {
+            if constexpr (STEP) b = join_parts<false>(warp_part[parity], kScoreWarps, lane, P.c);
+            else b = stats[parity].template join<false>(lane, P.c);
+        }
+        if (STEP && C > 1 && !out) {
+            // in turn by the rows that take part: a peer sends the row after next
+            // only when it has this CTA's of the next, sent after this one is read
+            const int slot = turn & 1;
+            if (lane == 0) counted_expect(&step_bar[slot], (uint32_t)C * 8);
+            __syncwarp();
+            if (lane < C) counted_store(&step_part[slot][crank], &step_bar[slot], lane, b.x, b.s);
+            const bool came = counted_wait(&step_bar[slot], turn >> 1 & 1);
+            ++turn;
+            Stat o{neg_inf(), 0.0f, 0.0f};
+            if (lane < C) o = {step_part[slot][lane].x, step_part[slot][lane].y, 0.0f};
+            if (!came) o.x = quiet_nan();
+            b = warp_join<false>(o, P.c);
+        } else if (!STEP && C > 1) {
+            if (!out && lane == 0) push_stat<false>(&part[parity][crank], 0, b);
             __syncwarp();
             cluster_arrive();
             cluster_wait();
-            if (joins && !out) b = join_cluster<false>(part[parity], C, lane, P.c);
+            if (joins && !out) b = join_parts<false>(part[parity], C, lane, P.c);
         }
         if (!joins) continue;
         if (out) {
@@ -408,39 +472,43 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                     P.stats[4 * row + 1] = P.stats[4 * row + 3] = 0.0f;
                 }
             }
-            if (STEP) bar_arrive(kRowStep);
+            if (STEP) {
+                bar_arrive(kRowStep);
+                store_listed();
+            }
             continue;
         }
-        Stat all{max_nan(b.x, l.x), 0.0f, 0.0f};
-        {
-            Stat r = b;
-            rebase<false>(r, all.x, P.c);
-            rebase<false>(l, all.x, P.c);
-            all.s = __fadd_rn(r.s, l.s);
+        Stat all{max_nan(b.x, l.x), 0.0f, 0.0f}, r = b;
+        rebase<false>(r, all.x, P.c);
+        rebase<false>(l, all.x, P.c);
+        all.s = __fadd_rn(r.s, l.s);
+        if (STEP) {
+            // The stream waits for this: no logarithm in it.  p_R = r.s / all.s
+            // An empty row (its y all -inf) gets zeros, one with NaN or +inf NaN.
+            const float y = __fmul_rn(all.x, P.scale);
+            const float inv = fabsf(y) < __int_as_float(0x7f800000) ? reciprocal(all.s) : y == neg_inf() ? 0.0f : quiet_nan();
+            if (lane == 0) {
+                const Ref k = reference(b.x, P.c);
+                const float mass = __fmul_rn(g, __fmaf_rn(__fmul_rn(r.s, inv), t.Q, -t.q_rest));
+                s_coef = {k.c, k.ref, __fmul_rn(b.x, P.scale) == neg_inf() ? 0.0f : __fmul_rn(__fmul_rn(mass, reciprocal(b.s)), undo(k))};
+            }
+            bar_arrive(kRowStep);
+            // the row before: its vector stores were done when the stream came to this one
+            store_listed();
+            each_reg(regs, [&](int i) {
+                listed_at[i] = s_out[parity][lane + 32 * i];
+                const float p = __fmul_rn(ex2(__fmul_rn(__fadd_rn(x[i], -all.x), P.c)), inv);
+                listed[i] = __fmul_rn(x[i], P.scale) == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(p, t.Q, -t.q[i]));
+            });
         }
+        if (crank != 0) continue;
         const Final f = finish(all, P.scale), rest = finish(b, P.scale);
         const float logp_rest = rest.m == neg_inf() ? neg_inf()
                               : __fmaf_rn(__fadd_rn(b.x, -all.x), P.scale, __fadd_rn(rest.log_s, -f.log_s));
-        float logp[kListRegs];
-#pragma unroll
-        for (int i = 0; i < kListRegs; ++i) {
-            logp[i] = log_prob(x[i], all, f, P.scale);
-            if (STEP && lane + 32 * i < P.K)
-                s_grad[lane + 32 * i] = x[i] == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(expf(logp[i]), t.Q, -t.q[i]));
-        }
-        if (STEP) {
-            if (lane == 0) {
-                const Ref k = reference(b.x, P.c);
-                const float mass = __fmul_rn(g, __fmaf_rn(expf(logp_rest), t.Q, -t.q_rest));
-                s_coef = {k.c, k.ref, rest.m == neg_inf() ? 0.0f : __fmul_rn(__fdiv_rn(mass, b.s), undo(k))};
-            }
-            bar_arrive(kRowStep);
-        }
-        if (crank != 0) continue;
         float loss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kListRegs; ++i)
-            if (!(t.q[i] == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q[i], __fadd_rn(t.logq[i], -logp[i])));
+        each_reg(regs, [&](int i) {
+            if (!(t.q[i] == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q[i], __fadd_rn(t.logq[i], -log_prob(x[i], all, f, P.scale))));
+        });
         loss = warp_sum(loss);
         if (!(t.q_rest == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q_rest, __fadd_rn(logf(t.q_rest), -logp_rest)));
         if (lane == 0) {
@@ -451,6 +519,14 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                 P.stats[4 * row + 2] = rest.m;
                 P.stats[4 * row + 3] = rest.logs;
             }
+        }
+    }
+    if (STEP) {
+        bar_sync(kRowHelped);
+        store_listed();
+        if (C > 1) {
+            cluster_arrive_relaxed();
+            cluster_wait();
         }
     }
 }
@@ -469,14 +545,19 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
         const uint32_t part = (uint32_t)(unit - row * (uint32_t)P.parts);
         const uint32_t sb_lo = part * P.part_sb, sb_hi = min(nsb, sb_lo + P.part_sb);
         RawList raw;
-        load_raw(raw, P, row, lane);
-        List L;
-        place_list<DT>(L, raw, P, row, regs);
+        load_raw(raw, P, row, regs, lane);
+        List L{};
+        uint32_t bits = 0;
+        place_list<DT>(L, raw, P, row, regs, [&](int i, const char*, int, uint32_t) {
+            const uint32_t sb = L.place[i] >> S::kLogSb;
+            if (sb >= sb_lo && sb < sb_hi) bits |= 1u << (sb - sb_lo);
+        });
+        const uint32_t entries = __reduce_or_sync(~0u, bits);      // superblocks of the unit that hold some
         Coef coef{P.c, 0.0f, 0.0f};
         float m = 0.0f, logs = 0.0f, g = 0.0f;
         Teacher t;
         if (L.some) {
-            teacher_mass(t, L, P);
+            teacher_mass(t, L, P, regs);
             m = P.stats_in[4 * row];
             logs = P.stats_in[4 * row + 1];
             const float m_rest = P.stats_in[4 * row + 2], logs_rest = P.stats_in[4 * row + 3];
@@ -488,7 +569,6 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
                                                   __fmul_rn(expf(__fadd_rn(k.rho, -logs_rest)), undo(k.f)))};
             }
         }
-        const uint32_t entries = rounds_with_entries<DT>(L, sb_lo, sb_hi, 1);
         Walk<DT> walk;
         Output<DT> out;
         for (uint32_t sb = sb_lo; sb < sb_hi; ++sb) {
@@ -502,28 +582,28 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
             }
             load_superblock<DT>(w, P, row, walk, sb, lane);
             // the listed places' gradients, from their scores before an in-place store takes them
-            const bool any = (entries >> ((sb - sb_lo) & 31)) & 1;
+            const bool any = (entries >> (sb - sb_lo)) & 1;
+            auto offset = [](uint32_t place) { return (place & ((1u << S::kLogSb) - 1)) * S::kBytes; };
             float listed[kListRegs];
             if (any) {
-#pragma unroll
-                for (int i = 0; i < kListRegs; ++i) {
+                each_reg(regs, [&](int i) {
                     listed[i] = 0.0f;
                     if ((L.place[i] >> S::kLogSb) == sb) {
-                        const float x = S::load_one(walk.shard(P, row).base + (uint64_t)(L.place[i] - (P.sb0[walk.r] << S::kLogSb)) * S::kBytes);
-                        const float logp = __fadd_rn(__fmaf_rn(x, P.scale, -m), -logs);
-                        if (x != neg_inf()) listed[i] = __fmul_rn(g, __fmaf_rn(expf(logp), t.Q, -t.q[i]));
+                        const float x = S::load_one(walk.address(sb) - lane * 16 + offset(L.place[i]));
+                        const float p = exp_near(__fadd_rn(__fmaf_rn(x, P.scale, -m), -logs));
+                        if (__fmul_rn(x, P.scale) != neg_inf()) listed[i] = __fmul_rn(g, __fmaf_rn(p, t.Q, -t.q[i]));
                     }
-                }
+                });
                 __syncwarp();
             }
             rest_gradient<DT>(w, coef);
             out.store(w, P, row, walk, sb, lane);
             if (any) {
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kListRegs; ++i)
+                each_reg(regs, [&](int i) {
                     if ((L.place[i] >> S::kLogSb) == sb)
-                        S::store_one(Output<DT>::element(P, row, walk.r, L.place[i] - (P.sb0[walk.r] << S::kLogSb)), listed[i]);
+                        S::store_one(out.in_superblock(P, row, walk, sb, offset(L.place[i]), lane), listed[i]);
+                });
             }
         }
     }

@@ -473,7 +473,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
             bar_arrive(kRowDone + parity);
             if (C > 1) {
                 if (!waited) cluster_wait();
-                cluster_arrive();
+                if (TOP) cluster_arrive();      // its runs' keys
+                else cluster_arrive_relaxed();
                 waited = false;         // for this row's phase: before the next one, or the end
             }
             if (TOP && crank == 0) {
@@ -522,14 +523,15 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
         Stat all{neg_inf(), 0.0f, 0.0f};
         if (!out) all = stats[parity].template join<ENT>(lane, P.c);
         if (C > 1) {
-            if (lane == 0 && !out) push_stat<ENT>(part[parity], crank, 0, all);
+            if (lane == 0 && !out) push_stat<ENT>(&part[parity][crank], 0, all);
+            __syncwarp();
             cluster_arrive();
             cluster_wait();
             if (crank != 0) {
                 row_ready(row + 2 * stride, id_after, parity);
                 continue;
             }
-            if (!out) all = join_cluster<ENT>(part[parity], C, lane, P.c);
+            if (!out) all = join_parts<ENT>(part[parity], C, lane, P.c);
         }
         Final f{neg_inf(), 0.0f, 0.0f};
         bool fits = true;

@@ -83,6 +83,19 @@ __device__ __forceinline__ float redux_max_nan(float v) {
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
+// e^x to some 2^-22 relative: the product's rounding, |x| 2^-24, is put back.
+__device__ __forceinline__ float exp_near(float x) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    float h = __fmul_rn(x, kLog2e);
+    if (h < kFarBelow) h = kFarBelow;       // NaN stays
+    const float lost = __fmaf_rn(x, kLog2e, -h), e = ex2(h);
+    return e == 0.0f ? 0.0f : __fmaf_rn(e, __fmul_rn(lost, 0.69314718f), e);
+}
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -303,6 +316,12 @@ struct Output {
         const uint32_t lo = shard_row<DT>(P.x[r], P.ld[r], row, 0).lo;
         return static_cast<char*>(P.g[r]) + (row * P.ldg[r] + (place - lo)) * Score<DT>::kBytes;
     }
+    // the element at byte `off` of the superblock the walk stands at
+    __device__ __forceinline__ char* in_superblock(const ScoreParams& P, uint64_t row, const Walk<DT>& walk, uint32_t sb, uint32_t off,
+                                                   int lane) const {
+        if (alike) return at + (uint64_t)sb * kSuperblockBytes - lane * 16 + off;
+        return element(P, row, walk.r, walk.place(P, sb) + off / Score<DT>::kBytes);
+    }
     // Stores a superblock's words; element by element at the row's ends, and
     // everywhere where the two rows are not alike.
     __device__ __forceinline__ void store(const uint32_t (&w)[16], const ScoreParams& P, uint64_t row, const Walk<DT>& walk, uint32_t sb,
@@ -486,7 +505,39 @@ __device__ __forceinline__ void peer_store(uint32_t a, uint32_t v) {
     asm volatile("st.shared::cluster.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// For a thread that has nothing to show its peers: the other form waits until
+// all its stores, a row's gradients among them, have been performed.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// Eight bytes into a peer's shared memory, counted by a barrier of the peer's
+// (mbarrier): what arrives there is complete without a fence here.  A fence
+// at cluster scope would wait for every global store before it, and the loss-
+// and-gradient kernel has a row's gradients on their way at that point.
+__device__ __forceinline__ void counted_init(uint64_t* bar) {
+    const uint32_t b = (uint32_t)__cvta_generic_to_shared(bar);
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(b) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void counted_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"((uint32_t)__cvta_generic_to_shared(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void counted_store(void* slot, uint64_t* bar, uint32_t rank, float a, float b) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+                 :: "r"(peer_address(slot, rank)), "f"(a), "f"(b), "r"(peer_address(bar, rank)) : "memory");
+}
+// Waits for a phase of the barrier; false after some seconds (the peers of a
+// cluster run together and each sends before it waits, so this never is).
+__device__ __forceinline__ bool counted_wait(uint64_t* bar, uint32_t parity) {
+    const uint32_t b = (uint32_t)__cvta_generic_to_shared(bar);
+    for (int i = 0; i < (1 << 24); ++i) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done) : "r"(b), "r"(parity) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
 
 // ---- running softmax statistics ----
 struct Stat {
@@ -590,27 +641,33 @@ __device__ __forceinline__ float warp_max_nan(float v) {
     for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, o));
     return v;
 }
-// Joins `each` statistics of every lane of a warp; all lanes get the result.
-template <bool ENT, int kEach>
-__device__ __forceinline__ Stat warp_join(Stat (&o)[kEach], float c) {
-    float X = o[0].x;
-#pragma unroll
-    for (int i = 1; i < kEach; ++i) X = max_nan(X, o[i].x);
-    X = warp_max_nan(X);
-    Stat b{X, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        rebase<ENT>(o[i], X, c);
-        b.s = __fadd_rn(b.s, o[i].s);
-        if (ENT) b.u = __fadd_rn(b.u, o[i].u);
-    }
-    b.s = warp_sum(b.s);
-    if (ENT) b.u = warp_sum(b.u);
-    return b;
+// Joins the statistics of a warp's lanes; every lane gets the result.
+template <bool ENT>
+__device__ __forceinline__ Stat warp_join(Stat a, float c) {
+    rebase<ENT>(a, redux_max_nan(a.x), c);
+    a.s = warp_sum(a.s);
+    if (ENT) a.u = warp_sum(a.u);
+    return a;
 }
-// The stream's threads leave their statistics of a row here, and the row warp
-// joins them: a join in every warp first is three times the instructions and
-// keeps the stream waiting for its shuffles.
+// Joins the n statistics of a row's warps (one warp; every lane gets the result).
+template <bool ENT>
+__device__ __forceinline__ Stat join_parts(const Stat* part, int n, int lane, float c) {
+    Stat b = lane < n ? part[lane] : Stat{neg_inf(), 0.0f, 0.0f};
+    for (int i = lane + 32; i - lane < n; i += 32) {
+        Stat o = i < n ? part[i] : Stat{neg_inf(), 0.0f, 0.0f};
+        const float X = max_nan(b.x, o.x);
+        rebase<ENT>(b, X, c);
+        rebase<ENT>(o, X, c);
+        b.s = __fadd_rn(b.s, o.s);
+        if (ENT) b.u = __fadd_rn(b.u, o.u);
+    }
+    return warp_join<ENT>(b, c);
+}
+// In the forward-only kernels the stream's threads leave their statistics of a
+// row here for the row warp, which has time while the stream is in the next
+// row: a join in every warp first kept the stream at its shuffles (distillation
+// loss of 4096 x 131072 172 against 163 us).  Where the stream waits for the
+// result (loss and gradient in one) the warps join first: 774 against 793 us.
 struct LaneStats {
     float x[kThreads], s[kThreads], u[kThreads];
     template <bool ENT>
@@ -621,21 +678,28 @@ struct LaneStats {
     }
     template <bool ENT>
     __device__ __forceinline__ Stat join(int lane, float c) const {
-        Stat o[kScoreWarps];
+        Stat o[kScoreWarps], b{neg_inf(), 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < kScoreWarps; ++i) o[i] = {x[32 * i + lane], s[32 * i + lane], ENT ? u[32 * i + lane] : 0.0f};
-        return warp_join<ENT>(o, c);
+        for (int i = 0; i < kScoreWarps; ++i) {
+            o[i] = {x[32 * i + lane], s[32 * i + lane], ENT ? u[32 * i + lane] : 0.0f};
+            b.x = max_nan(b.x, o[i].x);
+        }
+        b.x = redux_max_nan(b.x);
+#pragma unroll
+        for (int i = 0; i < kScoreWarps; ++i) {
+            rebase<ENT>(o[i], b.x, c);
+            b.s = __fadd_rn(b.s, o[i].s);
+            if (ENT) b.u = __fadd_rn(b.u, o[i].u);
+        }
+        b.s = warp_sum(b.s);
+        if (ENT) b.u = warp_sum(b.u);
+        return b;
     }
 };
-// The cluster's CTAs' statistics, pushed by their row warps.
+// A warp's statistic of a row, into the cluster CTA `to_rank`'s array.
 template <bool ENT>
-__device__ __forceinline__ Stat join_cluster(const Stat* part, int C, int lane, float c) {
-    Stat o[1] = {lane < C ? part[lane] : Stat{neg_inf(), 0.0f, 0.0f}};
-    return warp_join<ENT>(o, c);
-}
-template <bool ENT>
-__device__ __forceinline__ void push_stat(Stat* part, int crank, int to_rank, const Stat& a) {
-    const uint32_t to = peer_address(&part[crank], to_rank);
+__device__ __forceinline__ void push_stat(Stat* slot, int to_rank, const Stat& a) {
+    const uint32_t to = peer_address(slot, to_rank);
     peer_store(to, __float_as_uint(a.x));
     peer_store(to + 4, __float_as_uint(a.s));
     if (ENT) peer_store(to + 8, __float_as_uint(a.u));
