@@ -41,17 +41,10 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 __device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) { return __reduce_max_sync(~0u, v); }
 
-// A bound that at least k of n keys reach, and not many more (0 where fewer
-// than k are not 0): bisected, by votes, among the largest keys of up to 128
-// groups of them.  One warp.
-template <class Key>
-__device__ __forceinline__ uint32_t kth_bound(Key key, uint32_t n, int k, int lane) {
-    uint32_t top[4] = {0, 0, 0, 0};
-    for (uint32_t i = lane; i < n; i += 128) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (i + 32 * q < n) top[q] = max(top[q], key(i + 32 * q));
-    }
+// A bound that at least k of a warp's keys reach, and not many more (0 where
+// fewer than k of them are not 0), bisected by votes.  A lane gives the largest
+// of each of four groups of its keys.
+__device__ __forceinline__ uint32_t kth_bound(const uint32_t (&top)[4], int k) {
     auto reach = [&](uint32_t bound) {
         int c = 0;
 #pragma unroll
@@ -172,7 +165,7 @@ template <int DT>
 __device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t bound, int* next, uint32_t* ring, uint2* cand,
                                         int* n_cand, int lane) {
     using S = Score<DT>;
-    constexpr int kBatch = 4;       // runs in flight
+    constexpr int kBatch = 2;       // runs in flight: they were prefetched, and more registers cost more than they hide
     const int cap = score_top_candidates(k);
     int ties = 0, head = 0, tail = 0;
     auto take_apart = [&](int count) {
@@ -274,6 +267,7 @@ __device__ __forceinline__ void collect_in_order(const uint4* at, int n, int k, 
             }
             __syncwarp();
             count++;
+            if (j == 0 && left == 1) floor_key = top;       // this run alone holds k: nothing below its k-th counts
         }
     }
     if (lane == 0) *n_cand = count;
@@ -321,49 +315,79 @@ struct TopShared {
     uint32_t published;             // the row's number here + 1
 };
 template <int DT>
-__device__ __forceinline__ void help(const ScoreParams& P, TopShared& T, uint2* cand, int warp, int lane) {
-    collect<DT>(T.at, T.n_picked, P.top_k, T.bound, &T.next, T.ring[warp], cand, &T.n_cand, lane);
+__device__ __noinline__ void help(int k, TopShared& T, uint2* cand, int warp, int lane) {
+    collect<DT>(T.at, T.n_picked, k, T.bound, &T.next, T.ring[warp], cand, &T.n_cand, lane);
 }
 
 // Calls of their own: inlined, their registers crowd the stream's.
 template <int DT>
 __device__ __forceinline__ void locate(const ScoreParams& P, uint64_t row, TopShared& T, int n, int lane) {
-    for (int i = lane; i < n; i += 32) T.at[i] = locate_run<DT>(P, row, T.picked[i]);
+    // The row left the L2 when the others streamed through it: all its runs are
+    // asked for at once, before they are read in batches.
+    for (int i = lane; i < n; i += 32) {
+        const uint4 run = locate_run<DT>(P, row, T.picked[i]);
+        const uint32_t lo = run.w & 0xffffu, hi = run.w >> 16;
+        const char* a = reinterpret_cast<const char*>((uint64_t)run.y << 32 | run.x);
+        for (uint32_t e = lo; e < hi; e += 128 / Score<DT>::kBytes)
+            asm volatile("prefetch.global.L2 [%0];" :: "l"(a + e * Score<DT>::kBytes));
+        T.at[i] = run;
+    }
     __syncwarp();
 }
 // Picks a row's runs and publishes them as number `count`; false where they overflow.
 template <int DT>
-__device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, uint32_t count, const uint32_t* keys, uint32_t runs, uint2* cand,
-                                       TopShared& T, int lane) {
+__device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, uint32_t count, const uint32_t* keys, uint32_t runs, TopShared& T, int lane) {
     using S = Score<DT>;
     const int k = P.top_k;
-    uint32_t bound = kth_bound([&](uint32_t i) { return keys[i]; }, runs, k, lane);
+    // Lane l has runs [l n, (l + 1) n): a lane's finds are in column order, and
+    // one scan over the lanes places them.
+    const uint32_t n = (runs + 127) / 128 * 4, lo = min(runs, lane * n), hi = min(runs, lo + n);
+    uint32_t top[4] = {0, 0, 0, 0};
+    for (uint32_t i = lo; i < hi; i += 16) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (i + 4 * q < hi) {
+                const uint4 v = *reinterpret_cast<const uint4*>(keys + i + 4 * q);
+                top[q] = max(top[q], max(max(v.x, v.y), max(v.z, v.w)));
+            }
+    }
+    uint32_t bound = kth_bound(top, k);
     // the runs that reach it: all those above, the first k of those at it
-    int m = 0, ties = 0;
-    const uint32_t below = (1u << lane) - 1;
-    for (uint32_t i0 = lane; i0 - lane < runs; i0 += 128) {
-        uint32_t key[4];
+    uint32_t found = 0;         // above in the low half, at it in the high one
+    for (uint32_t i = lo; i < hi; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+        found += (v.x > bound) + (v.y > bound) + (v.z > bound) + (v.w > bound);
+        if (bound) found += ((v.x == bound) + (v.y == bound) + (v.z == bound) + (v.w == bound)) << 16;
+    }
+    uint32_t upto = found;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) key[q] = i0 + 32 * q < runs ? keys[i0 + 32 * q] : 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t same = __ballot_sync(~0u, key[q] == bound && key[q] != 0);
-            const bool take = key[q] > bound || (((same >> lane) & 1) && ties + __popc(same & below) < k);
-            const uint32_t who = __ballot_sync(~0u, take);
-            const int to = m + __popc(who & below);
-            if (take && to < kMaxPicked) T.picked[to] = i0 + 32 * q;
-            m += __popc(who);
-            ties += __popc(same);
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += up;
+    }
+    const uint32_t all = __shfl_sync(~0u, upto, 31), before = upto - found;
+    const int m = (int)(all & 0xffffu) + min((int)(all >> 16), k);
+    if (m <= kMaxPicked && found) {
+        int to = (int)(before & 0xffffu) + min((int)(before >> 16), k), keep = k - (int)(before >> 16);
+        for (uint32_t i = lo; i < hi; ++i) {
+            const uint32_t key = keys[i];
+            if (key > bound || (key == bound && key != 0 && keep-- > 0)) T.picked[to++] = i;
         }
     }
     __syncwarp();
     const bool fits = m <= kMaxPicked;
     if (fits) locate<DT>(P, row, T, m, lane);
     if (bound == 0 && fits && m > k) {      // places without a score left too few groups: without them
-        bound = kth_bound([&](uint32_t i) { return keys[T.picked[i]]; }, (uint32_t)m, k, lane);
+        uint32_t most[4] = {0, 0, 0, 0};
+        for (int i = lane; i < m; i += 128) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (i + 32 * q < m) most[q] = max(most[q], keys[T.picked[i + 32 * q]]);
+        }
+        bound = kth_bound(most, k);
     } else if (bound == 0 && fits) {
         // fewer runs than k: a bound from the lanes' largest scores in them
-        uint32_t* lanes = reinterpret_cast<uint32_t*>(cand);
+        uint32_t most[4] = {0, 0, 0, 0};
         for (int j0 = 0; j0 < m; j0 += 4) {
             uint32_t v[16], in_row[4];
 #pragma unroll
@@ -371,10 +395,9 @@ __device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, uint3
                 if (j0 + b < m) in_row[b] = load_run<DT>(v, b, T.at[j0 + b], lane);
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                if (j0 + b < m) lanes[(j0 + b) * 32 + lane] = in_row[b] ? order_key(S::template max_words<4>(&v[4 * b])) : 0;
+                if (j0 + b < m && in_row[b]) most[b] = max(most[b], order_key(S::template max_words<4>(&v[4 * b])));
         }
-        __syncwarp();
-        bound = kth_bound([&](uint32_t i) { return lanes[i]; }, (uint32_t)m * 32, k, lane);
+        bound = kth_bound(most, k);
     }
     __syncwarp();
     if (lane == 0) {
@@ -481,7 +504,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
                 if (!last_out) {        // the row before: what its runs' readers have left
                     if (*reinterpret_cast<volatile uint32_t*>(&top.published) == count) {
                         __threadfence_block();
-                        help<DT>(P, top, cand, warp, lane);
+                        help<DT>(k, top, cand, warp, lane);
                     }
                     bar_arrive(kRowHelped);
                 }
@@ -491,7 +514,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
         }
         if (TOP && !last_out) {
             bar_sync(kRowHelp);
-            help<DT>(P, top, cand, warp, lane);
+            help<DT>(k, top, cand, warp, lane);
             bar_arrive(kRowHelped);
         }
         if (!waited) cluster_wait();
@@ -536,7 +559,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
         Final f{neg_inf(), 0.0f, 0.0f};
         bool fits = true;
         if (TOP && !out) {
-            fits = pick_runs<DT>(P, row, count, keys + parity * runs, runs, cand, top, lane);
+            fits = pick_runs<DT>(P, row, count, keys + parity * runs, runs, top, lane);
             if (row + stride >= P.rows) bar_arrive(kRowHelp);      // the last row: the stream has nothing else to do
         }
         if (!out) f = finish(all, P.scale);
@@ -549,7 +572,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
             if (ENT) P.entropy[row] = f.m == neg_inf() ? 0.0f : __fmaf_rn(-kLn2, __fdiv_rn(all.u, all.s), f.log_s);
         }
         if (TOP && !out) {
-            if (fits) help<DT>(P, top, cand, kScoreWarps, lane);
+            if (fits) help<DT>(k, top, cand, kScoreWarps, lane);
             bar_sync(kRowHelped);
             if (!fits || top.n_cand > score_top_candidates(k)) mend_candidates<DT>(P, row, keys + parity * runs, runs, cand, top, lane);
         }

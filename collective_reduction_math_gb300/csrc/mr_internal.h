@@ -172,12 +172,10 @@ __host__ __device__ constexpr int score_top_candidates(int k) {
     return k * (k + 1) / 2 > 12 * k + 128 ? k * (k + 1) / 2 : 12 * k + 128;
 }
 // Shared memory of the top-k path: its fixed part, a key for each 512-byte run
-// of a row (two rows of them), and the candidates (or, before them, 32 k keys
-// of lanes).
+// of a row (two rows of them), and the candidates.
 constexpr size_t kTopSharedBytes = 7 * 1024;
 constexpr size_t score_top_smem(uint32_t runs, int k) {
-    return kTopSharedBytes + (size_t)runs * 8 +
-           (size_t)(score_top_candidates(k) * 8 > k * 128 ? score_top_candidates(k) * 8 : k * 128);
+    return kTopSharedBytes + (size_t)runs * 8 + (size_t)score_top_candidates(k) * 8;
 }
 
 struct GatherParams {

@@ -261,10 +261,15 @@ bool step_needs(const Call& c, int C, int choice, size_t* smem, double* again) {
     return true;
 }
 
-// Warps per row of an elementwise kernel, and the grid.
-dim3 grad_grid(Call& c) {
+// Warps per row of an elementwise kernel, each of `most` superblocks or, where
+// there are few rows, fewer, and the grid.  The distillation's units read the
+// row's list: 16 superblocks each (4096 x 128000 bf16, 100 entries, units of 4,
+// 8, 12, 16, 24: 406, 360, 353, 349, 360 us); the log probabilities' read
+// next to nothing and keep the GPU's window on memory smaller with 4 (8192 x
+// 131072: 623, 635, 642, 653, 657 us).
+dim3 grad_grid(Call& c, uint32_t most) {
     const size_t warps = (size_t)mr::device_sms() * 3 * (mr::kThreads / 32);
-    uint32_t s = 8;
+    uint32_t s = most;
     while (s > 1 && c.rows * ((c.nsb + s - 1) / s) < 2 * warps) s /= 2;
     c.P.part_sb = s;
     c.P.parts = (int)((c.nsb + s - 1) / s);
@@ -386,7 +391,7 @@ mr_status_t mr_logprob_grad(const void* const* logits, const size_t* ld, int W, 
     c.P.entropy_in = entropy;
     c.P.g_row = g_logprob;
     c.P.g_entropy = g_entropy;
-    const dim3 grid = grad_grid(c);
+    const dim3 grid = grad_grid(c, 4);
     return launched(c, mr::launch_logprob_grad(c.P, dtype, grid, (cudaStream_t)stream), grid, 0);
 }
 
@@ -423,7 +428,7 @@ mr_status_t mr_distill_topk_grad(const void* const* logits, const size_t* ld, in
     if ((st = check_spans(c.spans)) != MR_OK) return st;
     c.P.stats_in = stats;
     c.P.g_row = g_loss;
-    const dim3 grid = grad_grid(c);
+    const dim3 grid = grad_grid(c, 16);
     return launched(c, mr::launch_distill_grad(c.P, dtype, grid, (cudaStream_t)stream), grid, 0);
 }
 

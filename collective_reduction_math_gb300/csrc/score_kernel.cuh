@@ -408,11 +408,18 @@ struct Feed {
         return first_superblock(sb_lo, warp, of) < sb_hi ? load<RUNS>(w, P, warp, lane) : runs;
     }
     // Gives work(w, sb, runs) a row's superblocks; on entry and on return w
-    // holds the next one.  Two in turn, so that none is moved between registers.
+    // holds the next one.  Two in turn, so that none is moved between registers;
+    // with RUNS (the top-k kernels, whose stream has no registers to spare) one,
+    // the next loaded when it has been worked on: top 64 of 2048 x 160000 bf16
+    // 218 us against 240.
     template <bool RUNS, class Work>
     __device__ __forceinline__ uint32_t each(uint32_t (&w)[16], uint32_t runs, const ScoreParams& P, uint32_t first, int warp, int lane,
                                              Work work) {
-        for (uint32_t s = first; s < sb_hi; s += 2 * kScoreWarps) {
+        for (uint32_t s = first; RUNS && s < sb_hi; s += kScoreWarps) {
+            work(w, s, runs);
+            runs = load<RUNS>(w, P, warp, lane);
+        }
+        for (uint32_t s = first; !RUNS && s < sb_hi; s += 2 * kScoreWarps) {
             uint32_t x[16];
             const uint32_t more = load<RUNS>(x, P, warp, lane);
             work(w, s, runs);
