@@ -172,11 +172,12 @@ int resident_clusters(int dev, mr::ScoreKernel kernel, int C, size_t smem) {
         size_t smem;
         int C, dev, n;
     };
-    static Known known[256];
-    static int count = 0;
+    constexpr int kMost = 256;      // the oldest gives way
+    static Known known[kMost];
+    static unsigned count = 0;
     static std::mutex mutex;
     std::lock_guard<std::mutex> lock(mutex);
-    for (int i = 0; i < count; ++i)
+    for (unsigned i = 0; i < std::min(count, (unsigned)kMost); ++i)
         if (known[i].kernel == kernel && known[i].smem == smem && known[i].C == C && known[i].dev == dev) return known[i].n;
     int n = 0;
     cudaError_t e = mr::allow_score_kernel(kernel, C, smem);
@@ -200,7 +201,7 @@ int resident_clusters(int dev, mr::ScoreKernel kernel, int C, size_t smem) {
         cudaGetLastError();
         return 0;       // not kept: the launch will say what is wrong
     }
-    if (count < 256) known[count++] = {kernel, smem, C, dev, n};
+    known[count++ % kMost] = {kernel, smem, C, dev, n};
     return n;
 }
 
