@@ -27,7 +27,7 @@
 // What bounds them (GB300, bf16): the loss alone memory, 6.48 TB/s of 6.69 at
 // 4096 x 131072 with 64 entries (161 us); its gradient 5.8 TB/s (355 us at 4096 x
 // 128000, 100 entries), the units' own reading of the list; loss and gradient
-// in one 5.45 TB/s (777 us at 8192 x 131072): two passes over a row cost some 440
+// in one 5.45 TB/s (777 us at 8192 x 131072): two passes over a row cost some 460
 // instructions a 2 KiB superblock, and the stream waits at each row's join.
 #include "score_kernel.cuh"
 

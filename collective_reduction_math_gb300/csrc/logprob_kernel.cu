@@ -21,12 +21,12 @@
 // k (k + 1) / 2 places hold them all.
 //
 // What bounds it (GB300): 8192 x 131072 bf16 in 337 us, 6.17 TB/s of the copy's
-// 6.69; 67 % of the issue slots (8.6 instructions a score with the entropy) and
+// 6.69; 67 % of the issue slots (8.7 instructions a score with the entropy) and
 // memory bind together.  Three CTAs an SM, 72 registers.  Top 64 of 160000
 // takes 2.9 TB/s: its stream has no registers for a superblock ahead, and the
 // row warp's picking and ranking are chains of votes and small loads.  One
 // token of 131072 with 20 alternatives takes 12.7 us, 2.8 of them without the
-// alternatives: 16 CTAs stream the row in 1 us, the rest is that chain.
+// alternatives: the rest is that chain.
 //
 // Gradient: with t = y - m, p = e^t / e^logs and a, b of the row alone,
 //     dx = scale * (-g_lp p - g_H p (log p + H)) = e^t (a + b t),
