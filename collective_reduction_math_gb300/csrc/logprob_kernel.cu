@@ -60,10 +60,15 @@ __device__ __forceinline__ uint32_t kth_bound(const uint32_t (&top)[4], int k) {
         for (int q = 0; q < 4; ++q) c += __popc(__ballot_sync(~0u, top[q] >= bound));
         return c;
     };
-    if (reach(1) < k) return 0;
+    // A bound to start from: with the lanes that have one, the least of their
+    // largest keys is reached once by each, the least of their second ones twice.
+    const uint32_t a = max(top[0], top[1]), b = max(top[2], top[3]), most = max(a, b);
+    const uint32_t second = max(min(a, b), a > b ? min(top[0], top[1]) : min(top[2], top[3]));
+    uint32_t lo = 1, hi = warp_max_u32(most);
+    if (__popc(__ballot_sync(~0u, most != 0)) >= k) lo = __reduce_min_sync(~0u, most ? most : ~0u);
+    else if (2 * __popc(__ballot_sync(~0u, second != 0)) >= k) lo = __reduce_min_sync(~0u, second ? second : ~0u);
+    else if (reach(1) < k) return 0;
     // reach(lo) >= k > reach(hi + 1)
-    uint32_t lo = 1, hi = warp_max_u32(max(max(top[0], top[1]), max(top[2], top[3])));
-    if (hi > 0x80000000u && reach(0x80000000u) >= k) lo = 0x80000000u;      // k scores above -0
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo) / 2 + 1;
         const int c = reach(mid);
@@ -283,18 +288,16 @@ __device__ __forceinline__ void collect_in_order(const uint4* at, int n, int k, 
     __syncwarp();
 }
 
-// Calls put(rank, entry) for the best k of a list of (key, column) (one warp).
-template <class Put>
-__device__ __forceinline__ void rank_list(const uint2* list, int n, int k, int lane, Put put) {
+// The best k of a list of (key, column), in order (one warp).
+__device__ __forceinline__ void rank_list(const uint2* list, int n, int k, uint2* best, int lane) {
     constexpr int kEach = 4;
     for (int i = lane; i < n; i += 32 * kEach) {
-        uint2 mine[kEach];
-        uint64_t whole[kEach];      // key, then the lower column first
+        uint64_t mine[kEach];       // key, then the lower column first
         int rank[kEach];
 #pragma unroll
         for (int q = 0; q < kEach; ++q) {
-            mine[q] = i + 32 * q < n ? list[i + 32 * q] : make_uint2(0, 0);
-            whole[q] = (uint64_t)mine[q].x << 32 | ~mine[q].y;
+            const uint2 c = i + 32 * q < n ? list[i + 32 * q] : make_uint2(0, 0);
+            mine[q] = (uint64_t)c.x << 32 | ~c.y;
             rank[q] = 0;
         }
 #pragma unroll 4
@@ -302,12 +305,13 @@ __device__ __forceinline__ void rank_list(const uint2* list, int n, int k, int l
             const uint2 c = list[o];
             const uint64_t other = (uint64_t)c.x << 32 | ~c.y;
 #pragma unroll
-            for (int q = 0; q < kEach; ++q) rank[q] += other > whole[q];
+            for (int q = 0; q < kEach; ++q) rank[q] += other > mine[q];
         }
 #pragma unroll
         for (int q = 0; q < kEach; ++q)
-            if (i + 32 * q < n && rank[q] < k) put(rank[q], mine[q]);
+            if (i + 32 * q < n && rank[q] < k) best[rank[q]] = make_uint2((uint32_t)(mine[q] >> 32), ~(uint32_t)mine[q]);
     }
+    __syncwarp();
 }
 
 // The top k of a row from its runs' keys, by the row warp of the cluster's
@@ -378,9 +382,16 @@ __device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, uint3
     const int m = (int)(all & 0xffffu) + min((int)(all >> 16), k);
     if (m <= kMaxPicked && found) {
         int to = (int)(before & 0xffffu) + min((int)(before >> 16), k), keep = k - (int)(before >> 16);
-        for (uint32_t i = lo; i < hi; ++i) {
-            const uint32_t key = keys[i];
-            if (key > bound || (key == bound && key != 0 && keep-- > 0)) T.picked[to++] = i;
+        for (uint32_t i = lo; i < hi; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+            const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool tie = key[e] == bound && bound != 0 && keep > 0, take = key[e] > bound || tie;
+                if (take) T.picked[to] = i + e;
+                to += take;
+                keep -= tie;
+            }
         }
     }
     __syncwarp();
@@ -428,15 +439,18 @@ __device__ __noinline__ void mend_candidates(const ScoreParams& P, uint64_t row,
     locate<DT>(P, row, T, r, lane);
     collect_in_order<DT>(T.at, r, P.top_k, floor_key, cand, &T.n_cand, lane);
 }
-__device__ __noinline__ void put_top(const ScoreParams& P, uint64_t row, const uint2* cand, int n, const Stat& all, const Final& f, int lane) {
+__device__ __noinline__ void put_top(const ScoreParams& P, uint64_t row, const uint2* cand, TopShared& T, const Stat& all, const Final& f,
+                                     int lane) {
     const int k = P.top_k;
-    const float scale = P.scale;
-    long long* const top_ids = P.top_ids ? P.top_ids + row * k : nullptr;
-    float* const top_logprob = P.top_logprob ? P.top_logprob + row * k : nullptr;
-    rank_list(cand, n, k, lane, [&](int rank, uint2 c) {
-        if (top_ids) top_ids[rank] = c.y;
-        if (top_logprob) top_logprob[rank] = log_prob(key_value(c.x), all, f, scale);
-    });
+    uint2* const best = reinterpret_cast<uint2*>(T.ring);       // its readers are through
+    static_assert(sizeof(T.ring) >= MR_MAX_TOP * sizeof(uint2), "the best k fit");
+    rank_list(cand, T.n_cand, k, best, lane);
+#pragma unroll 1
+    for (int i = lane; i < k; i += 32) {
+        const uint2 c = best[i];
+        if (P.top_ids) P.top_ids[row * k + i] = c.y;
+        if (P.top_logprob) P.top_logprob[row * k + i] = log_prob(key_value(c.x), all, f, P.scale);
+    }
     __syncwarp();
 }
 
@@ -593,7 +607,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
                     if (P.top_logprob) P.top_logprob[row * k + i] = neg_inf();
                 }
             } else {
-                put_top(P, row, cand, top.n_cand, all, f, lane);
+                put_top(P, row, cand, top, all, f, lane);
             }
         }
     }
