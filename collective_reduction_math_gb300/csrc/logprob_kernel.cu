@@ -326,7 +326,6 @@ struct TopShared {
     uint32_t picked[kMaxPicked];
     uint32_t bound;
     int n_picked, n_cand, next;
-    uint32_t published;             // the row's number here + 1
 };
 template <int DT>
 __device__ __noinline__ void help(int k, TopShared& T, uint2* cand, int warp, int lane) {
@@ -348,9 +347,9 @@ __device__ __forceinline__ void locate(const ScoreParams& P, uint64_t row, TopSh
     }
     __syncwarp();
 }
-// Picks a row's runs and publishes them as number `count`; false where they overflow.
+// Picks a row's runs for the CTA's warps; false, and none, where they overflow.
 template <int DT>
-__device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, uint32_t count, const uint32_t* keys, uint32_t runs, TopShared& T, int lane) {
+__device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, const uint32_t* keys, uint32_t runs, TopShared& T, int lane) {
     using S = Score<DT>;
     const int k = P.top_k;
     // Lane l has runs [l n, (l + 1) n): a lane's finds are in column order, and
@@ -425,8 +424,6 @@ __device__ __noinline__ bool pick_runs(const ScoreParams& P, uint64_t row, uint3
         T.n_cand = T.next = 0;
         T.n_picked = fits ? m : 0;
         T.bound = bound;
-        __threadfence_block();
-        *reinterpret_cast<volatile uint32_t*>(&T.published) = count + 1;
     }
     __syncwarp();
     return fits;
@@ -529,11 +526,10 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
                 waited = false;         // for this row's phase: before the next one, or the end
             }
             if (TOP && crank == 0) {
-                if (!last_out) {        // the row before: what its runs' readers have left
-                    if (*reinterpret_cast<volatile uint32_t*>(&top.published) == count) {
-                        __threadfence_block();
-                        help<DT>(k, top, cand, warp, lane);
-                    }
+                // the row before: its runs have to be read before the row after this one can start
+                if (!last_out) {
+                    bar_sync(kRowHelp);
+                    help<DT>(k, top, cand, warp, lane);
                     bar_arrive(kRowHelped);
                 }
                 last_out = out;
@@ -558,12 +554,11 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
         }
     };
     long long id = id_of(row), id_next = id_of(row + stride);
-    if (TOP && lane == 0) top.published = 0;
     row_ready(row, id, 0);
     row_ready(row + stride, id_next, 1);
     if (C > 1) cluster_wait();
     int parity = 0;
-    for (uint32_t count = 0; row < P.rows; row += stride, parity ^= 1, ++count) {
+    for (; row < P.rows; row += stride, parity ^= 1) {
         const bool out = id < 0;
         const long long id_after = id_of(row + 2 * stride);
         float x_id = quiet_nan();
@@ -587,8 +582,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) logprob_kernel(const __grid_
         Final f{neg_inf(), 0.0f, 0.0f};
         bool fits = true;
         if (TOP && !out) {
-            fits = pick_runs<DT>(P, row, count, keys + parity * runs, runs, top, lane);
-            if (row + stride >= P.rows) bar_arrive(kRowHelp);      // the last row: the stream has nothing else to do
+            fits = pick_runs<DT>(P, row, keys + parity * runs, runs, top, lane);
+            bar_arrive(kRowHelp);
         }
         if (!out) f = finish(all, P.scale);
         if (lane == 0) {

@@ -215,8 +215,13 @@ using Needs = bool (*)(const Call&, int C, int choice, size_t* smem, double* aga
 
 // CTAs per row (a cluster), from the modelled time of the whole call: rounds
 // of rows over the resident clusters, each a CTA's part of a row at its share
-// of the bandwidth and a fixed cost of the row's start and join.
-Plan plan_forward(const Call& c, mr::ScoreKernel kernel, Needs needs, double passes, double fixed_us, double join_us) {
+// of the bandwidth (26 GB/s alone) and the cost of the row's start and join.
+// `pick_us` is what the top alternatives take the row warp, one row after
+// another: a round is not shorter than that, so many rows take small clusters
+// (513 rows of 131072 with 20 alternatives: 56 us on clusters of 1, 58 on 2, 87
+// on 4; 37 rows: 23, 18, 15).
+Plan plan_forward(const Call& c, mr::ScoreKernel kernel, Needs needs, double passes, double join_us, double pick_us) {
+    constexpr double kRowUs = 1.0;
     Plan best{0, 1, 0};
     double best_us = 1e300;
     int dev = 0;
@@ -231,9 +236,10 @@ Plan plan_forward(const Call& c, mr::ScoreKernel kernel, Needs needs, double pas
             if (clusters < 1) continue;
             const double rounds = ceil((double)c.rows / clusters);
             const double active = std::min<double>(clusters, c.rows) * C;
-            const double gbs = std::min(45.0, 6600.0 / active);
-            const double us = rounds * ((double)c.nsb * mr::kSuperblockBytes * (passes + again) / C / (gbs * 1e3) + fixed_us +
-                                        (C == 1 ? 0.0 : join_us));
+            const double gbs = std::min(26.0, 6600.0 / active);
+            const double row_us = (double)c.nsb * mr::kSuperblockBytes * (passes + again) / C / (gbs * 1e3) + kRowUs +
+                                  (C == 1 ? 0.0 : join_us);
+            const double us = row_us + (rounds - 1.0) * std::max(row_us, pick_us);
             if (us < best_us) {
                 best_us = us;
                 best = {C, clusters, bytes};
@@ -318,7 +324,7 @@ mr_status_t run_forward(Call& c, mr::ScoreKernel kernel, const Plan& plan, void*
 
 mr_status_t run_distill(Call& c, bool step, void* stream) {
     const mr::ScoreKernel kernel = mr::distill_forward(c.dtype, step);
-    Plan plan = plan_forward(c, kernel, step ? step_needs : plain_needs, step ? 2.0 : 1.0, 1.0, 1.0);
+    Plan plan = plan_forward(c, kernel, step ? step_needs : plain_needs, step ? 2.0 : 1.0, step ? 2.0 : 1.0, 0.0);
     if (plan.C == 0) {
         // no GPU to ask, or a row too long for sixteen CTAs' shared memory:
         // what does not fit is read again
@@ -366,7 +372,7 @@ mr_status_t mr_logprob(const void* const* logits, const size_t* ld, int W, size_
     c.P.top_ids = top_ids;
     c.P.top_logprob = top_logprob;
     const mr::ScoreKernel kernel = mr::logprob_forward(c.P, dtype);
-    Plan plan = plan_forward(c, kernel, top_k ? top_needs : plain_needs, 1.0, 1.0, 1.0);
+    Plan plan = plan_forward(c, kernel, top_k ? top_needs : plain_needs, 1.0, 1.0, top_k ? 14.0 + 0.22 * top_k : 0.0);
     if (plan.C == 0) plan = {1, 1, top_k ? mr::score_top_smem(c.nsb * mr::kSbRuns, top_k) : 0};       // no GPU to ask: the launch will fail
     return run_forward(c, kernel, plan, stream);
 }
