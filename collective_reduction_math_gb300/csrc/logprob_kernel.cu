@@ -174,7 +174,8 @@ constexpr int kWaiting = 64;
 // equal to it, the first k that this warp meets.  Counts past the list's end
 // are not stored.  A run has a score or two that reach the bound: its lanes
 // only note the vectors that do, and 32 of those are taken apart at a time, a
-// lane each.
+// lane each; once a warp has its k that equal the bound it passes such vectors
+// by (a mask that leaves less than k places makes all the others equal to it).
 template <int DT>
 __device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t bound, int* next, uint32_t* ring, uint2* cand,
                                         int* n_cand, int lane) {
@@ -238,7 +239,8 @@ __device__ __forceinline__ void collect(const uint4* at, int n, int k, uint32_t 
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (j0 + b >= n) break;
-            const bool hit = in_row[b] != 0 && order_key(S::template max_words<4>(&v[4 * b])) >= bound;
+            const uint32_t most = order_key(S::template max_words<4>(&v[4 * b]));
+            const bool hit = in_row[b] != 0 && (most > bound || (most == bound && ties < k));
             const uint32_t who = __ballot_sync(~0u, hit);
             if (hit) ring[(tail + __popc(who & ((1u << lane) - 1))) % kWaiting] = (uint32_t)(j0 + b) << 5 | lane;
             tail += __popc(who);
@@ -288,23 +290,61 @@ __device__ __forceinline__ void collect_in_order(const uint4* at, int n, int k, 
     __syncwarp();
 }
 
+__device__ __forceinline__ uint64_t in_order(uint2 c) { return (uint64_t)c.x << 32 | ~c.y; }      // the lower column first
+
+// Ranking by counting grows with the square of the list: of one longer than
+// kRanked the best stay, at least k, at most kRanked of them (one warp; the
+// entries differ).  Returns how many.
+constexpr int kRanked = 128;
+__device__ __noinline__ int shorten(uint2* list, int n, int k, int lane) {
+    uint32_t least = ~0u, most = 0;
+    for (int i = lane; i < n; i += 32) {
+        least = min(least, list[i].x);
+        most = max(most, list[i].x);
+    }
+    // at least k of the entries reach lo, fewer than k reach hi + 1
+    uint64_t lo = (uint64_t)__reduce_min_sync(~0u, least) << 32, hi = (uint64_t)warp_max_u32(most) << 32 | ~0u;
+    while (lo < hi) {
+        const uint64_t mid = lo + (hi - lo) / 2 + 1;
+        int c = 0;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) c += in_order(list[i]) >= mid;
+        c = __reduce_add_sync(~0u, c);
+        if (c >= k) {
+            lo = mid;
+            if (c <= kRanked) break;
+        } else {
+            hi = mid - 1;
+        }
+    }
+    int m = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const uint2 c = i0 + lane < n ? list[i0 + lane] : make_uint2(0, 0);
+        const bool stays = i0 + lane < n && in_order(c) >= lo;
+        const uint32_t who = __ballot_sync(~0u, stays);
+        if (stays) list[m + __popc(who & ((1u << lane) - 1))] = c;      // before what is read next
+        m += __popc(who);
+    }
+    __syncwarp();
+    return m;
+}
+
 // The best k of a list of (key, column), in order (one warp; kEach entries of
 // a lane at a time).
 template <int kEach>
 __device__ __forceinline__ void rank_list(const uint2* list, int n, int k, uint2* best, int lane) {
     for (int i = lane; i < n; i += 32 * kEach) {
-        uint64_t mine[kEach];       // key, then the lower column first
+        uint64_t mine[kEach];
         int rank[kEach];
 #pragma unroll
         for (int q = 0; q < kEach; ++q) {
             const uint2 c = i + 32 * q < n ? list[i + 32 * q] : make_uint2(0, 0);
-            mine[q] = (uint64_t)c.x << 32 | ~c.y;
+            mine[q] = in_order(c);
             rank[q] = 0;
         }
 #pragma unroll 4
         for (int o = 0; o < n; ++o) {
-            const uint2 c = list[o];
-            const uint64_t other = (uint64_t)c.x << 32 | ~c.y;
+            const uint64_t other = in_order(list[o]);
 #pragma unroll
             for (int q = 0; q < kEach; ++q) rank[q] += other > mine[q];
         }
@@ -437,16 +477,18 @@ __device__ __noinline__ void mend_candidates(const ScoreParams& P, uint64_t row,
     locate<DT>(P, row, T, r, lane);
     collect_in_order<DT>(T.at, r, P.top_k, floor_key, cand, &T.n_cand, lane);
 }
-__device__ __noinline__ void put_top(const ScoreParams& P, uint64_t row, const uint2* cand, TopShared& T, const Stat& all, const Final& f,
+__device__ __noinline__ void put_top(const ScoreParams& P, uint64_t row, uint2* cand, TopShared& T, const Stat& all, const Final& f,
                                      int lane) {
     const int k = P.top_k;
     uint2* const best = reinterpret_cast<uint2*>(T.ring);       // its readers are through
     static_assert(sizeof(T.ring) >= MR_MAX_TOP * sizeof(uint2), "the best k fit");
+    int n = T.n_cand;
+    if (n > kRanked) n = shorten(cand, n, k, lane);
     // A list of a warp's size spares the other entries' compares (one token with
     // 20 alternatives 10.6 us against 11.2); longer ones are read once for four
     // (2048 rows with 64: 207 us against 216 one at a time).
-    if (T.n_cand <= 32) rank_list<1>(cand, T.n_cand, k, best, lane);
-    else rank_list<4>(cand, T.n_cand, k, best, lane);
+    if (n <= 32) rank_list<1>(cand, n, k, best, lane);
+    else rank_list<4>(cand, n, k, best, lane);
 #pragma unroll 1
     for (int i = lane; i < k; i += 32) {
         const uint2 c = best[i];
