@@ -245,6 +245,31 @@ def test_top_k_ties_and_masks(mr, dtype, k, T):
         _close(o["top_lp"][t].cpu().numpy(), want[4], REL + 4 * U * 128, f"row {t}")
 
 
+@pytest.mark.parametrize("T", [7, 700])         # a row on many CTAs, and rows in turn on few
+@pytest.mark.parametrize("k", [20, 64])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_top_k_of_long_candidate_lists(mr, dtype, k, T):
+    """More scores at or above the bound than are ranked at a time, in a long row."""
+    V = 70001
+    x = _scores(67, 7, V, dtype).float()
+    x[0] = 0.0
+    x[1, 1000:1100] = x[2, :100]
+    x[1, :1000] = x[1, 1100:] = float("-inf")
+    x[2, 5000:5256] += 50.0
+    x[3, 30000:32000] += 50.0
+    x[4, ::23] = float("nan")
+    x[5] = x[5].sort()[0]
+    x[6] = (x[6] * 2).round() / 2
+    x = x.to(_dt(dtype))
+    rows = Rows(2, T, V, dtype, 0, 0, x.repeat((T + 6) // 7, 1)[:T].contiguous())
+    o = _forward(mr, rows, np.zeros(T, np.int64), 1.0, k)
+    for t in range(7):
+        want = ref.logprob_row(x[t].double().numpy(), 0, 1.0, k)
+        for u in (t, T - 7 + t):
+            assert o["top"][u].tolist() == want[3], u
+            _close(o["top_lp"][u].cpu().numpy(), want[4], REL + 4 * U * 128, f"row {u}")
+
+
 @pytest.mark.parametrize("scale", [0.7, 3.0])
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_lowest_values_at_a_scale(mr, dtype, scale):
