@@ -24,7 +24,7 @@
 // scores are over 2^8 apart in the exponent and the smaller one's term is 0:
 // any c that keeps them 2^7 apart gives the same sums, and the power of two
 // that does so neither rounds nor overflows.
-// NaN and +inf live in x_m (the maximum passes NaN on), and x_m = -inf stands
+// NaN and +inf live in x_m (the maximum passes NaN on, a new one keeps an old NaN), and x_m = -inf stands
 // for "nothing but -inf so far", where the sums stay 0.
 #pragma once
 
@@ -605,13 +605,14 @@ __device__ __forceinline__ Running start_running(float c) { return {{neg_inf(), 
 template <int DT, bool ENT>
 __device__ __forceinline__ void accumulate(Running& t, const uint32_t (&w)[16], float top, float c) {
     using S = Score<DT>;
-    if (!(top <= t.a.x)) {      // a new maximum, or NaN
-        rebase<ENT>(t.a, top, c);
-        t.f = reference(top, c);
+    if (!(top <= t.a.x)) {      // a new maximum, or NaN: in this superblock or, which stays, in one before
+        const float most = max_nan(t.a.x, top);
+        rebase<ENT>(t.a, most, c);
+        t.f = reference(most, c);
         if (ENT) {
-            t.flat = !(fabsf(__fmul_rn(top, c)) < kFlatRef);
+            t.flat = !(fabsf(__fmul_rn(most, c)) < kFlatRef);
             // 1000 in the exponent or, for the rounding to the type, 1/64 of the maximum
-            t.least = S::floor_word(__fadd_rn(top, -fmaxf(__fdiv_rn(1000.0f, c), fabsf(top) * 0.015625f)));
+            t.least = S::floor_word(__fadd_rn(most, -fmaxf(__fdiv_rn(1000.0f, c), fabsf(most) * 0.015625f)));
         }
     }
     const F2 cc = f2(t.f.c, t.f.c), off = f2(-t.f.ref, -t.f.ref);
