@@ -107,10 +107,8 @@ all_gather_kernel(const __grid_constant__ GatherParams P) {
 }
 
 cudaError_t launch_all_gather(const GatherParams& P, dim3 grid, size_t smem, cudaStream_t s) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(all_gather_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_dynamic_smem(all_gather_kernel, smem);
+    if (e != cudaSuccess) return e;
     return launch_kernel(all_gather_kernel, grid, smem, s, 0, P);
 }
 

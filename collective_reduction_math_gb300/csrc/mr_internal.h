@@ -285,6 +285,20 @@ __device__ __forceinline__ void pdl_enter() {
 }
 #endif
 
+// Most dynamic shared memory of a launch, beside up to 24 KB of static arrays
+// (227 KB a CTA in all).
+constexpr size_t kMostDynamicSmem = 200 * 1024;
+// Lets `k` have `smem` bytes of dynamic shared memory; without this a CTA has
+// 48 KB, its static arrays included.  The limit belongs to the kernel, not to
+// a launch, so every call sets it to the same bytes: one that set it to its own
+// could lower it between another host thread's call here and that thread's
+// launch, which then failed.
+template <class K>
+inline cudaError_t allow_dynamic_smem(K k, size_t smem) {
+    if (smem <= 24 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostDynamicSmem);
+}
+
 // Launch `k` on `s` with programmatic stream serialisation (when enabled)
 // and, when cluster > 0, as 1-D thread-block clusters of that many CTAs.
 template <class... Exp, class... Act>
@@ -355,11 +369,10 @@ void clear_error();
 // The forward kernels (kScoreThreads threads, clusters of P.csize).
 using ScoreKernel = void (*)(ScoreParams);
 constexpr int kScoreThreads = kThreads + 32;
-// Lets a forward kernel have clusters of C and that much dynamic shared memory
-// (48 KB without the opt-in, static arrays of up to 21 KB included).
+// Lets a forward kernel have clusters of C and `smem` bytes of dynamic shared
+// memory.
 inline cudaError_t allow_score_kernel(ScoreKernel kernel, int C, size_t smem) {
-    cudaError_t e = cudaSuccess;
-    if (smem > 27 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_dynamic_smem(kernel, smem);
     if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e;
 }

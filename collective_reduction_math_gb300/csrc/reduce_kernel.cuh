@@ -923,10 +923,8 @@ reduce_kernel(const __grid_constant__ ReduceParams P) {
 template <class K>
 cudaError_t launch_spread(K k, dim3 grid, size_t smem, cudaStream_t stream, const ReduceParams& P) {
     if (P.spread_smem > smem) smem = P.spread_smem;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_dynamic_smem(k, smem);
+    if (e != cudaSuccess) return e;
     return launch_kernel(k, grid, smem, stream, 0, P);
 }
 

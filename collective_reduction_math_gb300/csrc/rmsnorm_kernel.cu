@@ -353,10 +353,8 @@ allreduce_rmsnorm_kernel(const __grid_constant__ NormParams P) {
 template <int DT, int ALGO, int WCAP, int VB, bool PIPE>
 static cudaError_t launch_one(const NormParams& P, dim3 grid, size_t smem, cudaStream_t s) {
     auto k = allreduce_rmsnorm_kernel<DT, ALGO, WCAP, VB, PIPE>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_dynamic_smem(k, smem);
+    if (e != cudaSuccess) return e;
     return launch_kernel(k, grid, smem, s, (unsigned)P.csize, P);
 }
 

@@ -17,8 +17,6 @@ namespace {
 using mr::report_error;
 using mr::ScoreParams;
 
-constexpr size_t kMostDynamicSmem = 200 * 1024;     // of a CTA's 227 KB, beside its static arrays
-
 constexpr float kLeastScale = 5.421010862427522e-20f;       // 2^-64
 constexpr size_t kMostRows = (size_t)1 << 36, kMostStride = (size_t)1 << 40;
 
@@ -231,7 +229,7 @@ Plan plan_forward(const Call& c, mr::ScoreKernel kernel, Needs needs, double pas
         size_t bytes = 0;
         double again = 0.0;
         for (int choice = 0; needs(c, C, choice, &bytes, &again); ++choice) {
-            if (bytes > kMostDynamicSmem) continue;
+            if (bytes > mr::kMostDynamicSmem) continue;
             const int clusters = resident_clusters(dev, kernel, C, bytes);
             if (clusters < 1) continue;
             const double rounds = ceil((double)c.rows / clusters);
