@@ -17,17 +17,19 @@
 // product per place, and no quotient of small masses.
 //
 // The forward kernel streams a row's scores with 8 warps while a ninth, the row
-// warp, sets the next row up (its list as places, the teacher's mass, the listed
+// warp, sets the next row up (its list as places, the teacher's masses, the listed
 // scores) and joins the last one.  A score that is in the list becomes -inf
 // before it is summed.  With the gradient in the same call (STEP) a cluster
 // of CTAs keeps the row in shared memory: pass 1 sums it, the row warps exchange
 // their CTAs' statistics, pass 2 turns it into gradients, and as a block of
-// it is used up the next row's is copied there.
+// it is used up the next row's is copied there.  While the statistics are
+// exchanged, the stream's last warp works out the next row's masses: on the row
+// warp they kept the stream waiting (8192 x 131072 bf16 737 us against 701).
 //
-// What bounds them (GB300, bf16): the loss alone memory, 6.48 TB/s of 6.69 at
-// 4096 x 131072 with 64 entries (161 us); its gradient 5.8 TB/s (355 us at 4096 x
+// What bounds them (GB300, bf16): the loss alone memory, 6.37 TB/s of 6.69 at
+// 4096 x 131072 with 64 entries (164 us); its gradient 5.9 TB/s (349 us at 4096 x
 // 128000, 100 entries), the units' own reading of the list; loss and gradient
-// in one 5.45 TB/s (777 us at 8192 x 131072): two passes over a row cost some 460
+// in one 6.0 TB/s (705 us at 8192 x 131072): two passes over a row cost some 460
 // instructions a 2 KiB superblock, and the stream waits at each row's join.
 #include "score_kernel.cuh"
 
@@ -36,6 +38,7 @@ namespace mr {
 namespace {
 
 constexpr int kListRegs = MR_MAX_TEACHER / 32;
+constexpr int kTeacherWarp = kScoreWarps - 1;       // no warp has fewer superblocks
 constexpr uint32_t kNoPlace = ~0u;     // past every superblock: a row has fewer than 2^32 - 2^10 places
 
 // A warp's copy of a row's list: entry k = lane + 32 i, in the first `regs` of
@@ -44,7 +47,6 @@ constexpr uint32_t kNoPlace = ~0u;     // past every superblock: a row has fewer
 // 97 entries does not need is skipped, and what two steps share is kept.
 struct List {
     uint32_t place[kListRegs];      // in units of scores, counted through the row's superblocks; kNoPlace if absent
-    float v[kListRegs];             // the teacher's value; -inf if absent, NaN for a column past the vocabulary
     bool some;                      // any entry at all
 };
 template <class F>
@@ -71,74 +73,170 @@ __device__ __forceinline__ void load_raw(RawList& R, const ScoreParams& P, uint6
         }
     });
 }
-// Places, values, and by entry(i, score's address, rank, column of the rank)
-// whatever else is to be had of an entry.
+// Places, into `values` the teacher's values (-inf for no entry, NaN for a column
+// past the vocabulary), and by entry(i, score's address, rank, column of the
+// rank) whatever else is to be had of an entry.
 template <int DT, class Entry>
-__device__ __forceinline__ void place_list(List& L, const RawList& R, const ScoreParams& P, uint64_t row, int regs, Entry entry) {
+__device__ __forceinline__ void place_list(List& L, float* values, const RawList& R, const ScoreParams& P, uint64_t row, int regs, int lane,
+                                           Entry entry) {
     using S = Score<DT>;
     bool some = false;
 #pragma unroll
-    for (int i = 0; i < kListRegs; ++i) {
-        L.place[i] = kNoPlace;
-        L.v[i] = neg_inf();
-    }
+    for (int i = 0; i < kListRegs; ++i) L.place[i] = kNoPlace;
     each_reg(regs, [&](int i) {
+        float v = neg_inf();
         if (R.id[i] >= 0) {
             some = true;
-            L.v[i] = quiet_nan();
+            v = quiet_nan();
             if (R.id[i] < (long long)P.vocab) {
                 const uint32_t id = (uint32_t)R.id[i];
                 const int r = shard_of(P, id);
                 const uint32_t column = id - P.col0[r];
                 const uintptr_t start = reinterpret_cast<uintptr_t>(P.x[r]) + row * P.ld[r] * S::kBytes;
-                L.v[i] = R.v[i];
+                v = R.v[i];
                 L.place[i] = (P.sb0[r] << S::kLogSb) + column + (uint32_t)(start & 15) / S::kBytes;
                 entry(i, reinterpret_cast<const char*>(start + (uint64_t)column * S::kBytes), r, column);
             }
         }
+        values[lane + 32 * i] = v;
     });
     L.some = __any_sync(~0u, some);
 }
 
-// The teacher's side of a row.
-struct Teacher {
-    float q[kListRegs], logq[kListRegs];
-    float q_rest, Q;
+// ---- the teacher's masses, beyond fp32 ----
+// The mass outside the list is 1 - sum q: where the list holds nearly all of
+// it, sums and exponentials of fp32 would leave the rounding of q in its place
+// (a remainder of 1e-6 off by 4 to 13 %).  So an exponential is the sum of two
+// floats, and the sum over the list is one of integers.
+struct Pair {
+    float h, l;
 };
-__device__ __forceinline__ void teacher_mass(Teacher& t, const List& L, const ScoreParams& P, int regs) {
-    float total = 0.0f;
+// 2^(j/32), the part of it in a float and the rest.  The forward kernels keep
+// a copy in shared memory: a load of it from beyond took its turn behind the
+// stream's, some 1000 cycles a row of the step.
+__device__ const float2 kTwoToThe32nds[32] = {
+    {1.0f, 0.0f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f}, {0x1.11301ep+0f, -0x1.fdb496p-25f},
+    {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f}, {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f},
+    {0x1.306fep+0f, 0x1.4636e2p-25f}, {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.5342b6p+0f, -0x1.2c561p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f}, {0x1.6247ecp+0f, -0x1.f8b55p-25f},
+    {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f}, {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f},
+    {0x1.8ace54p+0f, 0x1.15506ep-27f}, {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b7f77p+0f, -0x1.a09438p-25f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f}, {0x1.cb720ep+0f, -0x1.8837ccp-27f},
+    {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f}, {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.f50766p+0f, -0x1.246ebp-26f},
+};
+// e^(h + l) (l is small beside h) to 2^-33 relative.  Table-driven (P. T. P. Tang, Table-driven
+// implementation of the exponential function, 1989): h + l = k ln 2 / 32 + r,
+// e^r - 1 by its series, as |r| < 0.011.  0 below e^-87, NaN for NaN.
+__device__ __forceinline__ Pair exp_pair(float h, float l, const float2* two_to_the_32nds) {
+    constexpr float kRound = 12582912.0f;       // 1.5 * 2^23: an fp32 sum with it is rounded to a whole number
+    constexpr float kLn2 = 0x1.62e43p-6f, kLn2Rest = -0x1.05c61p-34f;       // ln 2 / 32
+    const float x = h < -88.0f ? -88.0f : h > 89.0f ? 89.0f : h;
+    const float shifted = __fmaf_rn(x, 46.166241f, kRound), k = __fadd_rn(shifted, -kRound);
+    const int i = __float_as_int(shifted) - __float_as_int(kRound);
+    const float2 t = two_to_the_32nds[i & 31];
+    // x - k ln 2 / 32, what the product and the difference lost put back
+    const float p = __fmul_rn(k, kLn2), p_low = __fmaf_rn(k, kLn2, -p), d = __fadd_rn(x, -p);
+    const float r = __fadd_rn(d, -p_low), r_low = __fmaf_rn(-k, kLn2Rest, __fadd_rn(__fadd_rn(__fadd_rn(d, -r), -p_low), l));
+    const float series = __fmaf_rn(__fmul_rn(r, r), __fmaf_rn(r, __fmaf_rn(r, 0.041666667f, 0.16666667f), 0.5f), __fmaf_rn(r_low, r, r_low));
+    const float a = __fmul_rn(t.x, r), a_low = __fmaf_rn(t.x, r, -a), e = __fadd_rn(t.x, a);
+    const float low = __fadd_rn(__fadd_rn(__fadd_rn(t.x, -e), a), __fadd_rn(a_low, __fmaf_rn(t.x, series, __fmaf_rn(t.y, r, t.y))));
+    const float whole = __fadd_rn(e, low), rest = __fadd_rn(low, -__fadd_rn(whole, -e));
+    const float scale = x < -87.0f ? 0.0f : __int_as_float(((i >> 5) + 127) << 23);
+    return {__fmul_rn(whole, scale), __fmul_rn(rest, scale)};
+}
+// The sum of masses, in units of 2^-20 and of 2^-42 (at most 128 of them, none
+// over 2).  A sum with 1.5 * 2^(n + 23) is rounded to whole units of 2^n, which
+// its last bits then count: no conversion, whose unit the 2^x of the stream
+// keeps busy.
+struct MassSum {
+    int high = 0, low = 0;
+    __device__ __forceinline__ void add(Pair q) {
+        constexpr float kHigh = 12.0f, kLow = 0x1.8p-19f;
+        const float h = __fadd_rn(q.h, kHigh), l = __fadd_rn(__fadd_rn(__fadd_rn(q.h, -__fadd_rn(h, -kHigh)), q.l), kLow);
+        high += __float_as_int(h) - __float_as_int(kHigh);
+        low += __float_as_int(l) - __float_as_int(kLow);
+    }
+    __device__ __forceinline__ void over_warp() {
+        high = __reduce_add_sync(~0u, high);
+        low = __reduce_add_sync(~0u, low);
+    }
+};
+
+// The teacher's side of a row: its masses, what they leave, and what log q is
+// made of.  It lives in shared memory and is worked out by one warp, entry
+// k = lane + 32 i after the other: unrolled, its registers crowd the stream's,
+// and what spills to local memory takes its turn behind the stream's stores (a
+// row of the step 4000 cycles longer).
+struct Teacher {
+    float v[MR_MAX_TEACHER], q[MR_MAX_TEACHER], low[MR_MAX_TEACHER];
+    float2 rest;            // q_rest and Q,
+    float2 log_terms;       // ref and log_total
+};
+// log q is the value (the tail mode) or teacher_scale (value - ref) - log_total.
+__device__ __forceinline__ float log_mass(float v, float2 terms, const ScoreParams& P) {
+    return P.tail ? v : __fadd_rn(__fmul_rn(__fadd_rn(v, -terms.x), P.teacher_scale), -terms.y);
+}
+// From the values (of 32 regs entries) the rest.
+__device__ __forceinline__ void teacher_mass(Teacher& T, const ScoreParams& P, int regs, const float2* powers, int lane) {
+    MassSum sum;
+    const int end = lane + 32 * regs;
     if (P.tail) {
-        each_reg(regs, [&](int i) {
-            t.logq[i] = L.v[i];
-            t.q[i] = expf(L.v[i]);
-            total = __fadd_rn(total, t.q[i]);
-        });
-        const float rest = __fadd_rn(1.0f, -warp_sum(total));
-        t.q_rest = rest < 0.0f ? 0.0f : rest;
-        t.Q = rest < 0.0f ? __fadd_rn(1.0f, -rest) : rest == rest ? 1.0f : rest;
+        bool odd = false;       // no log probability: its mass is over 2, or NaN
+#pragma unroll 1
+        for (int k = lane; k < end; k += 32) {
+            const Pair q = exp_pair(T.v[k], 0.0f, powers);
+            T.q[k] = q.h;
+            odd |= !(q.h <= 2.0f);
+            sum.add(q);
+        }
+        sum.over_warp();
+        float rest = __fmaf_rn((float)sum.low, -0x1p-42f, __fmul_rn((float)((1 << 20) - sum.high), 0x1p-20f));
+        if (__any_sync(~0u, odd)) {
+            float total = 0.0f;
+#pragma unroll 1
+            for (int k = lane; k < end; k += 32) total = __fadd_rn(total, T.q[k]);
+            rest = __fadd_rn(1.0f, -warp_sum(total));
+        }
+        if (lane == 0) {
+            T.rest = make_float2(rest < 0.0f ? 0.0f : rest, rest < 0.0f ? __fadd_rn(1.0f, -rest) : rest == rest ? 1.0f : rest);
+            T.log_terms = make_float2(0.0f, 0.0f);
+        }
     } else {
         float m = neg_inf();
-        each_reg(regs, [&](int i) {
-            t.logq[i] = __fmul_rn(L.v[i], P.teacher_scale);
-            m = max_nan(m, t.logq[i]);
-        });
+#pragma unroll 1
+        for (int k = lane; k < end; k += 32) m = max_nan(m, T.v[k]);
         m = redux_max_nan(m);
         const float ref = m == neg_inf() ? 0.0f : m;
-        each_reg(regs, [&](int i) {
-            t.logq[i] = __fadd_rn(t.logq[i], -ref);
-            t.q[i] = expf(t.logq[i]);
-            total = __fadd_rn(total, t.q[i]);
-        });
-        total = warp_sum(total);
+#pragma unroll 1
+        for (int k = lane; k < end; k += 32) {
+            // teacher_scale (v - m), what the difference and the product lost put back
+            const float v = T.v[k], d = __fadd_rn(v, -ref), from_v = __fadd_rn(d, -v);
+            const float d_low = __fadd_rn(__fadd_rn(v, -__fadd_rn(d, -from_v)), -__fadd_rn(ref, from_v));
+            const float y = __fmul_rn(d, P.teacher_scale);
+            // no low part where there is no mass: -inf, or out of range
+            const float low = y < -88.0f ? 0.0f : __fmaf_rn(d_low, P.teacher_scale, __fmaf_rn(d, P.teacher_scale, -y));
+            const Pair q = exp_pair(y, low, powers);
+            T.q[k] = q.h;
+            T.low[k] = q.l;
+            sum.add(q);
+        }
+        sum.over_warp();
         const bool none = m == neg_inf();
-        const float log_total = none ? 0.0f : logf(total), inv = none ? 0.0f : __fdiv_rn(1.0f, total);
-        each_reg(regs, [&](int i) {
-            t.logq[i] = __fadd_rn(t.logq[i], -log_total);
-            t.q[i] = __fmul_rn(t.q[i], inv);
-        });
-        t.q_rest = 0.0f;
-        t.Q = none ? 0.0f : m == m ? 1.0f : m;
+        const float high = __fmul_rn((float)sum.high, 0x1p-20f), total = __fmaf_rn((float)sum.low, 0x1p-42f, high);
+        const float total_low = __fmaf_rn((float)sum.low, 0x1p-42f, __fadd_rn(high, -total));
+        const float inv = none ? 0.0f : m == m ? __fdiv_rn(1.0f, total) : m;
+#pragma unroll 1
+        for (int k = lane; k < end; k += 32) {
+            // the quotient of the two sums, rounded once
+            const float h = T.q[k], x = __fmul_rn(h, inv);
+            T.q[k] = __fmaf_rn(inv, __fadd_rn(__fmaf_rn(-x, total, h), __fmaf_rn(-x, total_low, T.low[k])), x);
+        }
+        if (lane == 0) {
+            T.rest = make_float2(0.0f, none ? 0.0f : m == m ? 1.0f : m);
+            T.log_terms = make_float2(ref, none ? 0.0f : logf(total));
+        }
     }
+    __syncwarp();
 }
 
 // The rounds (every `step`-th superblock from `first`, up to `end`) in which an
@@ -232,6 +330,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
     __shared__ uint32_t s_mask[2][STEP ? MR_MAX_TEACHER : 1];       // STEP: where the entries lie in the cache,
     __shared__ char* s_out[2][STEP ? MR_MAX_TEACHER : 1];           // and in the gradients of this CTA's part
     __shared__ Coef s_coef;
+    __shared__ Teacher s_teacher[2];
+    __shared__ float2 powers[32];           // kTwoToThe32nds, the row warp's copy
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int C = P.csize, crank = C > 1 ? (int)cluster_rank() : 0;
@@ -245,6 +345,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
         counted_init(&step_bar[1]);
     }
     if (C > 1) cluster_arrive();        // every CTA of the cluster has started: waited for before the first store to a peer
+    if (warp == kScoreWarps) powers[lane] = kTwoToThe32nds[lane];
     pdl_enter();
 
     if (warp < kScoreWarps) {
@@ -269,8 +370,9 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
         }
         bool waited = C == 1;
         int parity = 0;
+        if (STEP && row < P.rows) bar_sync(kRowReady);
         for (uint32_t count = 0; row < P.rows; row += stride, parity ^= 1, ++count) {
-            bar_sync(kRowReady + parity);
+            if (!STEP) bar_sync(kRowReady + parity);
             const bool out = row_out[parity];
             const uint32_t first = STEP ? sb_lo + warp : first_superblock(sb_lo, warp, count);
             List L;
@@ -337,14 +439,18 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             }
             if constexpr (STEP) {
                 Coef coef{P.c, 0.0f, 0.0f};
+                const uint64_t next_row = row + stride;
+                const bool more = next_row < P.rows;
+                if (more) {
+                    bar_sync(kRowReady + (parity ^ 1));
+                    if (warp == kTeacherWarp) teacher_mass(s_teacher[parity ^ 1], P, regs, powers, lane);
+                }
                 bar_sync(kRowStep);
                 if (!out) coef = s_coef;
                 // The next row's copies go into the blocks as they empty.
                 Walk<DT> ahead;
                 walk = Walk<DT>{};
                 Output<DT> to;
-                const uint64_t next_row = row + stride;
-                const bool more = next_row < P.rows;
                 uint32_t sb = first;
                 for (uint32_t i = 0; i < rounds; ++i, sb += kScoreWarps) {
                     if (walk.seek(P, row, sb, lane)) to.follow(P, row, walk, lane);
@@ -401,7 +507,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             x_next[i] = neg_inf();
             if (STEP) s_out[par][lane + 32 * i] = nullptr;
         });
-        place_list<DT>(next, raw, P, r, regs, [&](int i, const char* score, int rank, uint32_t column) {
+        place_list<DT>(next, s_teacher[par].v, raw, P, r, regs, lane, [&](int i, const char* score, int rank, uint32_t column) {
             if (joins) x_next[i] = S::load_one(score);
             if (STEP) {
                 const uint32_t sb = next.place[i] >> S::kLogSb;
@@ -421,9 +527,11 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
         bar_arrive(kRowReady + par);
         if (r + stride < P.rows) load_raw(raw, P, r + stride, regs, lane);
     };
+    __syncwarp();       // of the lanes' entries of powers
     if (row < P.rows) {
         load_raw(raw, P, row, regs, lane);
         set_up(row, 0);
+        if (STEP) teacher_mass(s_teacher[0], P, regs, powers, lane);       // the stream has no wait yet
     }
     if (C > 1) cluster_wait();
     int parity = 0;
@@ -434,12 +542,12 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
         for (int i = 0; i < kListRegs; ++i) x[i] = x_next[i];
         if (row + stride < P.rows) set_up(row + stride, parity ^ 1);
         const bool out = !cur.some;
-        Teacher t;
+        const Teacher& t = s_teacher[parity];
         Stat l{neg_inf(), 0.0f, 0.0f};      // the listed scores, as one more statistic
         float g = 0.0f;
         if (joins && !out) {
             if (STEP) g = __fmul_rn(P.scale, P.g_row[row]);
-            teacher_mass(t, cur, P, regs);
+            else teacher_mass(s_teacher[parity], P, regs, powers, lane);
             each_reg(regs, [&](int i) { l.x = max_nan(l.x, x[i]); });
             l.x = redux_max_nan(l.x);
             if (l.x != neg_inf()) {
@@ -488,6 +596,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             }
             continue;
         }
+        const float q_rest = t.rest.x, Q = t.rest.y;
         Stat all{max_nan(b.x, l.x), 0.0f, 0.0f}, r = b;
         rebase<false>(r, all.x, P.c);
         rebase<false>(l, all.x, P.c);
@@ -499,7 +608,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             const float inv = fabsf(y) < __int_as_float(0x7f800000) ? reciprocal(all.s) : y == neg_inf() ? 0.0f : quiet_nan();
             if (lane == 0) {
                 const Ref k = reference(b.x, P.c);
-                const float mass = __fmul_rn(g, __fmaf_rn(__fmul_rn(r.s, inv), t.Q, -t.q_rest));
+                const float mass = __fmul_rn(g, __fmaf_rn(__fmul_rn(r.s, inv), Q, -q_rest));
                 s_coef = {k.c, k.ref, __fmul_rn(b.x, P.scale) == neg_inf() ? 0.0f : __fmul_rn(__fmul_rn(mass, reciprocal(b.s)), undo(k))};
             }
             bar_arrive(kRowStep);
@@ -508,7 +617,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             each_reg(regs, [&](int i) {
                 listed_at[i] = s_out[parity][lane + 32 * i];
                 const float p = __fmul_rn(ex2(__fmul_rn(__fadd_rn(x[i], -all.x), P.c)), inv);
-                listed[i] = __fmul_rn(x[i], P.scale) == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(p, t.Q, -t.q[i]));
+                listed[i] = __fmul_rn(x[i], P.scale) == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(p, Q, -t.q[lane + 32 * i]));
             });
         }
         if (crank != 0) continue;
@@ -517,10 +626,11 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                               : __fmaf_rn(__fadd_rn(b.x, -all.x), P.scale, __fadd_rn(rest.log_s, -f.log_s));
         float loss = 0.0f;
         each_reg(regs, [&](int i) {
-            if (!(t.q[i] == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q[i], __fadd_rn(t.logq[i], -log_prob(x[i], all, f, P.scale))));
+            const float q = t.q[lane + 32 * i], logq = log_mass(t.v[lane + 32 * i], t.log_terms, P);
+            if (!(q == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(q, __fadd_rn(logq, -log_prob(x[i], all, f, P.scale))));
         });
         loss = warp_sum(loss);
-        if (!(t.q_rest == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(t.q_rest, __fadd_rn(logf(t.q_rest), -logp_rest)));
+        if (!(q_rest == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(q_rest, __fadd_rn(logf(q_rest), -logp_rest)));
         if (lane == 0) {
             if (P.loss) P.loss[row] = loss;
             if (P.stats) {
@@ -544,10 +654,12 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_constant__ ScoreParams P) {
     using S = Score<DT>;
+    __shared__ Teacher teachers[kScoreWarps];
     const int lane = threadIdx.x & 31;
     const uint32_t nsb = P.sb0[P.W];
     const uint64_t units = P.rows * (uint64_t)P.parts;
     const int regs = (P.K + 31) / 32;
+    Teacher& t = teachers[threadIdx.x >> 5];
     pdl_enter();
     for (uint64_t unit = (uint64_t)blockIdx.x * kScoreWarps + (threadIdx.x >> 5); unit < units;
          unit += (uint64_t)gridDim.x * kScoreWarps) {
@@ -558,16 +670,16 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
         load_raw(raw, P, row, regs, lane);
         List L{};
         uint32_t bits = 0;
-        place_list<DT>(L, raw, P, row, regs, [&](int i, const char*, int, uint32_t) {
+        __syncwarp();
+        place_list<DT>(L, t.v, raw, P, row, regs, lane, [&](int i, const char*, int, uint32_t) {
             const uint32_t sb = L.place[i] >> S::kLogSb;
             if (sb >= sb_lo && sb < sb_hi) bits |= 1u << (sb - sb_lo);
         });
         const uint32_t entries = __reduce_or_sync(~0u, bits);      // superblocks of the unit that hold some
         Coef coef{P.c, 0.0f, 0.0f};
         float m = 0.0f, logs = 0.0f, g = 0.0f;
-        Teacher t;
         if (L.some) {
-            teacher_mass(t, L, P, regs);
+            teacher_mass(t, P, regs, kTwoToThe32nds, lane);
             m = P.stats_in[4 * row];
             logs = P.stats_in[4 * row + 1];
             const float m_rest = P.stats_in[4 * row + 2], logs_rest = P.stats_in[4 * row + 3];
@@ -575,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
             if (m_rest != neg_inf()) {
                 const SavedRef k = saved_reference<DT>(m_rest, P.scale, P.c);
                 const float p_rest = expf(__fadd_rn(__fadd_rn(m_rest, -m), __fadd_rn(logs_rest, -logs)));
-                coef = {k.f.c, k.f.ref, __fmul_rn(__fmul_rn(g, __fmaf_rn(p_rest, t.Q, -t.q_rest)),
+                coef = {k.f.c, k.f.ref, __fmul_rn(__fmul_rn(g, __fmaf_rn(p_rest, t.rest.y, -t.rest.x)),
                                                   __fmul_rn(expf(__fadd_rn(k.rho, -logs_rest)), undo(k.f)))};
             }
         }
@@ -601,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
                     if ((L.place[i] >> S::kLogSb) == sb) {
                         const float x = S::load_one(walk.address(sb) - lane * 16 + offset(L.place[i]));
                         const float p = exp_near(__fadd_rn(__fmaf_rn(x, P.scale, -m), -logs));
-                        if (__fmul_rn(x, P.scale) != neg_inf()) listed[i] = __fmul_rn(g, __fmaf_rn(p, t.Q, -t.q[i]));
+                        if (__fmul_rn(x, P.scale) != neg_inf()) listed[i] = __fmul_rn(g, __fmaf_rn(p, t.rest.y, -t.q[lane + 32 * i]));
                     }
                 });
                 __syncwarp();

@@ -285,7 +285,7 @@ __device__ __forceinline__ void pdl_enter() {
 }
 #endif
 
-// Most dynamic shared memory of a launch, beside up to 24 KB of static arrays
+// Most dynamic shared memory of a launch, beside up to 27 KB of static arrays
 // (227 KB a CTA in all).
 constexpr size_t kMostDynamicSmem = 200 * 1024;
 // Lets `k` have `smem` bytes of dynamic shared memory; without this a CTA has
@@ -295,7 +295,7 @@ constexpr size_t kMostDynamicSmem = 200 * 1024;
 // launch, which then failed.
 template <class K>
 inline cudaError_t allow_dynamic_smem(K k, size_t smem) {
-    if (smem <= 24 * 1024) return cudaSuccess;
+    if (smem <= 21 * 1024) return cudaSuccess;
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostDynamicSmem);
 }
 
