@@ -29,7 +29,7 @@
 // What bounds them (GB300, bf16): the loss alone memory, 6.37 TB/s of 6.69 at
 // 4096 x 131072 with 64 entries (164 us); its gradient 5.9 TB/s (349 us at 4096 x
 // 128000, 100 entries), the units' own reading of the list; loss and gradient
-// in one 6.0 TB/s (705 us at 8192 x 131072): two passes over a row cost some 460
+// in one 6.0 TB/s (701 us at 8192 x 131072): two passes over a row cost some 460
 // instructions a 2 KiB superblock, and the stream waits at each row's join.
 #include "score_kernel.cuh"
 
@@ -328,7 +328,10 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
     __shared__ uint32_t s_place[2][MR_MAX_TEACHER];
     __shared__ int row_out[2];              // the row is left out
     __shared__ uint32_t s_mask[2][STEP ? MR_MAX_TEACHER : 1];       // STEP: where the entries lie in the cache,
-    __shared__ char* s_out[2][STEP ? MR_MAX_TEACHER : 1];           // and in the gradients of this CTA's part
+    // and in the gradients of this CTA's part: the last row's are stored when the
+    // stream's vector stores of that row are done, while the next but one is set up
+    __shared__ char* s_out[3][STEP ? MR_MAX_TEACHER : 1];
+    __shared__ float s_listed[STEP ? MR_MAX_TEACHER : 1];
     __shared__ Coef s_coef;
     __shared__ Teacher s_teacher[2];
     __shared__ float2 powers[32];           // kTwoToThe32nds, the row warp's copy
@@ -485,34 +488,26 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
     RawList raw;        // the list after the one in `cur` / `next`
     List cur{}, next{};
     float x[kListRegs], x_next[kListRegs];
-    // STEP: the last row's listed gradients of this CTA's part, stored when the
-    // stream's vector stores of that row are done
-    char* listed_at[kListRegs];
-    float listed[kListRegs];
 #pragma unroll
-    for (int i = 0; i < kListRegs; ++i) {
-        listed[i] = 0.0f;
-        listed_at[i] = nullptr;
-        x_next[i] = neg_inf();
-    }
-    auto store_listed = [&] {
+    for (int i = 0; i < kListRegs; ++i) x_next[i] = neg_inf();
+    auto store_listed = [&](int slot) {
         each_reg(regs, [&](int i) {
-            if (listed_at[i]) S::store_one(listed_at[i], listed[i]);
-            listed_at[i] = nullptr;
+            char* const to = s_out[slot][lane + 32 * i];
+            if (to) S::store_one(to, s_listed[lane + 32 * i]);
         });
     };
     // Sets a row up: places for the stream, and the listed scores.
-    auto set_up = [&](uint64_t r, int par) {
+    auto set_up = [&](uint64_t r, int par, int slot) {
         each_reg(regs, [&](int i) {
             x_next[i] = neg_inf();
-            if (STEP) s_out[par][lane + 32 * i] = nullptr;
+            if (STEP) s_out[slot][lane + 32 * i] = nullptr;
         });
         place_list<DT>(next, s_teacher[par].v, raw, P, r, regs, lane, [&](int i, const char* score, int rank, uint32_t column) {
             if (joins) x_next[i] = S::load_one(score);
             if (STEP) {
                 const uint32_t sb = next.place[i] >> S::kLogSb;
                 if (sb >= sb_lo && sb < sb_hi)
-                    s_out[par][lane + 32 * i] = static_cast<char*>(P.g[rank]) + (r * P.ldg[rank] + column) * S::kBytes;
+                    s_out[slot][lane + 32 * i] = static_cast<char*>(P.g[rank]) + (r * P.ldg[rank] + column) * S::kBytes;
             }
         });
         each_reg(regs, [&](int i) {
@@ -530,17 +525,19 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
     __syncwarp();       // of the lanes' entries of powers
     if (row < P.rows) {
         load_raw(raw, P, row, regs, lane);
-        set_up(row, 0);
+        set_up(row, 0, 0);
         if (STEP) teacher_mass(s_teacher[0], P, regs, powers, lane);       // the stream has no wait yet
     }
     if (C > 1) cluster_wait();
     int parity = 0;
     uint32_t turn = 0;      // of the two counted barriers
+    int slot = 0, last = -1;        // of s_out: this row's and the last one's
     for (; row < P.rows; row += stride, parity ^= 1) {
+        const int after = slot == 2 ? 0 : slot + 1;
         cur = next;
 #pragma unroll
         for (int i = 0; i < kListRegs; ++i) x[i] = x_next[i];
-        if (row + stride < P.rows) set_up(row + stride, parity ^ 1);
+        if (row + stride < P.rows) set_up(row + stride, parity ^ 1, after);
         const bool out = !cur.some;
         const Teacher& t = s_teacher[parity];
         Stat l{neg_inf(), 0.0f, 0.0f};      // the listed scores, as one more statistic
@@ -592,7 +589,9 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             }
             if (STEP) {
                 bar_arrive(kRowStep);
-                store_listed();
+                if (last >= 0) store_listed(last);
+                last = slot;
+                slot = after;
             }
             continue;
         }
@@ -613,11 +612,12 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             }
             bar_arrive(kRowStep);
             // the row before: its vector stores were done when the stream came to this one
-            store_listed();
+            if (last >= 0) store_listed(last);
+            last = slot;
+            slot = after;
             each_reg(regs, [&](int i) {
-                listed_at[i] = s_out[parity][lane + 32 * i];
-                const float p = __fmul_rn(ex2(__fmul_rn(__fadd_rn(x[i], -all.x), P.c)), inv);
-                listed[i] = __fmul_rn(x[i], P.scale) == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(p, Q, -t.q[lane + 32 * i]));
+                const float p = __fmul_rn(exp_near(__fmul_rn(__fadd_rn(x[i], -all.x), P.scale)), inv);     // as the gradient's own call
+                s_listed[lane + 32 * i] = __fmul_rn(x[i], P.scale) == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(p, Q, -t.q[lane + 32 * i]));
             });
         }
         if (crank != 0) continue;
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
     }
     if (STEP) {
         bar_sync(kRowHelped);
-        store_listed();
+        if (last >= 0) store_listed(last);
         if (C > 1) {
             cluster_arrive_relaxed();
             cluster_wait();

@@ -83,18 +83,20 @@ __device__ __forceinline__ float redux_max_nan(float v) {
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-// e^x to some 2^-22 relative: the product's rounding, |x| 2^-24, is put back.
+// e^x to some 2^-22 relative: what the product lost is put back, its rounding
+// and that of log2 e, up to |x| 2^-24 each.
 __device__ __forceinline__ float exp_near(float x) {
-    constexpr float kLog2e = 1.4426950408889634f;
+    constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.925963e-8f;
     float h = __fmul_rn(x, kLog2e);
     if (h < kFarBelow) h = kFarBelow;       // NaN stays
-    const float lost = __fmaf_rn(x, kLog2e, -h), e = ex2(h);
+    const float lost = __fmaf_rn(x, kLog2eRest, __fmaf_rn(x, kLog2e, -h)), e = ex2(h);
     return e == 0.0f ? 0.0f : __fmaf_rn(e, __fmul_rn(lost, 0.69314718f), e);
 }
+// 1 / x for x of the size of a sum of exponentials: an estimate and a Newton step.
 __device__ __forceinline__ float reciprocal(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
+    return __fmaf_rn(__fmaf_rn(-x, r, 1.0f), r, r);
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;

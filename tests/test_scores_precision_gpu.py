@@ -80,3 +80,29 @@ def test_masses_are_rounded_once(mr, K, tail):  # noqa: F811
         for t in range(T):
             q = ref.teacher(val[t].astype(np.float64), tail, t_scale)[1]
             _close(grad[t][ids[t]], -q, q * (U + 2.0 ** -31) + TINY["fp32"], f"{which} row {t}")
+
+
+@pytest.mark.parametrize("K", [20, 128])
+def test_listed_probabilities_far_below_the_best(mr, K):  # noqa: F811
+    """Listed places without a teacher's mass, of scores down to 60 below the
+    row's only large one: their gradient is p.  The difference from the best
+    score is exact here, and so is the row's sum but for u; the exponential is
+    off by 2^-22, by the rounding of the log sum that the gradient is given
+    (u, of e^-60 and less here) and by that of its argument's last step."""
+    import torch
+    T, V = 4, 1500
+    rng = np.random.default_rng(K)
+    ids = np.stack([1 + rng.permutation(V - 1)[:K] for _ in range(T)]).astype(np.int64)
+    x = np.full((T, V), -64.0)
+    x[:, 0] = 0.0
+    np.put_along_axis(x, ids, -np.round(rng.uniform(20, 60, (T, K)) * 4096) / 4096, 1)
+    val = np.full((T, K), -np.inf, np.float32)
+    val[:, 0] = 0.0
+    rows = Rows(1, T, V, "fp32", fill=torch.from_numpy(x).float())
+    res = [ref.distill_row(x[t], ids[t], val[t].astype(np.float64), 1.0, False, 1.0, 1.0) for t in range(T)]
+    stats = np.array([r[1] for r in res])
+    for which, _, grad in _step_and_grad(mr, rows, T, V, 1, "fp32", ids, val, np.ones(T, np.float32), stats.astype(np.float32),
+                                         mode="renorm"):
+        for t in range(T):
+            want = res[t][2][ids[t][1:]]
+            _close(grad[t][ids[t][1:]], want, np.abs(want) * (2.0 ** -22 + 4 * U), f"{which} row {t}")
