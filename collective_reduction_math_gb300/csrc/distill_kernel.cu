@@ -39,6 +39,11 @@ namespace {
 
 constexpr int kListRegs = MR_MAX_TEACHER / 32;
 constexpr int kTeacherWarp = kScoreWarps - 1;       // no warp has fewer superblocks
+// What up to 128 fp32 log probabilities may lack of 1, or have over it, by their
+// rounding and that of the log sum they were taken from: 128 additions' u each,
+// the exponentials' 2^-22 and the rounding of their arguments, 2^-22 a nat of
+// entropy (at most 4.9 over 128 places): below 2^-18.
+constexpr float kRoundingMass = 0x1p-18f;
 constexpr uint32_t kNoPlace = ~0u;     // past every superblock: a row has fewer than 2^32 - 2^10 places
 
 // A warp's copy of a row's list: entry k = lane + 32 i, in the first `regs` of
@@ -630,7 +635,10 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             if (!(q == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(q, __fadd_rn(logq, -log_prob(x[i], all, f, P.scale))));
         });
         loss = warp_sum(loss);
-        if (!(q_rest == 0.0f)) loss = __fadd_rn(loss, __fmul_rn(q_rest, __fadd_rn(logf(q_rest), -logp_rest)));
+        // Against a student with no place outside the list, what the rounding of the
+        // given log probabilities leaves of 1 is no mass: the loss would be +inf or
+        // not by their last bits.
+        if (!(q_rest <= (rest.m == neg_inf() ? kRoundingMass : 0.0f))) loss = __fadd_rn(loss, __fmul_rn(q_rest, __fadd_rn(logf(q_rest), -logp_rest)));
         if (lane == 0) {
             if (P.loss) P.loss[row] = loss;
             if (P.stats) {

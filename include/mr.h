@@ -321,7 +321,10 @@ mr_status_t mr_logprob_grad(const void* const* logits, const size_t* ld, int W, 
  *     mass q_R = max(0, 1 - sum q) is one more outcome, against the student's
  *     mass p_R outside the list.
  *   loss[t] = sum q (log q - log p) [+ q_R (log q_R - log p_R)], 0 log 0 = 0;
- *     +inf where the student has masked a place with q > 0.
+ *     +inf where the student has masked a place with q > 0.  Where the student
+ *     has no place outside the list (masked, or the list is the vocabulary), a
+ *     q_R of up to 2^-18 is the rounding of the given log probabilities and
+ *     counts as 0; a larger one makes the loss +inf.
  *   stats[4t..]: m and lse - m over the row, then over the places outside the
  *     list: what mr_distill_topk_grad takes.  Loss or stats may be NULL.
  * A row with no entry is left out: not read, loss 0, stats (-inf, 0, -inf, 0),

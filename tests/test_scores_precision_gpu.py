@@ -106,3 +106,46 @@ def test_listed_probabilities_far_below_the_best(mr, K):  # noqa: F811
         for t in range(T):
             want = res[t][2][ids[t][1:]]
             _close(grad[t][ids[t][1:]], want, np.abs(want) * (2.0 ** -22 + 4 * U), f"{which} row {t}")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V,K", [(4000, 20), (4000, 128), (20, 20), (64, 64)])
+def test_list_of_all_that_is_left(mr, dtype, V, K):  # noqa: F811
+    """Teacher and student under one mask that leaves at most K places, the list
+    from mr_logprob: what its log probabilities lack of 1 is their rounding,
+    and the loss is finite.  A list that leaves a real remainder is +inf."""
+    import torch
+    T, k = 60, min(K, 64)
+    rng = np.random.default_rng(V + K)
+    x, teacher = rng.normal(0, 3, (2, T, V))
+    for t in range(T):
+        if V > K:
+            left = rng.permutation(V)[:1 + t % k]
+            mask = np.ones(V, bool)
+            mask[left] = False
+            x[t, mask] = teacher[t, mask] = -np.inf
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    x, teacher = torch.from_numpy(x).to(dt), torch.from_numpy(teacher).to(dt)
+    ids = torch.full((T, K), -1, dtype=torch.int64, device="cuda")
+    val = torch.zeros(T, K, device="cuda")
+    top, top_lp = torch.empty(T, k, dtype=torch.int64, device="cuda"), torch.empty(T, k, device="cuda")
+    mr.mr_logprob(Rows(2, T, V, dtype, fill=teacher).views, top_ids=top, top_logprob=top_lp)
+    ids[:, :k], val[:, :k] = top, top_lp
+    ids, val = ids.cpu().numpy(), val.cpu().numpy()
+    xs, rows = x.double().numpy(), Rows(2, T, V, dtype, fill=x)
+    g = np.ones(T, np.float32)
+    want, size, lacks = np.zeros(T), np.zeros(T), []
+    for t in range(T):
+        q = np.exp(val[t, :k].astype(np.float64))
+        on, lp = q > 0, ref.log_softmax(xs[t])
+        terms = q[on] * (val[t, :k].astype(np.float64)[on] - lp[ids[t, :k]][on])
+        want[t], size[t] = terms.sum(), (q[on] * (np.abs(val[t, :k][on]) + np.abs(lp[ids[t, :k]][on]) + 1)).sum()
+        lacks.append(1 - q.sum())
+    assert max(lacks) > 0 and np.abs(lacks).max() < 2.0 ** -18
+    for which in ("forward", "step"):
+        loss, _ = _run_distill(mr, which, rows, Rows(2, T, V, dtype), ids, val, g, None, mode="tail")
+        _close(loss, want, 2 * REL * size, which)
+    low = np.where(val > -np.inf, val - np.float32(0.01), val)
+    for which in ("forward", "step"):
+        loss, _ = _run_distill(mr, which, rows, Rows(2, T, V, dtype), ids, low, g, None, mode="tail")
+        assert (loss == np.inf).all(), which
