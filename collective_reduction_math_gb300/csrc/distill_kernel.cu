@@ -613,7 +613,9 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             if (lane == 0) {
                 const Ref k = reference(b.x, P.c);
                 const float mass = __fmul_rn(g, __fmaf_rn(__fmul_rn(r.s, inv), Q, -q_rest));
-                s_coef = {k.c, k.ref, __fmul_rn(b.x, P.scale) == neg_inf() ? 0.0f : __fmul_rn(__fmul_rn(mass, reciprocal(b.s)), undo(k))};
+                const float none_left = inv == inv ? 0.0f : inv;        // every place there is masked; NaN in a row of NaN
+                s_coef = {k.c, k.ref,
+                          __fmul_rn(b.x, P.scale) == neg_inf() ? none_left : __fmul_rn(__fmul_rn(mass, reciprocal(b.s)), undo(k))};
             }
             bar_arrive(kRowStep);
             // the row before: its vector stores were done when the stream came to this one
@@ -622,7 +624,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             slot = after;
             each_reg(regs, [&](int i) {
                 const float p = __fmul_rn(exp_near(__fmul_rn(__fadd_rn(x[i], -all.x), P.scale)), inv);     // as the gradient's own call
-                s_listed[lane + 32 * i] = __fmul_rn(x[i], P.scale) == neg_inf() ? 0.0f : __fmul_rn(g, __fmaf_rn(p, Q, -t.q[lane + 32 * i]));
+                const bool no_part = __fmul_rn(x[i], P.scale) == neg_inf() && inv == inv;
+                s_listed[lane + 32 * i] = no_part ? 0.0f : __fmul_rn(g, __fmaf_rn(p, Q, -t.q[lane + 32 * i]));
             });
         }
         if (crank != 0) continue;
@@ -697,6 +700,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
                 const float p_rest = expf(__fadd_rn(__fadd_rn(m_rest, -m), __fadd_rn(logs_rest, -logs)));
                 coef = {k.f.c, k.f.ref, __fmul_rn(__fmul_rn(g, __fmaf_rn(p_rest, t.rest.y, -t.rest.x)),
                                                   __fmul_rn(expf(__fadd_rn(k.rho, -logs_rest)), undo(k.f)))};
+            } else if (m != m) {
+                coef.coef = m;
             }
         }
         Walk<DT> walk;
@@ -721,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
                     if ((L.place[i] >> S::kLogSb) == sb) {
                         const float x = S::load_one(walk.address(sb) - lane * 16 + offset(L.place[i]));
                         const float p = exp_near(__fadd_rn(__fmaf_rn(x, P.scale, -m), -logs));
-                        if (__fmul_rn(x, P.scale) != neg_inf()) listed[i] = __fmul_rn(g, __fmaf_rn(p, t.rest.y, -t.q[lane + 32 * i]));
+                        if (__fmul_rn(x, P.scale) != neg_inf() || m != m) listed[i] = __fmul_rn(g, __fmaf_rn(p, t.rest.y, -t.q[lane + 32 * i]));
                     }
                 });
                 __syncwarp();

@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_grad_kernel(const __grid_
             if (has_id) {       // before an in-place store takes the score
                 const float x = S::load_one(score_at<DT>(P, row, (uint32_t)id));
                 const float t = fmaxf(__fmaf_rn(x, ref.c, -ref.ref), kFarBelow);
-                g_id = x == neg_inf() ? 0.0f : __fmaf_rn(ex2(t), __fmaf_rn(B, t, A), __fmul_rn(P.scale, g_lp));
+                g_id = x == neg_inf() ? (A == A ? 0.0f : A) : __fmaf_rn(ex2(t), __fmaf_rn(B, t, A), __fmul_rn(P.scale, g_lp));
                 __syncwarp();
             }
             if (id >= 0) {

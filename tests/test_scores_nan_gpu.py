@@ -84,3 +84,52 @@ def test_one_nan_reaches_every_output(mr, dtype, T, V, W):  # noqa: F811
         mr.mr_distill_topk_grad(rows.views, t_ids, t_val, st, weight, out.views, mode=mode)
         check("gradient", torch.cat(out.views, 1), unmasked)
         out.fenced()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_masked_places_of_spoilt_rows(mr, dtype, bad):  # noqa: F811
+    """All gradients of such a row are NaN: those of masked places, listed or
+    not, and of the given token's, too."""
+    import torch
+    T, V, K, ninf = 6, 3001, 4, float("-inf")
+    ids = torch.arange(T, device="cuda")[:, None] * 100 + torch.arange(K, device="cuda") * 7
+    x = torch.randn(T, V, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    x[0, 2000] = bad
+    x[0, ids[0, 1:3]] = ninf                # masked places in the list
+    x[1] = ninf
+    x[1, ids[1]] = 1.0
+    x[1, ids[1, 1]] = bad                   # nothing left outside the list
+    x[2] = ninf
+    x[2, ids[2, 0]] = bad                   # nothing else at all
+    x[3, ::2] = ninf
+    x[3, 1] = bad
+    x[4] = ninf
+    x[4, 2999] = bad                        # outside the list alone; row 5 stays whole
+    x = x.to(_dt(dtype))
+    token = ids[:, 1].clone()
+    token[3] = 0
+    rows, one = Rows(2, T, V, dtype, fill=x), torch.ones(T, device="cuda")
+
+    def check(what, out):
+        nan = torch.isnan(torch.cat(out.views, 1).float())
+        assert bool(nan[:5].all()) and not bool(nan[5].any()), f"{what}: {nan.sum(1).tolist()} of {V}"
+        out.fenced()
+
+    h, st2 = torch.empty(T, device="cuda"), torch.empty(T, 2, device="cuda")
+    mr.mr_logprob(rows.views, entropy=h, stats=st2)
+    for ent in (None, one):
+        out = Rows(2, T, V, dtype)
+        mr.mr_logprob_grad(rows.views, token, st2, out.views, g_logprob=one, entropy=h, g_entropy=ent)
+        check("log probability", out)
+    val = torch.log_softmax(torch.randn(T, K, device="cuda"), 1) - 0.1
+    loss, st4 = torch.empty(T, device="cuda"), torch.empty(T, 4, device="cuda")
+    for mode in ("renorm", "tail"):
+        mr.mr_distill_topk(rows.views, ids, val, loss, stats=st4, mode=mode)
+        assert torch.isnan(loss).tolist() == [True] * 5 + [False]
+        out = Rows(2, T, V, dtype)
+        mr.mr_distill_topk_grad(rows.views, ids, val, st4, one, out.views, mode=mode)
+        check(f"gradient, {mode}", out)
+        out = Rows(2, T, V, dtype)
+        mr.mr_distill_topk_step(rows.views, ids, val, one, loss, out.views, mode=mode)
+        check(f"step, {mode}", out)
