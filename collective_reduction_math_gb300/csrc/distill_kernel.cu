@@ -300,7 +300,8 @@ __device__ __forceinline__ void mask_listed_in_registers(uint32_t (&w)[16], cons
             if ((mine >> (j * S::VE + e)) & 1) S::put(w, j, e, S::kBytes == 2 ? S::kFill & 0xffffu : S::kFill);
 }
 
-// What the gradient outside the list needs: coef * 2^(c x - ref).
+// What the gradient outside the list needs: coef * 2^(c x - ref); c = 0 for a
+// row whose teacher has no mass, which gets zeros whatever its scores are.
 struct Coef {
     float c, ref, coef;
 };
@@ -455,6 +456,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                 }
                 bar_sync(kRowStep);
                 if (!out) coef = s_coef;
+                const bool zero = out || coef.c == 0.0f;
                 // The next row's copies go into the blocks as they empty.
                 Walk<DT> ahead;
                 walk = Walk<DT>{};
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                 uint32_t sb = first;
                 for (uint32_t i = 0; i < rounds; ++i, sb += kScoreWarps) {
                     if (walk.seek(P, row, sb, lane)) to.follow(P, row, walk, lane);
-                    if (out) {
+                    if (zero) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) w[e] = 0;
                     } else {
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                 const Ref k = reference(b.x, P.c);
                 const float mass = __fmul_rn(g, __fmaf_rn(__fmul_rn(r.s, inv), Q, -q_rest));
                 const float none_left = inv == inv ? 0.0f : inv;        // every place there is masked; NaN in a row of NaN
-                s_coef = {k.c, k.ref,
+                s_coef = {Q == 0.0f ? 0.0f : k.c, k.ref,
                           __fmul_rn(b.x, P.scale) == neg_inf() ? none_left : __fmul_rn(__fmul_rn(mass, reciprocal(b.s)), undo(k))};
             }
             bar_arrive(kRowStep);
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             slot = after;
             each_reg(regs, [&](int i) {
                 const float p = __fmul_rn(exp_near(__fmul_rn(__fadd_rn(x[i], -all.x), P.scale)), inv);     // as the gradient's own call
-                const bool no_part = __fmul_rn(x[i], P.scale) == neg_inf() && inv == inv;
+                const bool no_part = Q == 0.0f || (__fmul_rn(x[i], P.scale) == neg_inf() && inv == inv);
                 s_listed[lane + 32 * i] = no_part ? 0.0f : __fmul_rn(g, __fmaf_rn(p, Q, -t.q[lane + 32 * i]));
             });
         }
@@ -704,12 +706,13 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
                 coef.coef = m;
             }
         }
+        const bool zero = !L.some || t.rest.y == 0.0f;      // left out, or the teacher has no mass
         Walk<DT> walk;
         Output<DT> out;
         for (uint32_t sb = sb_lo; sb < sb_hi; ++sb) {
             if (walk.seek(P, row, sb, lane)) out.follow(P, row, walk, lane);
             uint32_t w[16];
-            if (!L.some) {
+            if (zero) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = 0;
                 out.store(w, P, row, walk, sb, lane);

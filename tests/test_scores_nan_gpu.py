@@ -133,3 +133,32 @@ def test_masked_places_of_spoilt_rows(mr, dtype, bad):  # noqa: F811
         out = Rows(2, T, V, dtype)
         mr.mr_distill_topk_step(rows.views, ids, val, one, loss, out.views, mode=mode)
         check(f"step, {mode}", out)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_teacher_without_mass(mr, dtype):  # noqa: F811
+    """Renormalised teacher values that are all -inf: loss and gradient 0, also
+    where the student's row is NaN or empty."""
+    import torch
+    T, V, K = 4, 3001, 4
+    ids = torch.arange(T, device="cuda")[:, None] * 100 + torch.arange(K, device="cuda") * 7
+    x = torch.randn(T, V, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    x[1, 2000] = float("nan")
+    x[2, int(ids[2, 0])] = float("inf")
+    x[3] = float("-inf")
+    x = x.to(_dt(dtype))
+    rows, one = Rows(2, T, V, dtype, fill=x), torch.ones(T, device="cuda")
+    val = torch.full((T, K), float("-inf"), device="cuda")
+    loss, st = torch.full((T,), 77.0, device="cuda"), torch.empty(T, 4, device="cuda")
+    mr.mr_distill_topk(rows.views, ids, val, loss, stats=st)
+    assert loss.tolist() == [0.0] * T
+    for which in ("gradient", "step"):
+        out = Rows(2, T, V, dtype)
+        loss.fill_(77.0)
+        if which == "gradient":
+            mr.mr_distill_topk_grad(rows.views, ids, val, st, one, out.views)
+        else:
+            mr.mr_distill_topk_step(rows.views, ids, val, one, loss, out.views)
+            assert loss.tolist() == [0.0] * T
+        assert not torch.cat(out.views, 1).any(), which     # NaN counts as one here
+        out.fenced()
