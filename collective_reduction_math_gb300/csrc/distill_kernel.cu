@@ -457,7 +457,9 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                 bar_sync(kRowStep);
                 if (!out) coef = s_coef;
                 const bool zero = out || coef.c == 0.0f;
-                // The next row's copies go into the blocks as they empty.
+                // The next row's copies go into the blocks as they empty; a row that
+                // is left out has none.
+                const bool copy = more && !row_out[parity ^ 1];
                 Walk<DT> ahead;
                 walk = Walk<DT>{};
                 Output<DT> to;
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
                         else load_superblock<DT>(w, P, row, walk, sb, lane);
                         rest_gradient<DT>(w, coef);
                     }
-                    if (more && i < cached) {
+                    if (copy && i < cached) {
                         ahead.seek(P, next_row, sb, lane);
                         begin_copy<DT>(block_of(i), P, next_row, ahead, sb, lane);
                     }

@@ -286,8 +286,8 @@ mr_status_t mr_reduce_scatter_ex(const void* const* send, void* const* recv, int
  *     y - lse: larger first, equal scores (-0 equals +0) lower column first,
  *     NaN above all.  0 <= top_k <= min(MR_MAX_TOP, vocab); vocab at most
  *     MR_MAX_TOP_VOCAB where top_k > 0 (else MR_ERR_UNSUPPORTED).
- * Any output may be NULL.  ids[t] < 0 leaves the row out: it is not read, and
- * gets logprob 0, entropy 0, stats (-inf, 0), top_ids -1, top_logprob -inf.
+ * Any output may be NULL.  ids[t] < 0 leaves the row out: its scores do not
+ * count (at most a beginning of them is read ahead), and it gets logprob 0, entropy 0, stats (-inf, 0), top_ids -1, top_logprob -inf.
  * ids[t] >= vocab gives logprob NaN.  A row of nothing but -inf has stats
  * (-inf, 0), entropy 0 and log probabilities -inf.
  */
@@ -327,7 +327,7 @@ mr_status_t mr_logprob_grad(const void* const* logits, const size_t* ld, int W, 
  *     counts as 0; a larger one makes the loss +inf.
  *   stats[4t..]: m and lse - m over the row, then over the places outside the
  *     list: what mr_distill_topk_grad takes.  Loss or stats may be NULL.
- * A row with no entry is left out: not read, loss 0, stats (-inf, 0, -inf, 0),
+ * A row with no entry is left out (its scores as in mr_logprob): loss 0, stats (-inf, 0, -inf, 0),
  * gradient 0.  So is, in the renormalised mode, the loss and gradient of a row
  * whose teacher values are all -inf.
  */
@@ -351,7 +351,8 @@ mr_status_t mr_distill_topk_grad(const void* const* logits, const size_t* ld, in
  * Loss and gradient in one kernel, for a training step that knows each
  * token's weight in advance: loss[t] (unweighted, may be NULL) and
  * grad[t][i] = weight[t] * d loss[t] / d x[t][i].  The row stays in shared
- * memory between the two, so it is read from HBM once.
+ * memory between the two as far as it fits there (a cluster's CTAs hold up to
+ * 3 MB, fewer and smaller clusters less); the rest is read a second time.
  */
 mr_status_t mr_distill_topk_step(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab,
                                  mr_dtype_t dtype, float scale, int K, const long long* teacher_ids, const float* teacher_val,
