@@ -386,13 +386,13 @@ bool pdl_enabled() {
     return on;
 }
 
-// Records `fmt` as the calling thread's last error and returns `st` (for
-// entry points defined in other translation units).
 int device_sms() { return sm_count(); }
 int debug_log_level() { return debug_level(); }
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 void clear_error() { g_last_error.clear(); }
 
+// Records `fmt` as the calling thread's last error and returns `st` (for
+// entry points defined in other translation units).
 mr_status_t report_error(mr_status_t st, const char* fmt, ...) {
     char buf[512];
     va_list ap;

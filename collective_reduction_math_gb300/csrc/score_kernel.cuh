@@ -646,11 +646,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(~0u, v, o));
     return v;
 }
-__device__ __forceinline__ float warp_max_nan(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, o));
-    return v;
-}
 // Joins the statistics of a warp's lanes; every lane gets the result.
 template <bool ENT>
 __device__ __forceinline__ Stat warp_join(Stat a, float c) {
@@ -659,19 +654,11 @@ __device__ __forceinline__ Stat warp_join(Stat a, float c) {
     if (ENT) a.u = warp_sum(a.u);
     return a;
 }
-// Joins the n statistics of a row's warps (one warp; every lane gets the result).
+// Joins the n statistics of a row's warps or CTAs (one warp; every lane gets the result).
+static_assert(kScoreWarps <= 32 && kMaxScoreCluster <= 32, "a lane each");
 template <bool ENT>
 __device__ __forceinline__ Stat join_parts(const Stat* part, int n, int lane, float c) {
-    Stat b = lane < n ? part[lane] : Stat{neg_inf(), 0.0f, 0.0f};
-    for (int i = lane + 32; i - lane < n; i += 32) {
-        Stat o = i < n ? part[i] : Stat{neg_inf(), 0.0f, 0.0f};
-        const float X = max_nan(b.x, o.x);
-        rebase<ENT>(b, X, c);
-        rebase<ENT>(o, X, c);
-        b.s = __fadd_rn(b.s, o.s);
-        if (ENT) b.u = __fadd_rn(b.u, o.u);
-    }
-    return warp_join<ENT>(b, c);
+    return warp_join<ENT>(lane < n ? part[lane] : Stat{neg_inf(), 0.0f, 0.0f}, c);
 }
 // In the forward-only kernels the stream's threads leave their statistics of a
 // row here for the row warp, which has time while the stream is in the next
@@ -792,13 +779,21 @@ __device__ __forceinline__ SavedRef saved_reference(float m, float scale, float 
 // stream is in the next one, so the stream never waits for a chain of small
 // loads.  They meet at named barriers; what passes through shared memory is
 // double-buffered by the row's parity:
-//   kRowReady + parity   the row warp has set a row up (the first two before it
-//                        begins, row i+2 when it has joined row i); the stream
-//                        waits before it starts the row
+//   kRowReady + parity   the row warp has set a row up; the stream waits before
+//                        it starts the row (loss and gradient in one: before the
+//                        last row's gradients).  The log probabilities' row warp
+//                        sets up the first two rows before it begins and row
+//                        i+2 when it has joined row i; the distillation's the
+//                        first one, and row i+1 before it joins row i
 //   kRowDone + parity    the stream's warps have left their results of row i;
 //                        the row warp waits before it joins them
+//   kRowStep             loss and gradient in one: what row i's gradients need is
+//                        there
+//   kRowHelp             the runs that hold the row's best scores are picked; the
+//   kRowHelped           stream's warps of the first CTA have read their share.
+//                        In the loss and gradient: the last row is stored
 // So the stream is at most one row ahead and no buffer of row i is still in
-// use when row i+2 begins.
+// use when row i+2 is set up.
 enum { kRowReady = 1, kRowDone = 3, kRowStep = 5, kRowHelp = 6, kRowHelped = 7 };     // 0 is __syncthreads
 __device__ __forceinline__ void bar_sync(int id) { asm volatile("barrier.cta.sync %0, %1;" :: "r"(id), "n"(kScoreThreads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id) { asm volatile("barrier.cta.arrive %0, %1;" :: "r"(id), "n"(kScoreThreads) : "memory"); }
