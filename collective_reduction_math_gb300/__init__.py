@@ -430,7 +430,8 @@ def mr_distill_topk_grad(logits, teacher_ids, teacher_val, stats, g_loss, grad, 
 def mr_distill_topk_step(logits, teacher_ids, teacher_val, weight, loss, grad, mode="renorm", scale=1.0,
                          teacher_scale=1.0, stream=None):
     """Loss [T] (unweighted; may be None) and the gradient of weight . loss in
-    one kernel, reading the scores once (``grad`` may be ``logits``)."""
+    one kernel, which keeps a row on the chip between the two as far as it
+    fits (``grad`` may be ``logits``)."""
     from torch import float32
     xp, ld, rows, vocab, code = _score_rows(logits, "logits")
     gp, gl = _grad_rows(logits, grad, rows, vocab, code)

@@ -26,10 +26,10 @@
 // exchanged, the stream's last warp works out the next row's masses: on the row
 // warp they kept the stream waiting (8192 x 131072 bf16 737 us against 701).
 //
-// What bounds them (GB300, bf16): the loss alone memory, 6.37 TB/s of 6.69 at
-// 4096 x 131072 with 64 entries (164 us); its gradient 5.9 TB/s (349 us at 4096 x
+// What bounds them (GB300, bf16): the loss alone memory, 6.4 TB/s of 6.69 at
+// 4096 x 131072 with 64 entries (163 us); its gradient 5.9 TB/s (351 us at 4096 x
 // 128000, 100 entries), the units' own reading of the list; loss and gradient
-// in one 6.0 TB/s (701 us at 8192 x 131072): two passes over a row cost some 460
+// in one 6.1 TB/s (693 us at 8192 x 131072, one row in 32 left out): two passes over a row cost some 460
 // instructions a 2 KiB superblock, and the stream waits at each row's join.
 #include "score_kernel.cuh"
 

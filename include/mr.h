@@ -255,6 +255,8 @@ mr_status_t mr_reduce_scatter_ex(const void* const* send, void* const* recv, int
  *   logits[r]: rank r's columns of row 0; ld[r] elements from one row to the
  *     next, at least the rank's columns (ld NULL: exactly those).  Any
  *     alignment to the element; rows on 16-byte boundaries are read fastest.
+ *     Gradients are written in vectors where a row of grad[r] starts as far past
+ *     a 16-byte boundary as that of logits[r], else element by element.
  *     A rank with no column (vocab < W) is never looked at.
  *   dtype: MR_FP32 or MR_BF16 (MR_INT32 returns MR_ERR_UNSUPPORTED);
  *     1 <= vocab < 2^31; rows == 0 is a no-op.
@@ -340,7 +342,7 @@ mr_status_t mr_distill_topk(const void* const* logits, const size_t* ld, int W, 
 /*
  * Its gradient: grad[t][i] = g_loss[t] * d loss[t] / d x[t][i].  With q_i = 0
  * outside the list, p_i - q_i, less softmax over the outside * q_R there,
- * times scale.
+ * times scale (p_i times sum q where that is over 1).
  */
 mr_status_t mr_distill_topk_grad(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab,
                                  mr_dtype_t dtype, float scale, int K, const long long* teacher_ids, const float* teacher_val,
