@@ -614,10 +614,11 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             // An empty row (its y all -inf) gets zeros, one with NaN or +inf NaN.
             const float y = __fmul_rn(all.x, P.scale);
             const float inv = fabsf(y) < __int_as_float(0x7f800000) ? reciprocal(all.s) : y == neg_inf() ? 0.0f : quiet_nan();
+            const bool spoilt = inv != inv || Q != Q;       // every gradient is NaN
             if (lane == 0) {
                 const Ref k = reference(b.x, P.c);
                 const float mass = __fmul_rn(g, __fmaf_rn(__fmul_rn(r.s, inv), Q, -q_rest));
-                const float none_left = inv == inv ? 0.0f : inv;        // every place there is masked; NaN in a row of NaN
+                const float none_left = spoilt ? quiet_nan() : 0.0f;        // every place there is masked
                 s_coef = {Q == 0.0f ? 0.0f : k.c, k.ref,
                           __fmul_rn(b.x, P.scale) == neg_inf() ? none_left : __fmul_rn(__fmul_rn(mass, reciprocal(b.s)), undo(k))};
             }
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) distill_kernel(const __grid_
             slot = after;
             each_reg(regs, [&](int i) {
                 const float p = __fmul_rn(exp_near(__fmul_rn(__fadd_rn(x[i], -all.x), P.scale)), inv);     // as the gradient's own call
-                const bool no_part = Q == 0.0f || (__fmul_rn(x[i], P.scale) == neg_inf() && inv == inv);
+                const bool no_part = Q == 0.0f || (__fmul_rn(x[i], P.scale) == neg_inf() && !spoilt);
                 s_listed[lane + 32 * i] = no_part ? 0.0f : __fmul_rn(g, __fmaf_rn(p, Q, -t.q[lane + 32 * i]));
             });
         }
@@ -704,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
                 const float p_rest = expf(__fadd_rn(__fadd_rn(m_rest, -m), __fadd_rn(logs_rest, -logs)));
                 coef = {k.f.c, k.f.ref, __fmul_rn(__fmul_rn(g, __fmaf_rn(p_rest, t.rest.y, -t.rest.x)),
                                                   __fmul_rn(expf(__fadd_rn(k.rho, -logs_rest)), undo(k.f)))};
-            } else if (m != m) {
-                coef.coef = m;
+            } else if (m != m || t.rest.y != t.rest.y) {
+                coef.coef = quiet_nan();
             }
         }
         const bool zero = !L.some || t.rest.y == 0.0f;      // left out, or the teacher has no mass
@@ -731,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_
                     if ((L.place[i] >> S::kLogSb) == sb) {
                         const float x = S::load_one(walk.address(sb) - lane * 16 + offset(L.place[i]));
                         const float p = exp_near(__fadd_rn(__fmaf_rn(x, P.scale, -m), -logs));
-                        if (__fmul_rn(x, P.scale) != neg_inf() || m != m) listed[i] = __fmul_rn(g, __fmaf_rn(p, t.rest.y, -t.q[lane + 32 * i]));
+                        if (__fmul_rn(x, P.scale) != neg_inf() || m != m || t.rest.y != t.rest.y) listed[i] = __fmul_rn(g, __fmaf_rn(p, t.rest.y, -t.q[lane + 32 * i]));
                     }
                 });
                 __syncwarp();

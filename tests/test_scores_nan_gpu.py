@@ -162,3 +162,34 @@ def test_teacher_without_mass(mr, dtype):  # noqa: F811
             assert loss.tolist() == [0.0] * T
         assert not torch.cat(out.views, 1).any(), which     # NaN counts as one here
         out.fenced()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("mode", ["renorm", "tail"])
+def test_masked_places_of_spoilt_teachers(mr, dtype, mode):  # noqa: F811
+    """A column past the vocabulary, or a NaN among the teacher's values, makes
+    every gradient of its row NaN, those of masked places too."""
+    import torch
+    T, V, K, ninf = 4, 3001, 4, float("-inf")
+    ids = torch.arange(T, device="cuda")[:, None] * 100 + torch.arange(K, device="cuda") * 7
+    x = torch.randn(T, V, device="cuda", generator=torch.Generator("cuda").manual_seed(4))
+    x[0, ids[0, 0]] = ninf                  # in the list
+    x[1] = ninf
+    x[1, ids[1]] = 1.0                      # nothing left outside it
+    x[2, ids[2, 3]] = ninf                  # row 3 stays whole
+    val = torch.log_softmax(torch.randn(T, K, device="cuda"), 1) - 0.1
+    ids[0, 2], ids[1, 2], val[2, 1] = V, V + 5, float("nan")
+    x = x.to(_dt(dtype))
+    rows, one = Rows(2, T, V, dtype, fill=x), torch.ones(T, device="cuda")
+    loss, st = torch.empty(T, device="cuda"), torch.empty(T, 4, device="cuda")
+    mr.mr_distill_topk(rows.views, ids, val, loss, stats=st, mode=mode)
+    assert torch.isnan(loss).tolist() == [True] * 3 + [False]
+    for which in ("gradient", "step"):
+        out = Rows(2, T, V, dtype)
+        if which == "gradient":
+            mr.mr_distill_topk_grad(rows.views, ids, val, st, one, out.views, mode=mode)
+        else:
+            mr.mr_distill_topk_step(rows.views, ids, val, one, loss, out.views, mode=mode)
+        nan = torch.isnan(torch.cat(out.views, 1).float())
+        assert bool(nan[:3].all()) and not bool(nan[3].any()), f"{which}: {nan.sum(1).tolist()} of {V}"
+        out.fenced()
