@@ -729,9 +729,10 @@ __device__ __forceinline__ Final finish(const Stat& a, float scale) {
     }
     return f;
 }
-// log p of a score: -inf for a masked one, NaN in a row that has NaN.
+// log p of a score: -inf for a masked one, NaN in a row that has NaN and for a
+// column past the vocabulary, whose score is given as NaN.
 __device__ __forceinline__ float log_prob(float x, const Stat& a, const Final& f, float scale) {
-    if (f.m != f.m) return f.m;
+    if (f.m != f.m || x != x) return quiet_nan();
     if (x == neg_inf() || f.m == neg_inf()) return neg_inf();
     return __fmaf_rn(__fadd_rn(x, -a.x), scale, -f.log_s);
 }

@@ -193,3 +193,15 @@ def test_masked_places_of_spoilt_teachers(mr, dtype, mode):  # noqa: F811
         nan = torch.isnan(torch.cat(out.views, 1).float())
         assert bool(nan[:3].all()) and not bool(nan[3].any()), f"{which}: {nan.sum(1).tolist()} of {V}"
         out.fenced()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [1, 40, 3001])
+def test_token_past_the_vocabulary_of_an_empty_row(mr, dtype, V):  # noqa: F811
+    """NaN, as in any other row; the given token of an empty row otherwise has -inf."""
+    import torch
+    x = torch.full((3, V), float("-inf"))
+    x[2, V // 2] = 1.0
+    rows, lp = Rows(1, 3, V, dtype, fill=x.to(_dt(dtype))), torch.empty(3, device="cuda")
+    mr.mr_logprob(rows.views, torch.tensor([V, V - 1, V + 7], device="cuda"), logprob=lp)
+    assert torch.isnan(lp).tolist() == [True, False, True] and lp[1].item() == float("-inf")
