@@ -262,7 +262,8 @@ mr_status_t mr_reduce_scatter_ex(const void* const* send, void* const* recv, int
  *     1 <= vocab < 2^31; rows == 0 is a no-op.
  *   y = scale * x (1 / temperature, in [2^-64, 2^64]), in fp32; all
  *     sums are fp32 over a fixed split of the row, the same on every run;
- *     results in dtype are rounded once.
+ *     results in dtype are rounded once.  An exponential e^(y - m) below 2^-126
+ *     is 0.
  *   -inf is a masked place: it has no part in any sum and gradient 0.  A row
  *     with a NaN or a +inf has NaN for its statistics, log probabilities,
  *     entropy, loss and gradients.
