@@ -11,79 +11,27 @@
 #include "mr.h"
 #include "mr_internal.h"
 #include "order.cuh"
+#include "spans.h"
 
 namespace {
 
+using mr::check_spans;
+using mr::misaligned;
 using mr::report_error;
 using mr::ScoreParams;
 
 constexpr float kLeastScale = 5.421010862427522e-20f;       // 2^-64
 constexpr size_t kMostRows = (size_t)1 << 36, kMostStride = (size_t)1 << 40;
 
-// A byte range of the call, or (ld > 0) rows of `width` bytes every `ld` bytes from lo.
-struct Span {
-    uintptr_t lo, hi;
-    size_t ld, width;
-    const char* name;
-    int rank;       // -1: not a rank buffer
-    bool written;
-};
-
-struct Spans {
-    Span s[2 * MR_MAX_RANKS + 8];
-    int n = 0;
-    void add(const void* p, size_t bytes, const char* name, bool written) {
-        if (p && bytes) s[n++] = {(uintptr_t)p, (uintptr_t)p + bytes, 0, 0, name, -1, written};
-    }
-    void add_rows(const void* p, size_t rows, size_t ld, size_t width, const char* name, int rank, bool written) {
-        if (width) s[n++] = {(uintptr_t)p, (uintptr_t)p + (rows - 1) * ld + width, ld, width, name, rank, written};
-    }
-};
-
-// Whether two overlapping ranges never share a byte: rows of one stride whose
-// columns lie beside each other (column slices of one buffer).
-bool beside(const Span& a, const Span& b) {
-    if (!a.ld || a.ld != b.ld) return false;
-    const Span &x = a.lo <= b.lo ? a : b, &y = a.lo <= b.lo ? b : a;
-    const size_t d = (y.lo - x.lo) % x.ld;      // where y's columns start within x's rows
-    return d >= x.width && d + y.width <= x.ld;
-}
-
-mr_status_t check_spans(Spans& v) {
-    std::sort(v.s, v.s + v.n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
-    int open[2 * MR_MAX_RANKS + 8];
-    int nopen = 0;
-    for (int i = 0; i < v.n; ++i) {
-        const Span& b = v.s[i];
-        int keep = 0;
-        for (int j = 0; j < nopen; ++j) {
-            const Span& a = v.s[open[j]];
-            if (a.hi <= b.lo) continue;
-            open[keep++] = open[j];
-            if (!a.written && !b.written) continue;
-            // in place: a rank's gradients over its own scores, row by row
-            const bool in_place = a.rank >= 0 && a.rank == b.rank && a.written != b.written && a.lo == b.lo && a.ld == b.ld;
-            if (!in_place && !beside(a, b))
-                return report_error(MR_ERR_ALIAS, "%s[%d] overlaps %s[%d] in a form that is not an allowed in-place one",
-                                    a.name, std::max(0, a.rank), b.name, std::max(0, b.rank));
-        }
-        nopen = keep;
-        open[nopen++] = i;
-    }
-    return MR_OK;
-}
-
 struct Call {
     const char* what;
     ScoreParams P;
-    Spans spans;
+    mr::Spans<2 * MR_MAX_RANKS + 8> spans;
     size_t rows = 0;
     mr_dtype_t dtype = MR_FP32;
     size_t esize = 4;
     uint32_t nsb = 0;
 };
-
-bool misaligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
 // Shapes, rank buffers and strides of the scores (and of the gradients).
 mr_status_t check_scores(Call& c, const void* const* logits, const size_t* ld, void* const* grad, const size_t* ld_grad,
