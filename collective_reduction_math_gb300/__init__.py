@@ -20,16 +20,19 @@ __all__ = [
     "mr_allreduce", "mr_reduce_scatter", "mr_all_gather", "mr_allreduce_ex", "mr_reduce_scatter_ex", "mr_allreduce_rmsnorm", "mr_allreduce_sign_ef",
     "mr_reduce_scatter_sign_ef", "mr_reduce_scatter_sign_ef_noalloc", "mr_sign_ef_workspace_bytes",
     "mr_logprob", "mr_logprob_grad", "mr_distill_topk", "mr_distill_topk_grad", "mr_distill_topk_step",
+    "mr_embedding", "mr_embedding_grad", "mr_embedding_grad_workspace_bytes", "mr_adjust_logits", "mr_adjust_logits_grad",
+    "mr_grad_norm", "mr_clip_grad_norm", "mr_grad_norm_workspace_bytes",
     "mr_status_string", "mr_last_error",
     "mr_allreduce_ptrs", "mr_plan_auto", "mr_plan_ring_order", "mr_plan_tree", "mr_chunk_lo", "mr_launch_count", "mr_launch_floor", "MRError",
     "load", "LIB_PATH",
-    "DTYPES", "OPS", "ALGOS", "DISTILL_MODES", "MAX_RANKS", "MAX_TOP", "MAX_TEACHER",
+    "DTYPES", "OPS", "ALGOS", "DISTILL_MODES", "MAX_RANKS", "MAX_TOP", "MAX_TEACHER", "MAX_BIAS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmr.so")
 MAX_RANKS = 64
 MAX_TOP = 64            # top alternatives per row of mr_logprob
 MAX_TEACHER = 128       # teacher entries per row of mr_distill_topk
+MAX_BIAS = 1024         # biases per row of mr_adjust_logits
 DTYPES = {"fp32": 0, "bf16": 1, "int32": 2}
 OPS = {"sum": 0, "prod": 1, "min": 2, "max": 3, "avg": 4}
 ALGOS = {"ring": 0, "tree": 1, "hier": 2, "auto": 3}
@@ -42,6 +45,14 @@ _lib = None
 class Order(ctypes.Structure):
     """mr_order_t: accumulation order for mr_allreduce_ex / mr_reduce_scatter_ex."""
     _fields_ = [("algo", ctypes.c_int), ("group", ctypes.c_int), ("per_hop_rounding", ctypes.c_int)]
+
+
+class Adjust(ctypes.Structure):
+    """mr_adjust_t: what mr_adjust_logits and its gradient do to each row."""
+    _fields_ = [("history", ctypes.c_void_p), ("history_len", ctypes.c_size_t), ("n_history", ctypes.c_void_p),
+                ("n_prompt", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("bias_count", ctypes.c_int), ("mask", ctypes.c_void_p), ("ld_mask", ctypes.c_size_t)]
 
 
 class MRError(RuntimeError):
@@ -106,6 +117,18 @@ def load():
     L.mr_distill_topk_step.argtypes = scores + teacher + [vp, vp, vp, vp, vp]
     for g in (L.mr_logprob, L.mr_logprob_grad, L.mr_distill_topk, L.mr_distill_topk_grad, L.mr_distill_topk_step):
         g.restype = i
+    L.mr_embedding.argtypes = [vp, vp, i, sz, sz, i, f, vp, sz, vp, sz, vp]
+    L.mr_embedding_grad_workspace_bytes.argtypes = [sz, sz, sz]
+    L.mr_embedding_grad.argtypes = [vp, sz, i, vp, sz, f, vp, vp, i, sz, sz, i, i, vp, sz, vp]
+    L.mr_adjust_logits.argtypes = [vp, vp, i, sz, sz, i, vp, vp, vp, vp]
+    L.mr_adjust_logits_grad.argtypes = [vp, vp, i, sz, sz, i, vp, vp, vp, vp, vp, vp]
+    L.mr_grad_norm_workspace_bytes.argtypes = [i]
+    L.mr_grad_norm.argtypes = [vp, vp, vp, i, vp, vp, sz, vp]
+    L.mr_clip_grad_norm.argtypes = [vp, vp, vp, vp, i, f, vp, vp, sz, vp]
+    for g in (L.mr_embedding, L.mr_embedding_grad, L.mr_adjust_logits, L.mr_adjust_logits_grad, L.mr_grad_norm, L.mr_clip_grad_norm):
+        g.restype = i
+    L.mr_embedding_grad_workspace_bytes.restype = sz
+    L.mr_grad_norm_workspace_bytes.restype = sz
     _lib = L
     return L
 
@@ -441,6 +464,253 @@ def mr_distill_topk_step(logits, teacher_ids, teacher_val, weight, loss, grad, m
                                      _score_stream(stream, logits[0]))
     if st:
         _raise(st)
+
+
+# --------------------------------------------------------------------------
+# embedding, adjusted scores, gradient norm
+# --------------------------------------------------------------------------
+
+def _on_device(dev, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current; the current stream is that device's."""
+    import torch
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _on_device(dev, stream, fn, *args)
+    if stream is None:
+        direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = direct(dev) if direct is not None else torch.cuda.current_stream().cuda_stream
+    st = fn(*args, stream if isinstance(stream, int) else stream.cuda_stream)
+    if st:
+        _raise(st)
+
+
+def _workspace(workspace, need, dev, stream):
+    """The caller's workspace, or one of torch's memory that belongs to the stream of the call."""
+    import torch
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous CUDA tensor on the other tensors' device is needed")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, None, 0
+    if stream is not None:
+        s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+        with torch.cuda.stream(s):
+            t = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        t = torch.empty(need, dtype=torch.uint8, device=dev)
+    return t, t.data_ptr(), need
+
+
+def _rows_2d(t, name, dev, what="rows"):
+    """(address, elements from a row to the next) of a 2-D CUDA tensor whose rows are dense."""
+    if t.dim() != 2 or not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name}: a 2-D CUDA tensor on the other tensors' device is needed")
+    n = t.shape[1]
+    ld, step = t.stride()
+    if (step != 1 and n > 1) or (ld < n and t.shape[0] > 1):
+        raise ValueError(f"{name}: the elements of a row must lie beside each other and rows must not overlap")
+    return t.data_ptr(), ld if ld > n else n
+
+
+def _table(tensors, name):
+    """W rank buffers [rows of the rank, hidden] -> (pointers, strides, vocab, hidden, dtype code, device)."""
+    if not tensors:
+        raise ValueError(f"{name}: empty list of rank buffers")
+    W, t0 = len(tensors), tensors[0]
+    dev, hidden, vocab = t0.get_device(), t0.shape[-1], 0
+    ptrs, lds = [], []
+    for r, t in enumerate(tensors):
+        p, ld = _rows_2d(t, f"{name}[{r}]", dev)
+        if t.dtype is not t0.dtype or t.shape[1] != hidden:
+            raise ValueError(f"{name}: rank buffers must be of one dtype and row length")
+        ptrs.append(p)
+        lds.append(ld)
+        vocab += t.shape[0]
+    for r, t in enumerate(tensors):
+        if t.shape[0] != (r + 1) * vocab // W - r * vocab // W:
+            raise ValueError(f"{name}[{r}]: {t.shape[0]} rows, but rank {r} of {W} holds rows "
+                             f"[{r * vocab // W}, {(r + 1) * vocab // W}) of {vocab}")
+    return (ctypes.c_void_p * W)(*ptrs), (ctypes.c_size_t * W)(*lds), vocab, hidden, _dtype_code(t0), dev
+
+
+def _array(t, name, shape, dtype, dev):
+    """The address of a contiguous array of that shape on that device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on the other tensors' device is needed")
+    return t.data_ptr()
+
+
+def mr_embedding(table, ids, out, scale=1.0, stream=None):
+    """out[t] = scale * table[ids[t]].  table: W rank buffers [rows of the
+    rank, hidden] (fp32 or bf16; rows may be strided); ids: [T] int64, negative
+    gives zeros, past the vocabulary NaN; out: [T, hidden] of the table's
+    dtype."""
+    from torch import int64
+    tp, ld, vocab, hidden, code, dev = _table(table, "table")
+    T = ids.numel()
+    op, ld_out = _rows_2d(out, "out", dev)
+    if out.dtype is not table[0].dtype or out.shape[0] != T or out.shape[1] != hidden:
+        raise ValueError(f"out: [{T}, {hidden}] of the table's dtype is needed")
+    _on_device(dev, stream, load().mr_embedding, tp, ld, len(table), vocab, hidden, code, scale,
+               _array(ids, "ids", (T,), int64, dev), T, op, ld_out)
+
+
+def mr_embedding_grad_workspace_bytes(rows: int, vocab: int, hidden: int) -> int:
+    return int(load().mr_embedding_grad_workspace_bytes(rows, vocab, hidden))
+
+
+def mr_embedding_grad(g_out, ids, grad, scale=1.0, accumulate=False, workspace=None, stream=None):
+    """The gradient of mr_embedding: grad[v] (+)= scale * the sum of g_out[t]
+    over the tokens with ids[t] == v.  g_out: [T, hidden] fp32 or bf16; grad: W
+    rank buffers [rows of the rank, hidden], fp32 or bf16.  ``accumulate`` adds
+    to what grad holds, else every row is written.  workspace:
+    mr_embedding_grad_workspace_bytes(T, vocab, hidden) bytes (None: torch
+    provides them)."""
+    from torch import int64
+    gp, ld_grad, vocab, hidden, code, dev = _table(grad, "grad")
+    T = ids.numel()
+    xp, ld_g = _rows_2d(g_out, "g_out", dev)
+    if g_out.shape[0] != T or g_out.shape[1] != hidden:
+        raise ValueError(f"g_out: [{T}, {hidden}] is needed")
+    L = load()
+    keep, ws, n = _workspace(workspace, L.mr_embedding_grad_workspace_bytes(T, vocab, hidden), dev, stream)
+    _on_device(dev, stream, L.mr_embedding_grad, xp, ld_g, _dtype_code(g_out), _array(ids, "ids", (T,), int64, dev), T, scale, gp,
+               ld_grad, len(grad), vocab, hidden, code, 1 if accumulate else 0, ws, n)
+
+
+def _same_device(tensors, name, dev):
+    for r, t in enumerate(tensors):
+        if t.get_device() != dev:
+            raise ValueError(f"{name}[{r}]: on another device than the other tensors")
+
+
+def _adjust(rows, vocab, dev, history, n_history, n_prompt, repetition, frequency, presence, bias_ids, bias, mask):
+    from torch import float32, int32, int64
+    L = K = 0
+    if history is not None:
+        if history.dim() != 2:
+            raise ValueError("history: a [rows, entries] tensor is needed")
+        L = history.shape[1]
+    if bias_ids is not None:
+        if bias_ids.dim() != 2:
+            raise ValueError("bias_ids: a [rows, entries] tensor is needed")
+        K = bias_ids.shape[1]
+    ld_mask = 0
+    if mask is not None:
+        if mask.dtype is not int32 or mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] * 32 < vocab:
+            raise ValueError(f"mask: int32 words [{rows}, {(vocab + 31) // 32}] are needed")
+        mask, ld_mask = _rows_2d(mask, "mask", dev)
+    if L == 0:          # a history without entries is none
+        history = n_history = n_prompt = repetition = frequency = presence = None
+    return Adjust(_array(history, "history", (rows, L), int64, dev), L, _array(n_history, "n_history", (rows,), int64, dev),
+                  _array(n_prompt, "n_prompt", (rows,), int64, dev), _array(repetition, "repetition", (rows,), float32, dev),
+                  _array(frequency, "frequency", (rows,), float32, dev), _array(presence, "presence", (rows,), float32, dev),
+                  _array(bias_ids, "bias_ids", (rows, K), int64, dev) if K else None,
+                  _array(bias, "bias", (rows, K), float32, dev) if K else None, K, mask, ld_mask)
+
+
+def _like(logits, tensors, name, rows, vocab, code):
+    p, ld, t_rows, t_vocab, t_code = _score_rows(tensors, name)
+    if len(tensors) != len(logits) or t_rows != rows or t_vocab != vocab or t_code != code:
+        raise ValueError(f"{name}: rank buffers of the scores' shape and dtype are needed")
+    return p, ld
+
+
+def mr_adjust_logits(logits, out, history=None, n_history=None, n_prompt=None, repetition=None, frequency=None, presence=None,
+                     bias_ids=None, bias=None, mask=None, stream=None):
+    """Scores with penalties for repeated tokens, biases, and a mask of the
+    allowed tokens.  logits, out: W rank buffers [T, columns of the rank] (out
+    may be logits).  history: [T, L] int64, of which row t has its first
+    n_history[t] ([T] int64; None: L) entries, the first n_prompt[t] of them the
+    prompt's; negative entries are none.  repetition (counts prompt and
+    output), frequency and presence (output only): [T] fp32.  bias_ids [T, K]
+    int64 and bias [T, K] fp32.  mask: [T, ceil(vocab / 32)] int32 words, bit c %
+    32 of word c // 32 set where column c is allowed."""
+    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
+    op, ld_out = _like(logits, out, "out", rows, vocab, code)
+    dev = logits[0].get_device()
+    _same_device(logits, "logits", dev)
+    _same_device(out, "out", dev)
+    a = _adjust(rows, vocab, dev, history, n_history, n_prompt, repetition, frequency, presence, bias_ids, bias, mask)
+    _on_device(dev, stream, load().mr_adjust_logits, xp, ld, len(logits), rows, vocab, code, ctypes.byref(a), op, ld_out)
+
+
+def mr_adjust_logits_grad(logits, g_out, grad, history=None, n_history=None, n_prompt=None, repetition=None, frequency=None,
+                          presence=None, mask=None, stream=None):
+    """The gradient of mr_adjust_logits with respect to the scores: grad (W
+    rank buffers; may be ``g_out``, not ``logits``) from g_out.  logits are the
+    scores as they were before; frequency, presence and biases do not change
+    the gradient."""
+    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
+    ip, ld_g = _like(logits, g_out, "g_out", rows, vocab, code)
+    gp, ld_grad = _like(logits, grad, "grad", rows, vocab, code)
+    dev = logits[0].get_device()
+    for t, name in ((logits, "logits"), (g_out, "g_out"), (grad, "grad")):
+        _same_device(t, name, dev)
+    a = _adjust(rows, vocab, dev, history, n_history, n_prompt, repetition, frequency, presence, None, None, mask)
+    _on_device(dev, stream, load().mr_adjust_logits_grad, xp, ld, len(logits), rows, vocab, code, ctypes.byref(a), ip, ld_g, gp,
+               ld_grad)
+
+
+def mr_grad_norm_workspace_bytes(count: int) -> int:
+    return int(load().mr_grad_norm_workspace_bytes(count))
+
+
+def _tensor_list(tensors, name, like=None):
+    """Any number of dense tensors -> (pointers, sizes, dtype codes, device)."""
+    n = len(tensors)
+    dev = tensors[0].get_device() if n else -1
+    ptrs, sizes, codes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)(), (ctypes.c_int * n)()
+    for i, t in enumerate(tensors):
+        if not t.is_contiguous() or t.get_device() != dev or dev < 0:
+            raise ValueError(f"{name}[{i}]: contiguous CUDA tensors on one device are needed")
+        if like is not None and (t.dtype is not like[i].dtype or t.shape != like[i].shape or dev != like[i].get_device()):
+            raise ValueError(f"{name}[{i}]: the shape, dtype and device of the gradient are needed")
+        ptrs[i], sizes[i], codes[i] = t.data_ptr(), t.numel(), _dtype_code(t)
+    return ptrs, sizes, codes, dev
+
+
+def _norm_device(norm, dev):
+    """The device of the call: the tensors', or the norm's where there is no tensor."""
+    if dev < 0:
+        if norm is None or not norm.is_cuda:
+            raise ValueError("norm: a CUDA tensor is needed")
+        return norm.get_device()
+    return dev
+
+
+def mr_grad_norm(grads, norm, workspace=None, stream=None):
+    """norm[0] (fp32) receives the L2 norm of all tensors of the list (fp32 or
+    bf16, mixed as they come) taken together.  workspace:
+    mr_grad_norm_workspace_bytes(len(grads)) bytes (None: torch provides
+    them)."""
+    from torch import float32
+    ptrs, sizes, codes, dev = _tensor_list(grads, "grads")
+    dev = _norm_device(norm, dev)
+    L = load()
+    keep, ws, n = _workspace(workspace, L.mr_grad_norm_workspace_bytes(len(grads)), dev, stream)
+    _on_device(dev, stream, L.mr_grad_norm, ptrs, sizes, codes, len(grads), _row_ptr(norm, "norm", 1, float32), ws, n)
+
+
+def mr_clip_grad_norm(grads, out, max_norm, norm=None, workspace=None, stream=None):
+    """out[i] = grads[i] * min(1, max_norm / norm) with the norm of all tensors
+    taken together, which ``norm`` (one fp32 value, may be None) receives.
+    ``out`` may be ``grads``, in whole or in part."""
+    from torch import float32
+    if len(out) != len(grads):
+        raise ValueError("out: one tensor for each gradient is needed")
+    ptrs, sizes, codes, dev = _tensor_list(grads, "grads")
+    outs = ptrs if out is grads else _tensor_list(out, "out", grads)[0]
+    if dev < 0 and norm is None:
+        return
+    dev = _norm_device(norm, dev)
+    L = load()
+    keep, ws, n = _workspace(workspace, L.mr_grad_norm_workspace_bytes(len(grads)), dev, stream)
+    _on_device(dev, stream, L.mr_clip_grad_norm, ptrs, outs, sizes, codes, len(grads), max_norm,
+               _row_ptr(norm, "norm", 1, float32), ws, n)
 
 
 def mr_allreduce_ptrs(send_ptrs, recv_ptrs, N, dtype, op, algo, stream):

@@ -1,0 +1,47 @@
+// adjust.h -- the adjusted scores' parameters, shared by the C ABI
+// (adjust_api.cu) and the kernels (adjust_kernel.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mr_internal.h"
+
+namespace mr {
+
+struct AdjustParams {
+    const void* x[kMaxRanks];       // the scores of rank r's columns
+    const void* in[kMaxRanks];      // what is changed: the scores, or (gradient) what comes back to the adjusted ones
+    void* out[kMaxRanks];
+    uint64_t ldx[kMaxRanks];        // elements from a row to the next
+    uint64_t ldi[kMaxRanks];
+    uint64_t ldo[kMaxRanks];
+    uint32_t col0[kMaxRanks + 1];   // first column of each rank
+    uint64_t rows;
+    int W;
+    uint32_t vocab;
+    uint32_t window;                // columns a CTA takes of a row at a time
+    uint32_t windows;               // windows a row
+    // the history of each row (null: none)
+    const long long* history;
+    uint64_t ld_history;            // entries a row
+    const long long* n_history;     // null: ld_history
+    const long long* n_prompt;      // null: 0
+    const float* repetition;        // null: 1
+    const float* frequency;         // null: 0
+    const float* presence;          // null: 0
+    // biases (null: none)
+    const long long* bias_ids;
+    const float* bias;
+    uint32_t K;
+    const uint32_t* mask;           // null: every token is allowed
+    uint64_t ld_mask;               // 32-bit words from a row to the next
+};
+
+// Where a column of the window stands in the history: bit 31, it is there;
+// bit 30, it has a bias; below, how often the model has said it.
+constexpr uint32_t kSeen = 1u << 31, kBiased = 1u << 30, kTimes = kBiased - 1;
+
+cudaError_t launch_adjust(const AdjustParams& P, int dtype, bool grad, dim3 grid, size_t smem, cudaStream_t s);
+
+}  // namespace mr

@@ -1,0 +1,46 @@
+// grad_norm.h -- parameters of the gradient norm and the clipping, shared by
+// the C ABI (grad_norm_api.cu) and the kernels (grad_norm_kernel.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mr_internal.h"
+
+namespace mr {
+
+// A launch takes up to kListTensors tensors; longer lists take several.
+constexpr int kListTensors = 512;
+
+// A tensor is cut into tiles of kTileBytes, counted from its start rounded
+// down to 16 bytes.
+constexpr uint32_t kTileVectors = 4;        // 16-byte vectors a thread
+constexpr uint32_t kTileBytes = kThreads * kTileVectors * 16;
+
+struct TensorList {
+    const void* in[kListTensors];
+    void* out[kListTensors];                // clipping: where the clipped tensor goes (may be in)
+    uint64_t n[kListTensors];               // elements; bit 63: bf16
+    uint32_t tile0[kListTensors + 1];       // tiles of the tensors before
+    int count;
+};
+constexpr uint64_t kIsBf16 = 1ull << 63;
+
+// What a CTA has summed: the squares as they are, of x 2^-80, and of x 2^90.
+struct NormPart {
+    double mid, big, small;
+};
+constexpr int kMostNormGrid = 1024;         // parts of a launch at most
+
+struct NormOfParts {
+    const NormPart* parts;
+    int count;
+    float max_norm;
+    float* norm;        // may be null
+};
+
+cudaError_t launch_norm_parts(const TensorList& L, NormPart* parts, dim3 grid, cudaStream_t s);
+cudaError_t launch_norm_join(const NormOfParts& N, cudaStream_t s);
+cudaError_t launch_clip(const TensorList& L, const NormOfParts& N, dim3 grid, cudaStream_t s);
+
+}  // namespace mr

@@ -362,6 +362,140 @@ mr_status_t mr_distill_topk_step(const void* const* logits, const size_t* ld, in
                                  mr_distill_t mode, float teacher_scale, const float* weight, float* loss,
                                  void* const* grad, const size_t* ld_grad, void* stream);
 
+/*
+ * Embedding: rows of a table [vocab, hidden] looked up by tokens [EMBED].  Rank
+ * r holds rows [floor(r*vocab/W), floor((r+1)*vocab/W)) of the table ([EQ2], as
+ * mr_chunk_lo; the columns that mr_logprob gives rank r where the table is also
+ * the output head).
+ *     out[t] = scale * table[ids[t]]          (one fp32 product, rounded once)
+ *   table[r]: rank r's first row; ld[r] elements from one row to the next, at
+ *     least hidden (ld NULL: exactly hidden).  A rank with no row (vocab < W) is
+ *     never looked at.  Row slices of one buffer are fine.
+ *   out: rows of hidden elements, ld_out elements apart (0: hidden).
+ *   ids[t] < 0 leaves the row out: it gets zeros.  ids[t] >= vocab gives NaN.
+ *   dtype: MR_FP32 or MR_BF16 (MR_INT32 returns MR_ERR_UNSUPPORTED), of the
+ *     table and of out; 1 <= vocab, hidden < 2^31; rows < 2^31, 0 is a no-op;
+ *     scale finite.
+ *   Any alignment to the element; fastest where every row starts on a 16-byte
+ *     boundary and holds whole 16-byte vectors.  out overlaps nothing else.
+ * [EMBED] Ranks of their own would each look their part up and sum the parts by
+ * an all-reduce; over simulated ranks the row is read where it lies.  The pages
+ * have no counterpart: the definition is the library's own.
+ */
+mr_status_t mr_embedding(const void* const* table, const size_t* ld, int W, size_t vocab, size_t hidden, mr_dtype_t dtype,
+                         float scale, const long long* ids, size_t rows, void* out, size_t ld_out, void* stream);
+
+/*
+ * Its gradient, summed over the tokens:
+ *     grad[v] (+)= scale * sum over t with ids[t] == v of g_out[t]
+ *   g_out: rows of hidden elements of `dtype`, ld_g elements apart (0: hidden).
+ *   grad[r], ld_grad[r]: rank r's rows of the table's gradient, of grad_dtype
+ *     (fp32 or bf16 whatever dtype is).
+ *   accumulate == 0: every row is written, those of no token with zeros.
+ *   accumulate == 1: the sums are added to what is there (one fp32 addition,
+ *     rounded once); rows of no token are not touched.
+ *   The sums are fp32, in an order that depends on ids alone: the same bits on
+ *     every run.  Each result is rounded to grad_dtype once.
+ *   Tokens left out (ids[t] < 0) and past the vocabulary have no row and count
+ *     nowhere; their rows of g_out are not read.
+ *   workspace: at least mr_embedding_grad_workspace_bytes(rows, vocab, hidden)
+ *     bytes of device memory (NULL where that is 0), owned by the caller, on a
+ *     16-byte boundary; it needs no initialisation and is scratch after the
+ *     call.  Calls that share a workspace must not run at the same time.
+ *   Nothing that is written overlaps anything else.
+ */
+size_t mr_embedding_grad_workspace_bytes(size_t rows, size_t vocab, size_t hidden);
+mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, const long long* ids, size_t rows, float scale,
+                              void* const* grad, const size_t* ld_grad, int W, size_t vocab, size_t hidden,
+                              mr_dtype_t grad_dtype, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Adjusted scores: penalties for repeated tokens, biases, and a mask of the
+ * tokens that are allowed, on rows of scores in W shards (the layout, types and
+ * limits of the token scores above).  For a row with the history h, whose first
+ * n_prompt entries are its prompt and the others what the model has said,
+ *     s = x > 0 ? x / repetition : x * repetition     where the column is in h, else x
+ *     y = s - frequency * times - presence            where it is `times` > 0 times in what was said
+ *     y = y + bias                                    where it is in bias_ids
+ *     out = the mask allows it ? y : -inf
+ * in fp32, one IEEE operation a step, rounded to dtype once; a column that none
+ * of this concerns keeps its bits.
+ *   history: rows of history_len entries, those of row t in [0, n_history[t])
+ *     (NULL: all; what is outside [0, history_len] is taken as the nearer end),
+ *     the prompt's in [0, n_prompt[t]) (NULL: none).  An entry that is negative
+ *     or past the vocabulary is none.  history_len < 2^30.
+ *   repetition, frequency, presence: one value a row; NULL: 1, 0, 0.
+ *   bias_ids, bias: bias_count <= MR_MAX_BIAS entries a row.  A column that is
+ *     listed more than once has the sum, in the list's order; one that is
+ *     negative or past the vocabulary is none.
+ *   mask: rows of 32-bit words, ld_mask words apart (0: ceil(vocab / 32)); bit
+ *     c % 32 of word c / 32 is set where column c is allowed.  A row may allow
+ *     none: all -inf.  NULL: all allowed.  What a masked place held has no part
+ *     in anything, a NaN neither.
+ *   out[r] may be logits[r] with the same stride (in place): then places that
+ *     nothing concerns are neither read nor written.  Else nothing that is
+ *     written overlaps anything; rank buffers may be column slices of one buffer.
+ */
+#define MR_MAX_BIAS 1024
+
+typedef struct {
+    const long long* history;
+    size_t history_len;
+    const long long* n_history;
+    const long long* n_prompt;
+    const float* repetition;
+    const float* frequency;
+    const float* presence;
+    const long long* bias_ids;
+    const float* bias;
+    int bias_count;
+    const unsigned int* mask;
+    size_t ld_mask;
+} mr_adjust_t;
+
+mr_status_t mr_adjust_logits(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,
+                             const mr_adjust_t* adjust, void* const* out, const size_t* ld_out, void* stream);
+
+/*
+ * Its gradient: grad = g_out * ds/dx, with ds/dx = 1 / repetition (x > 0) or
+ * repetition where the column is in the history, else 1; 0 where it is masked.
+ *   logits: the scores as they were before; read only where the history has an
+ *     entry, and not needed (NULL) without a repetition penalty.
+ *   grad[r] may be g_out[r] with the same stride (in place), but not logits[r].
+ */
+mr_status_t mr_adjust_logits_grad(const void* const* logits, const size_t* ld, int W, size_t rows, size_t vocab, mr_dtype_t dtype,
+                                  const mr_adjust_t* adjust, const void* const* g_out, const size_t* ld_g, void* const* grad,
+                                  const size_t* ld_grad, void* stream);
+
+/*
+ * The L2 norm of a list of tensors, taken together, and the tensors scaled to a
+ * largest norm: what a training step does with the gradients that
+ * mr_allreduce or mr_reduce_scatter leaves.
+ *     norm = sqrt(sum of x^2 over all tensors)
+ *     coef = norm > max_norm ? max_norm / norm : 1      (NaN where norm is)
+ *     out  = coef * x                                    (one fp32 product, rounded once)
+ *   grad[i]: n[i] elements of dtype[i] (MR_FP32 or MR_BF16; MR_INT32 returns
+ *     MR_ERR_UNSUPPORTED), any alignment to the element; n[i] == 0 is skipped;
+ *     0 <= count <= 2^20 tensors, n[i] <= 2^40.  The three arrays are host
+ *     arrays, as send and recv are.
+ *   norm: one fp32 value in device memory (mr_clip_grad_norm: may be NULL).
+ *     Sums neither overflow nor underflow where the norm does not; a norm
+ *     beyond fp32 reads +inf, while coef comes from the norm itself.  A NaN
+ *     makes the norm and every out NaN; infinities make the norm +inf, coef 0.
+ *   out[i] may be grad[i] (in place: nothing is written where coef is 1); else
+ *     what is written overlaps nothing.  mr_grad_norm counts a tensor that is
+ *     listed twice twice.
+ *   The split of the sums is fixed: the same bits on every run.
+ *   workspace: at least mr_grad_norm_workspace_bytes(count) bytes of device
+ *     memory, 8-byte aligned, which need no initialisation.  Calls that share a
+ *     workspace must not run at the same time.
+ */
+size_t mr_grad_norm_workspace_bytes(int count);
+mr_status_t mr_grad_norm(const void* const* grad, const size_t* n, const mr_dtype_t* dtype, int count, float* norm,
+                         void* workspace, size_t workspace_bytes, void* stream);
+mr_status_t mr_clip_grad_norm(const void* const* grad, void* const* out, const size_t* n, const mr_dtype_t* dtype, int count,
+                              float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
 /* A static, human-readable name of a status code. */
 const char* mr_status_string(mr_status_t status);
 
