@@ -21,6 +21,7 @@ LIB = os.path.join(HERE, "libmr.so")
 
 SOURCES = (["api.cu", "all_gather.cu", "rmsnorm_kernel.cu", "sign_ef_kernel.cu", "sign_ef_noalloc.cu",
             "score_api.cu", "logprob_kernel.cu", "distill_kernel.cu", "embedding_api.cu", "embedding_kernel.cu",
+            "token_sort_kernel.cu",
             "adjust_api.cu", "adjust_kernel.cu", "grad_norm_api.cu", "grad_norm_kernel.cu"]
            + [f"reduce_{dt}_{algo}.cu" for dt in ("fp32", "bf16", "int32") for algo in ("ring", "tree", "hier")]
            + [f"reduce_bf16_{algo}_hop.cu" for algo in ("ring", "tree", "hier")])

@@ -86,6 +86,25 @@ mr_status_t check_scale(const char* what, float scale) {
     return MR_OK;
 }
 
+// The workspace's parts from `base` on; its size.
+size_t workspace_of(mr::EmbeddingGradParams& P, void* base, size_t rows, size_t vocab, size_t hidden) {
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return static_cast<char*>(base) + here;
+    };
+    const size_t longs = rows / (mr::kUnit + 1);        // rows with more than one unit, at most
+    P.counts = reinterpret_cast<mr::SortCounts*>(take(sizeof(mr::SortCounts)));
+    P.tokens = reinterpret_cast<uint32_t*>(take(rows * sizeof(uint32_t)));
+    P.units = reinterpret_cast<mr::Unit*>(take((rows + 1) * sizeof(mr::Unit)));
+    P.longs = reinterpret_cast<uint32_t*>(take(longs * sizeof(uint32_t)));
+    P.present = reinterpret_cast<uint32_t*>(take((vocab + 31) / 32 * sizeof(uint32_t)));
+    P.ld_partial = (hidden + 3) / 4 * 4;
+    P.partial = reinterpret_cast<float*>(take(longs ? (rows + mr::kUnit - 1) / mr::kUnit * 2 * P.ld_partial * sizeof(float) : 0));
+    return at;
+}
+
 dim3 warp_grid(uint64_t units, unsigned per_sm) {
     const uint64_t per = mr::kThreads / 32, ctas = (units + per - 1) / per;
     return dim3((unsigned)std::max<uint64_t>(1, std::min(ctas, (uint64_t)mr::device_sms() * per_sm)), 1, 1);
@@ -130,8 +149,9 @@ mr_status_t mr_embedding(const void* const* table, const size_t* ld, int W, size
 }
 
 size_t mr_embedding_grad_workspace_bytes(size_t rows, size_t vocab, size_t hidden) {
-    (void)rows, (void)vocab, (void)hidden;
-    return 0;
+    if (rows > MR_MAX_EMBEDDING_GRAD_ROWS || vocab >= ((size_t)1 << 31) || hidden >= ((size_t)1 << 31)) return 0;      // no such call
+    mr::EmbeddingGradParams P{};
+    return workspace_of(P, nullptr, rows, vocab, hidden);
 }
 
 mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, const long long* ids, size_t rows, float scale,
@@ -149,36 +169,58 @@ mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, 
     if (st != MR_OK) return st;
     if (accumulate != 0 && accumulate != 1) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: accumulate = %d is neither 0 nor 1", what, accumulate);
     if (rows == 0 && accumulate) return MR_OK;
-    const size_t b = bytes_of(dtype), need = mr_embedding_grad_workspace_bytes(rows, vocab, hidden);
+    if (rows > MR_MAX_EMBEDDING_GRAD_ROWS)
+        return report_error(MR_ERR_UNSUPPORTED, "%s takes at most %d rows a call", what, MR_MAX_EMBEDDING_GRAD_ROWS);
+    const size_t b = bytes_of(dtype), need = workspace_of(P, workspace, rows, vocab, hidden);
     P.ld_g = ld_g ? ld_g : hidden;
     if (rows > 0) {
         if ((st = check_rows(what, "g_out", g_out, rows, hidden, P.ld_g, b)) != MR_OK) return st;
         spans.add_rows(g_out, rows, P.ld_g * b, hidden * b, "g_out", -1, false);
         vec = vec && on_vectors(g_out, rows, P.ld_g, b);
     }
-    if (need > 0) {
-        if (!workspace || misaligned(workspace, 16))
-            return report_error(MR_ERR_INVALID_ARGUMENT, "%s: workspace is NULL or not on a 16-byte boundary", what);
-        if (workspace_bytes < need)
-            return report_error(MR_ERR_INVALID_ARGUMENT, "%s: workspace of %zu bytes, %zu are needed", what, workspace_bytes, need);
-        spans.add(workspace, need, "workspace", true);
-    }
+    if (!workspace || misaligned(workspace, 16))
+        return report_error(MR_ERR_INVALID_ARGUMENT, "%s: workspace is NULL or not on a 16-byte boundary", what);
+    if (workspace_bytes < need)
+        return report_error(MR_ERR_INVALID_ARGUMENT, "%s: workspace of %zu bytes, %zu are needed", what, workspace_bytes, need);
+    spans.add(workspace, need, "workspace", true);
     if ((st = check_spans(spans)) != MR_OK) return st;
     vec = vec && hidden % 8 == 0;
     P.g = g_out;
     P.ids = ids;
-    P.rows = rows;
+    P.rows = (uint32_t)rows;
     P.hidden = hidden;
     P.scale = scale;
     P.accumulate = accumulate;
-    P.slabs = (hidden + mr::kSlab - 1) / mr::kSlab;
-    const dim3 grid = warp_grid(P.rows * P.slabs, 16);
-    const cudaError_t e = mr::launch_embedding_grad(P, dtype, grad_dtype, vec, grid, (cudaStream_t)stream);
-    if (e != cudaSuccess) return report_error(MR_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
-    if (mr::debug_log_level() > 0)
-        fprintf(stderr, "[mr] %s dtype=%s grad=%s W=%d rows=%zu hidden=%zu vocab=%zu accumulate=%d vec=%d grid=%u\n", what,
-                dtype == MR_BF16 ? "bf16" : "fp32", grad_dtype == MR_BF16 ? "bf16" : "fp32", W, rows, hidden, vocab, accumulate, (int)vec, grid.x);
-    return MR_OK;
+    P.slabs = (uint32_t)((hidden + mr::kSlab - 1) / mr::kSlab);
+    // keys 0 .. vocab
+    uint32_t bits = 1;
+    while (vocab >> bits) ++bits;
+    P.passes = (bits + mr::kSortDigit - 1) / mr::kSortDigit;
+    P.digit = (bits + P.passes - 1) / P.passes;
+    int cluster = 1, items = 1;
+    while (cluster < 8 && (size_t)mr::kSortThreads * cluster < rows) cluster *= 2;
+    while (items < mr::kMostSortItems && (size_t)mr::kSortThreads * cluster * items < rows) items *= 2;
+    while ((size_t)mr::kSortThreads * cluster * items < rows) cluster *= 2;
+    cudaError_t e = mr::launch_token_sort(P, cluster, items, (cudaStream_t)stream);
+    if (e == cudaSuccess) {
+        mr::count_launch();
+        const uint64_t most = rows * P.slabs + (accumulate ? 0 : vocab);
+        const dim3 grid = warp_grid(most, 8);
+        e = mr::launch_embedding_sum(P, dtype, grad_dtype, vec, grid, (cudaStream_t)stream);
+        if (mr::debug_log_level() > 0)
+            fprintf(stderr, "[mr] %s dtype=%s grad=%s W=%d rows=%zu hidden=%zu vocab=%zu accumulate=%d vec=%d sort=%dx%d grid=%u\n", what,
+                    dtype == MR_BF16 ? "bf16" : "fp32", grad_dtype == MR_BF16 ? "bf16" : "fp32", W, rows, hidden, vocab, accumulate, (int)vec,
+                    cluster, items, grid.x);
+    }
+    if (e == cudaSuccess) {
+        mr::count_launch();
+        const size_t longs = rows / (mr::kUnit + 1);
+        if (longs == 0) return MR_OK;
+        const uint64_t most = longs * ((hidden + 127) / 128);
+        e = mr::launch_embedding_join(P, grad_dtype, dim3((unsigned)std::min<uint64_t>(most, (uint64_t)mr::device_sms() * 8), 1, 1), (cudaStream_t)stream);
+        if (e == cudaSuccess) mr::count_launch();
+    }
+    return e == cudaSuccess ? MR_OK : report_error(MR_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
 }
 
 }  // extern "C"

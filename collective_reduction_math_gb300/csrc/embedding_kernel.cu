@@ -4,7 +4,7 @@
 //   gradient:  grad[v] (+)= scale * sum over t with ids[t] = v of g[t]
 //
 // Both move rows; neither has arithmetic to speak of.
-#include <algorithm>
+#include <type_traits>
 
 #include "elements.cuh"
 #include "embedding.h"
@@ -72,118 +72,207 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// Gradient.  A warp has a token and kSlab columns.  The first token of its id
-// sums the rows of all that have it, in the order of the tokens, in fp32.
+// Gradient.  The tokens come sorted by row and cut into units
+// (token_sort_kernel.cu).  A warp has a unit and kSlab columns: it adds up to
+// kUnit rows of g in fp32, in the tokens' order, eight (bf16) or four rows'
+// loads at a time, and writes the table's row, or a partial sum where the row
+// has more units; embedding_join_kernel adds those.  Warps without a unit clear
+// rows of no token.
 // ---------------------------------------------------------------------------
-template <int DG, int DT, bool VEC>
-struct Slab {
-    static constexpr int kPer = kSlab / 32;
-    float acc[kPer];
-    // column i of lane l: beside one another where they are read in vectors
-    static __device__ __forceinline__ uint32_t column(uint32_t lane, int i) { return VEC ? lane * kPer + i : i * 32 + lane; }
-    __device__ __forceinline__ void clear() {
+constexpr int kPer = kSlab / 32;    // columns a lane
+
+// column i of lane l: beside one another where they are read in vectors
+template <bool VEC>
+__device__ __forceinline__ uint32_t column(uint32_t lane, int i) {
+    return VEC ? lane * kPer + i : i * 32 + lane;
+}
+
+// A lane's part of a row, as it lies in memory.
+template <int DT, bool VEC>
+struct Piece {
+    using E = Element<DT>;
+    static constexpr int kWords = VEC ? kPer / E::kLanes : kPer;
+    typename std::conditional<VEC, uint4, float>::type w[kWords];
+    __device__ __forceinline__ void load(const char* row, uint64_t c0, uint64_t hidden, uint32_t lane) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-    }
-    __device__ __forceinline__ void add(const char* row, uint64_t c0, uint64_t hidden, uint32_t lane) {
-        using E = Element<DG>;
-        if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < kPer; i += E::kLanes) {
-                const uint64_t c = c0 + column(lane, i);
-                if (c >= hidden) break;
-                float f[E::kLanes];
-                E::unpack(load16(row + c * E::kBytes), f);
-#pragma unroll
-                for (int k = 0; k < E::kLanes; ++k) acc[i + k] = __fadd_rn(acc[i + k], f[k]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const uint64_t c = c0 + column(lane, i);
-                if (c < hidden) acc[i] = __fadd_rn(acc[i], E::get(row, c));
+        for (int i = 0; i < kWords; ++i) {
+            const uint64_t c = c0 + column<VEC>(lane, VEC ? i * E::kLanes : i);
+            if constexpr (VEC) {
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (c < hidden) w[i] = load16(row + c * E::kBytes);
+            } else {
+                w[i] = c < hidden ? E::get(row, c) : 0.0f;
             }
         }
     }
-    __device__ __forceinline__ void finish(char* row, uint64_t c0, uint64_t hidden, uint32_t lane, float scale, bool accumulate) const {
-        using E = Element<DT>;
-        if constexpr (VEC) {
+    __device__ __forceinline__ void values(float (&f)[kPer]) const {
 #pragma unroll
-            for (int i = 0; i < kPer; i += E::kLanes) {
-                const uint64_t c = c0 + column(lane, i);
-                if (c >= hidden) break;
-                float f[E::kLanes];
-                if (accumulate) E::unpack(load16(row + c * E::kBytes), f);
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (VEC) {
+                float part[E::kLanes];
+                E::unpack(w[i], part);
 #pragma unroll
-                for (int k = 0; k < E::kLanes; ++k) {
-                    const float s = __fmul_rn(acc[i + k], scale);
-                    f[k] = accumulate ? __fadd_rn(f[k], s) : s;
-                }
-                store16(row + c * E::kBytes, E::pack(f));
+                for (int k = 0; k < E::kLanes; ++k) f[i * E::kLanes + k] = part[k];
+            } else {
+                f[i] = w[i];
             }
-        } else {
+        }
+    }
+    static __device__ __forceinline__ void store(char* row, uint64_t c0, uint64_t hidden, uint32_t lane, const float (&f)[kPer]) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const uint64_t c = c0 + column(lane, i);
-                if (c >= hidden) break;
-                const float s = __fmul_rn(acc[i], scale);
-                E::put(row, c, accumulate ? __fadd_rn(E::get(row, c), s) : s);
+        for (int i = 0; i < kWords; ++i) {
+            const uint64_t c = c0 + column<VEC>(lane, VEC ? i * E::kLanes : i);
+            if (c >= hidden) break;
+            if constexpr (VEC) {
+                float part[E::kLanes];
+#pragma unroll
+                for (int k = 0; k < E::kLanes; ++k) part[k] = f[i * E::kLanes + k];
+                store16(row + c * E::kBytes, E::pack(part));
+            } else {
+                E::put(row, c, f[i]);
             }
         }
     }
 };
 
+// Clears kFillBytes of each of eight rows that no token has.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) clear_table_kernel(const __grid_constant__ EmbeddingGradParams P) {
+__device__ __forceinline__ void fill(const EmbeddingGradParams& P, uint64_t task, uint32_t chunks, uint32_t lane) {
     using E = Element<DT>;
-    const uint32_t lane = threadIdx.x % 32;
-    const uint64_t warps = (uint64_t)gridDim.x * (kThreads / 32);
-    pdl_enter();
-    for (uint64_t v = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; v < P.grad.vocab; v += warps) {
-        char* row = row_of(P.grad, (uint32_t)v, E::kBytes);
+    const uint32_t group = (uint32_t)(task / chunks), chunk = (uint32_t)(task - (uint64_t)group * chunks);
+    constexpr uint32_t kColumns = kFillBytes / E::kBytes;
+    const uint32_t there = P.present[group / 4] >> (group % 4 * 8) & 0xffu;
+    const uint64_t c0 = (uint64_t)chunk * kColumns, c1 = min(P.hidden, c0 + kColumns);
+    for (uint32_t i = 0; i < 8; ++i) {
+        const uint32_t v = group * 8 + i;
+        if (v >= P.grad.vocab || there >> i & 1) continue;
+        char* row = row_of(P.grad, v, E::kBytes);
         if constexpr (VEC) {
-            for (uint64_t c = lane * E::kLanes; c < P.hidden; c += 32 * E::kLanes) store16(row + c * E::kBytes, make_uint4(0, 0, 0, 0));
+#pragma unroll
+            for (int k = 0; k < (int)(kFillBytes / 512); ++k) {
+                const uint64_t c = c0 + (k * 32 + lane) * E::kLanes;
+                if (c < c1) store16(row + c * E::kBytes, make_uint4(0, 0, 0, 0));
+            }
         } else {
-            for (uint64_t c = lane; c < P.hidden; c += 32) E::put(row, c, 0.0f);
+            for (uint64_t c = c0 + lane; c < c1; c += 32) E::put(row, c, 0.0f);
         }
     }
 }
 
 template <int DG, int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) embedding_grad_kernel(const __grid_constant__ EmbeddingGradParams P) {
+__global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ EmbeddingGradParams P) {
+    constexpr int kRows = DG == MR_BF16 || !VEC ? 8 : 4;
     const uint32_t lane = threadIdx.x % 32;
-    const uint64_t warps = (uint64_t)gridDim.x * (kThreads / 32), units = P.rows * P.slabs;
+    const uint32_t warps = gridDim.x * (kThreads / 32), first = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     const char* g = static_cast<const char*>(P.g);
     pdl_enter();
-    for (uint64_t u = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; u < units; u += warps) {
-        const uint64_t t = u / P.slabs, c0 = (u - t * P.slabs) * kSlab;
-        const long long id = P.ids[t];
-        if (id < 0 || id >= (long long)P.grad.vocab) continue;
-        bool first = true;
-        for (uint64_t i = 0; i < t && first; i += 32) first = !__any_sync(kAll, i + lane < t && P.ids[i + lane] == id);
-        if (!first) continue;
-        Slab<DG, DT, VEC> sum;
-        sum.clear();
-        for (uint64_t i = t; i < P.rows; i += 32) {
-            unsigned same = __ballot_sync(kAll, i + lane < P.rows && P.ids[i + lane] == id);
-            for (; same; same &= same - 1) sum.add(g + (i + __ffs(same) - 1) * P.ld_g * Element<DG>::kBytes, c0, P.hidden, lane);
+    const uint64_t sums = (uint64_t)P.counts->units * P.slabs;
+    const uint32_t chunks = (uint32_t)((P.hidden * Element<DT>::kBytes + kFillBytes - 1) / kFillBytes);
+    const uint64_t tasks = sums + (P.accumulate ? 0 : (uint64_t)((P.grad.vocab + 7) / 8) * chunks);
+    for (uint64_t task = first; task < tasks; task += warps) {
+        if (task >= sums) {
+            fill<DT, VEC>(P, task - sums, chunks, lane);
+            continue;
         }
-        sum.finish(row_of(P.grad, (uint32_t)id, Element<DT>::kBytes), c0, P.hidden, lane, P.scale, P.accumulate != 0);
+        const uint32_t u = (uint32_t)(task / P.slabs);
+        const uint64_t c0 = (task - (uint64_t)u * P.slabs) * kSlab;
+        const Unit unit = P.units[u];
+        const uint32_t start = unit.start & kStart, n = (P.units[u + 1].start & kStart) - start;
+        const uint32_t token = lane < n ? P.tokens[start + lane] : 0;
+        char* row = row_of(P.grad, unit.row, Element<DT>::kBytes);
+        const bool whole = !(unit.start & kPart), add = whole && P.accumulate;
+        Piece<DT, VEC> old;
+        if (add) old.load(row, c0, P.hidden, lane);
+        float acc[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
+        for (uint32_t i = 0; i < n; i += kRows) {
+            Piece<DG, VEC> piece[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (i + r < n)
+                    piece[r].load(g + (uint64_t)__shfl_sync(kAll, token, i + r) * P.ld_g * Element<DG>::kBytes, c0, P.hidden, lane);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                if (i + r >= n) break;
+                float f[kPer];
+                piece[r].values(f);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) acc[k] = __fadd_rn(acc[k], f[k]);
+            }
+        }
+        if (!whole) {
+            float* to = P.partial + partial_slot(start, unit.start & kFirst) * P.ld_partial;
+            Piece<MR_FP32, VEC>::store(reinterpret_cast<char*>(to), c0, P.hidden, lane, acc);
+            continue;
+        }
+        float was[kPer];
+        if (add) old.values(was);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            acc[k] = __fmul_rn(acc[k], P.scale);
+            if (add) acc[k] = __fadd_rn(was[k], acc[k]);
+        }
+        Piece<DT, VEC>::store(row, c0, P.hidden, lane, acc);
     }
 }
 
-template <int DG, int DT, bool VEC>
-cudaError_t launch_grad(const EmbeddingGradParams& P, dim3 grid, cudaStream_t s) {
-    if (!P.accumulate) {
-        const dim3 all((unsigned)std::min<uint64_t>(device_sms() * 8, (P.grad.vocab + kThreads / 32 - 1ull) / (kThreads / 32)), 1, 1);
-        const cudaError_t e = launch_kernel(clear_table_kernel<DT, VEC>, all, 0, s, 0, P);
-        if (e != cudaSuccess) return e;
-        count_launch();
+// A CTA adds a row's partial sums of 128 columns: each warp a run of them,
+// then the warps' sums in their order.
+constexpr uint32_t kJoinColumns = 128;
+template <int DT>
+__global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ EmbeddingGradParams P) {
+    using E = Element<DT>;
+    constexpr uint32_t kWarps = kThreads / 32;
+    __shared__ float4 sum[kWarps][32];
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    pdl_enter();
+    const uint32_t slabs = (uint32_t)((P.hidden + kJoinColumns - 1) / kJoinColumns), units = P.counts->units;
+    const uint64_t tasks = (uint64_t)P.counts->longs * slabs;
+    for (uint64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const uint32_t u = P.longs[task / slabs];
+        const uint64_t c = task % slabs * kJoinColumns + lane * 4;
+        const uint32_t start = P.units[u].start & kStart, row = P.units[u].row;
+        uint32_t parts = 1;     // the units of this row
+        for (bool all = true; all;) {
+            const uint32_t here = __ballot_sync(kAll, P.units[min(u + parts + lane, units)].row == row);
+            parts += __popc(here);
+            all = here == kAll;
+        }
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const uint32_t from = (uint32_t)((uint64_t)warp * parts / kWarps), to = (uint32_t)((uint64_t)(warp + 1) * parts / kWarps);
+        if (c < P.hidden) {
+#pragma unroll 8
+            for (uint32_t k = from; k < to; ++k) {
+                const float* p = P.partial + partial_slot(start + k * kUnit, k == 0) * P.ld_partial + c;
+                const uint4 v = load16(p);
+                s.x = __fadd_rn(s.x, __uint_as_float(v.x));
+                s.y = __fadd_rn(s.y, __uint_as_float(v.y));
+                s.z = __fadd_rn(s.z, __uint_as_float(v.z));
+                s.w = __fadd_rn(s.w, __uint_as_float(v.w));
+            }
+        }
+        __syncthreads();    // the last task's sums are read
+        sum[warp][lane] = s;
+        __syncthreads();
+        if (threadIdx.x < kJoinColumns) {
+            const uint64_t col = task % slabs * kJoinColumns + threadIdx.x;
+            float t = 0.0f;
+#pragma unroll
+            for (uint32_t w = 0; w < kWarps; ++w) t = __fadd_rn(t, reinterpret_cast<const float*>(sum[w])[threadIdx.x]);
+            if (col < P.hidden) {
+                char* to_row = row_of(P.grad, row, E::kBytes);
+                t = __fmul_rn(t, P.scale);
+                E::put(to_row, col, P.accumulate ? __fadd_rn(E::get(to_row, col), t) : t);
+            }
+        }
     }
-    if (P.rows == 0) return cudaSuccess;
-    const cudaError_t e = launch_kernel(embedding_grad_kernel<DG, DT, VEC>, grid, 0, s, 0, P);
-    if (e == cudaSuccess) count_launch();
-    return e;
+}
+
+template <int DG, int DT>
+cudaError_t launch_sum(const EmbeddingGradParams& P, bool vec, dim3 grid, cudaStream_t s) {
+    return vec ? launch_kernel(embedding_sum_kernel<DG, DT, true>, grid, 0, s, 0, P)
+               : launch_kernel(embedding_sum_kernel<DG, DT, false>, grid, 0, s, 0, P);
 }
 
 }  // namespace
@@ -196,15 +285,15 @@ cudaError_t launch_embedding(const EmbeddingParams& P, int dtype, bool vec, dim3
                : launch_kernel(embedding_kernel<MR_FP32, false>, grid, 0, s, 0, P);
 }
 
-cudaError_t launch_embedding_grad(const EmbeddingGradParams& P, int g_dtype, int table_dtype, bool vec, dim3 grid, cudaStream_t s) {
-    if (g_dtype == MR_BF16) {
-        if (table_dtype == MR_BF16)
-            return vec ? launch_grad<MR_BF16, MR_BF16, true>(P, grid, s) : launch_grad<MR_BF16, MR_BF16, false>(P, grid, s);
-        return vec ? launch_grad<MR_BF16, MR_FP32, true>(P, grid, s) : launch_grad<MR_BF16, MR_FP32, false>(P, grid, s);
-    }
-    if (table_dtype == MR_BF16)
-        return vec ? launch_grad<MR_FP32, MR_BF16, true>(P, grid, s) : launch_grad<MR_FP32, MR_BF16, false>(P, grid, s);
-    return vec ? launch_grad<MR_FP32, MR_FP32, true>(P, grid, s) : launch_grad<MR_FP32, MR_FP32, false>(P, grid, s);
+cudaError_t launch_embedding_sum(const EmbeddingGradParams& P, int g_dtype, int table_dtype, bool vec, dim3 grid, cudaStream_t s) {
+    if (g_dtype == MR_BF16)
+        return table_dtype == MR_BF16 ? launch_sum<MR_BF16, MR_BF16>(P, vec, grid, s) : launch_sum<MR_BF16, MR_FP32>(P, vec, grid, s);
+    return table_dtype == MR_BF16 ? launch_sum<MR_FP32, MR_BF16>(P, vec, grid, s) : launch_sum<MR_FP32, MR_FP32>(P, vec, grid, s);
+}
+
+cudaError_t launch_embedding_join(const EmbeddingGradParams& P, int table_dtype, dim3 grid, cudaStream_t s) {
+    return table_dtype == MR_BF16 ? launch_kernel(embedding_join_kernel<MR_BF16>, grid, 0, s, 0, P)
+                                  : launch_kernel(embedding_join_kernel<MR_FP32>, grid, 0, s, 0, P);
 }
 
 }  // namespace mr

@@ -1,0 +1,262 @@
+// token_sort_kernel.cu -- the tokens of a batch sorted by their table row, and
+// cut into units for the embedding's gradient.
+//
+// One cluster sorts them all, in its shared memory: a stable radix sort from
+// the lowest digit, of as many passes as the vocabulary's bits need at
+// kSortDigit bits a pass (2 up to a vocabulary of 2^20 - 1).  In a pass a warp
+// ranks its tokens among themselves, round by round (match of the digit, a
+// count a digit and warp); the counts are summed over the CTA's warps, the
+// CTAs' totals are exchanged, and each token goes to its place in the CTA that
+// has it, over distributed shared memory.  Tokens stay in registers between a
+// pass's reads and its writes, so one buffer is enough.
+//
+// A token without a row (negative, or past the vocabulary) gets the key
+// `vocab`, behind all others, and so does what fills the last CTA up.
+//
+// Then the runs of one row: each position finds its run's start (the last
+// start among the lanes, warps and CTAs before it); a unit starts every kUnit
+// positions of a run; units are numbered by a scan.
+#include "embedding.h"
+
+namespace mr {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = kSortThreads / 32;
+constexpr uint32_t kNone = 0xffffffffu;
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t shared_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t remote(uint32_t at, uint32_t cta) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(cta));
+    return r;
+}
+__device__ __forceinline__ uint32_t load_remote(const uint32_t* p, uint32_t cta) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(shared_at(p), cta)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_remote(uint2* p, uint32_t cta, uint2 v) {
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(remote(shared_at(p), cta)), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// Exclusive sum over the CTA's threads (every thread calls it).
+__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* sums) {
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint32_t s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint32_t o = __shfl_up_sync(kAll, s, d);
+        if (lane >= d) s += o;
+    }
+    __syncthreads();        // sums' last readers are done
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t t = sums[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const uint32_t o = __shfl_up_sync(kAll, t, d);
+            if (lane >= d) t += o;
+        }
+        sums[lane] = t;
+    }
+    __syncthreads();
+    return s - v + (warp ? sums[warp - 1] : 0);
+}
+
+// x: the key, y: the token
+template <int K>
+__global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(const __grid_constant__ EmbeddingGradParams P) {
+    constexpr uint32_t E = kSortThreads * K;        // tokens a CTA
+    extern __shared__ uint4 dynamic[];
+    uint2* item = reinterpret_cast<uint2*>(dynamic);
+    const uint32_t bins = 1u << P.digit;
+    uint32_t* total = reinterpret_cast<uint32_t*>(item + E);        // of the CTA's tokens, by digit
+    uint32_t* place = total + (1 << kSortDigit);                    // where the CTA's first token of a digit goes
+    uint16_t* count = reinterpret_cast<uint16_t*>(place + (1 << kSortDigit));      // [warp][digit]
+    __shared__ uint32_t sums[32], last_start[kWarps], cta_last, cta_units;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, cta = cluster_rank(), ctas = cluster_ctas();
+    const uint32_t before = (1u << lane) - 1;
+    const uint32_t at0 = warp * 32 * K + lane;      // this thread's tokens: at0 + 32 j of the CTA's
+    pdl_enter();
+
+    if (cta == 0 && threadIdx.x == 0) P.counts->longs = 0;
+    if (!P.accumulate)
+        for (uint32_t i = cta * kSortThreads + threadIdx.x; i < (P.grad.vocab + 31) / 32; i += ctas * kSortThreads) P.present[i] = 0;
+
+    uint2 v[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const uint32_t t = cta * E + at0 + 32 * j;
+        const long long id = t < P.rows ? P.ids[t] : -1;
+        v[j] = make_uint2((uint64_t)id < P.grad.vocab ? (uint32_t)id : P.grad.vocab, t);
+    }
+    for (uint32_t pass = 0; pass < P.passes; ++pass) {
+        const uint32_t shift = pass * P.digit;
+        if (pass) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) v[j] = item[at0 + 32 * j];
+        }
+        for (uint32_t i = threadIdx.x; i < kWarps * bins / 8; i += kSortThreads) reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        uint16_t* mine = count + warp * bins;
+        uint32_t rank[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const uint32_t d = v[j].x >> shift & (bins - 1);
+            const uint32_t same = __match_any_sync(kAll, d);
+            const uint32_t seen = mine[d];
+            __syncwarp();
+            if (!(same & before)) mine[d] = (uint16_t)(seen + __popc(same));
+            __syncwarp();
+            rank[j] = seen + __popc(same & before);
+        }
+        __syncthreads();
+        uint32_t n = 0;
+        if (threadIdx.x < bins) {
+#pragma unroll 8
+            for (int w = 0; w < kWarps; ++w) {
+                const uint32_t c = count[w * bins + threadIdx.x];
+                count[w * bins + threadIdx.x] = (uint16_t)n;
+                n += c;
+            }
+            total[threadIdx.x] = n;
+        }
+        cluster_sync();     // every CTA has its tokens in registers and its totals in place
+        uint32_t earlier = 0, all = 0;
+        if (threadIdx.x < bins) {
+            for (uint32_t c = 0; c < ctas; ++c) {
+                const uint32_t t = c == cta ? n : load_remote(total + threadIdx.x, c);
+                if (c < cta) earlier += t;
+                all += t;
+            }
+        }
+        const uint32_t first = scan(all, sums);
+        if (threadIdx.x < bins) place[threadIdx.x] = first + earlier;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const uint32_t d = v[j].x >> shift & (bins - 1);
+            const uint32_t p = place[d] + mine[d] + rank[j];
+            store_remote(item + p % E, p / E, v[j]);
+        }
+        cluster_sync();
+    }
+
+    // runs
+    uint32_t starts[K];     // the warp's starts of each round, a bit a lane
+    uint32_t last = kNone;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const uint32_t at = at0 + 32 * j, p = cta * E + at;
+        v[j] = item[at];
+        const bool there = v[j].x < P.grad.vocab;
+        uint32_t prev = kNone;
+        if (there && p > 0) prev = at ? item[at - 1].x : load_remote(&item[E - 1].x, cta - 1);
+        starts[j] = __ballot_sync(kAll, there && prev != v[j].x);
+        if (starts[j]) last = p - lane + 31 - __clz(starts[j]);
+    }
+    if (lane == 0) last_start[warp] = last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t t = kNone;
+        for (int w = 0; w < kWarps; ++w) t = last_start[w] != kNone ? last_start[w] : t;
+        cta_last = t;
+    }
+    cluster_sync();
+    uint32_t run = kNone;       // the last start before the warp's tokens
+    for (uint32_t c = 0; c < cta; ++c) {
+        const uint32_t t = load_remote(&cta_last, c);
+        if (t != kNone) run = t;
+    }
+    for (uint32_t w = 0; w < warp; ++w)
+        if (last_start[w] != kNone) run = last_start[w];
+
+    // units
+    uint32_t unit[K], begin[K], units = 0;      // the warp's units of each round, a bit a lane; this lane's run
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const uint32_t p = cta * E + at0 + 32 * j, upto = starts[j] & (before << 1 | 1);
+        begin[j] = upto ? p - lane + 31 - __clz(upto) : run;
+        if (starts[j]) run = p - lane + 31 - __clz(starts[j]);
+        unit[j] = __ballot_sync(kAll, v[j].x < P.grad.vocab && (p - begin[j]) % kUnit == 0);
+        units += __popc(unit[j]);
+    }
+    uint32_t number = scan(lane == 0 ? units : 0, sums);
+    if (threadIdx.x == 0) cta_units = sums[31];
+    cluster_sync();
+    uint32_t earlier = 0, all = 0;
+    for (uint32_t c = 0; c < ctas; ++c) {
+        const uint32_t t = load_remote(&cta_units, c);
+        if (c < cta) earlier += t;
+        all += t;
+    }
+    number = __shfl_sync(kAll, number, 0) + earlier;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const uint32_t at = at0 + 32 * j, p = cta * E + at;
+        const uint32_t row = v[j].x;
+        const bool there = row < P.grad.vocab;
+        if (there) {
+            P.tokens[p] = v[j].y;
+            if (unit[j] >> lane & 1) {
+                uint32_t flags = 0;
+                if (p != begin[j]) flags = kPart;
+                else {
+                    // a run longer than a unit has the same row kUnit places on
+                    const uint32_t on = at + kUnit;
+                    const uint32_t later = on < E ? item[on].x : cta + 1 < ctas ? load_remote(&item[on - E].x, cta + 1) : P.grad.vocab;
+                    if (later == row) flags = kPart | kFirst;
+                    if (!P.accumulate) atomicOr(P.present + row / 32, 1u << row % 32);
+                }
+                const uint32_t u = number + __popc(unit[j] & before);
+                P.units[u] = {p | flags, row};
+                if (flags & kFirst) P.longs[atomicAdd(&P.counts->longs, 1u)] = u;
+            }
+            // the last token of all: where the last unit ends
+            const uint32_t next = at + 1 < E ? item[at + 1].x : cta + 1 < ctas ? load_remote(&item[0].x, cta + 1) : P.grad.vocab;
+            if (next >= P.grad.vocab) P.units[all] = {p + 1, P.grad.vocab};
+        }
+        number += __popc(unit[j]);
+    }
+    if (cta == 0 && threadIdx.x == 0) P.counts->units = all;
+    cluster_sync();     // no CTA leaves while another reads its memory
+}
+
+template <int K>
+cudaError_t launch(const EmbeddingGradParams& P, int cluster, cudaStream_t s) {
+    const size_t smem = kSortThreads * K * sizeof(uint2) + 2 * sizeof(uint32_t) * (1 << kSortDigit) + kWarps * sizeof(uint16_t) * (1 << kSortDigit);
+    static_assert(kSortThreads * kMostSortItems * sizeof(uint2) + (8 + 2 * kWarps) * (1 << kSortDigit) <= kMostDynamicSmem, "the sort's shared memory");
+    cudaError_t e = allow_dynamic_smem(token_sort_kernel<K>, smem);
+    if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(token_sort_kernel<K>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return launch_kernel_of(kSortThreads, token_sort_kernel<K>, dim3(cluster, 1, 1), smem, s, cluster > 1 ? cluster : 0, P);
+}
+
+}  // namespace
+
+cudaError_t launch_token_sort(const EmbeddingGradParams& P, int cluster, int items, cudaStream_t s) {
+    switch (items) {
+        case 1: return launch<1>(P, cluster, s);
+        case 2: return launch<2>(P, cluster, s);
+        case 4: return launch<4>(P, cluster, s);
+        case 8: return launch<8>(P, cluster, s);
+        default: return launch<kMostSortItems>(P, cluster, s);
+    }
+}
+
+}  // namespace mr

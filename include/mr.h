@@ -399,11 +399,11 @@ mr_status_t mr_embedding(const void* const* table, const size_t* ld, int W, size
  *   Tokens left out (ids[t] < 0) and past the vocabulary have no row and count
  *     nowhere; their rows of g_out are not read.
  *   workspace: at least mr_embedding_grad_workspace_bytes(rows, vocab, hidden)
- *     bytes of device memory (NULL where that is 0), owned by the caller, on a
- *     16-byte boundary; it needs no initialisation and is scratch after the
+ *     bytes of device memory, owned by the caller, on a 16-byte boundary; it needs no initialisation and is scratch after the
  *     call.  Calls that share a workspace must not run at the same time.
  *   Nothing that is written overlaps anything else.
  */
+#define MR_MAX_EMBEDDING_GRAD_ROWS 262144     /* rows of a call (more: MR_ERR_UNSUPPORTED) */
 size_t mr_embedding_grad_workspace_bytes(size_t rows, size_t vocab, size_t hidden);
 mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, const long long* ids, size_t rows, float scale,
                               void* const* grad, const size_t* ld_grad, int W, size_t vocab, size_t hidden,
