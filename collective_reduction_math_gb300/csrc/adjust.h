@@ -36,12 +36,20 @@ struct AdjustParams {
     uint32_t K;
     const uint32_t* mask;           // null: every token is allowed
     uint64_t ld_mask;               // 32-bit words from a row to the next
+    uint32_t listed;                // columns of a window that the lists may name, at most
+    float ranks_per_col;            // W / vocab
 };
 
 // Where a column of the window stands in the history: bit 31, it is there;
 // bit 30, it has a bias; below, how often the model has said it.
 constexpr uint32_t kSeen = 1u << 31, kBiased = 1u << 30, kTimes = kBiased - 1;
 
-cudaError_t launch_adjust(const AdjustParams& P, int dtype, bool grad, dim3 grid, size_t smem, cudaStream_t s);
+// The listed columns of a window are kept in a hash table in shared memory: a
+// key, a word and a place in the list of the slots taken (at most four fifths).
+constexpr uint32_t kMostListed = 6144;
+__host__ __device__ constexpr uint32_t adjust_slots(uint32_t listed) { return (listed * 5 / 4 + 2) / 2 * 2; }
+constexpr size_t adjust_smem(uint32_t listed) { return (size_t)10 * adjust_slots(listed); }
+
+cudaError_t launch_adjust(const AdjustParams& P, int dtype, bool grad, dim3 grid, cudaStream_t s);
 
 }  // namespace mr

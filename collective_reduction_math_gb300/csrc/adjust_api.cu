@@ -18,7 +18,6 @@ using mr::misaligned;
 using mr::report_error;
 
 constexpr size_t kMostRows = (size_t)1 << 36, kMostStride = (size_t)1 << 40;
-constexpr uint32_t kWindow = 8192;
 
 struct Call {
     const char* what;
@@ -121,20 +120,32 @@ mr_status_t check_adjust(Call& c, const mr_adjust_t* a, bool grad) {
     return MR_OK;
 }
 
+// Columns a CTA takes at a time, and how many of them the lists may name.  Wide
+// windows read the history less often and lose L2 for what they write (4096 x
+// 131072 bf16, histories of 1024 to 2048: 567, 508 and 513 us with windows of
+// 16384, 32768 and 65536); few rows are cut finer, for four CTAs an SM.  Lists
+// too long for the table take windows of which every column fits.
+void plan_windows(mr::AdjustParams& P) {
+    const uint64_t listed = (P.history ? P.ld_history : 0) + P.K;
+    P.window = listed > mr::kMostListed ? 4096 : 32768;
+    while (P.window > 1024 && P.rows * ((P.vocab + P.window - 1) / P.window) < (uint64_t)mr::device_sms() * 4) P.window /= 2;
+    P.windows = (P.vocab + P.window - 1) / P.window;
+    P.listed = (uint32_t)std::min<uint64_t>(listed, P.window);
+    P.ranks_per_col = (float)P.W / (float)P.vocab;
+}
+
 mr_status_t run(Call& c, bool grad, void* stream) {
     mr_status_t st = check_spans(c.spans);
     if (st != MR_OK) return st;
     mr::AdjustParams& P = c.P;
-    P.window = std::min(kWindow, P.vocab);
-    P.windows = (P.vocab + P.window - 1) / P.window;
-    const dim3 grid((unsigned)std::min<uint64_t>(P.rows * P.windows, (uint64_t)mr::device_sms() * 48), 1, 1);
-    const size_t smem = P.history || P.K ? P.window * sizeof(uint32_t) : 0;
-    const cudaError_t e = mr::launch_adjust(P, c.dtype, grad, grid, smem, (cudaStream_t)stream);
+    plan_windows(P);
+    const dim3 grid((unsigned)std::min<uint64_t>(P.rows * P.windows, (uint64_t)1 << 30), 1, 1);
+    const cudaError_t e = mr::launch_adjust(P, c.dtype, grad, grid, (cudaStream_t)stream);
     if (e != cudaSuccess) return report_error(MR_ERR_CUDA, "%s launch failed: %s", c.what, cudaGetErrorString(e));
     mr::count_launch();
     if (mr::debug_log_level() > 0)
-        fprintf(stderr, "[mr] %s dtype=%s W=%d rows=%zu vocab=%u window=%u grid=%u smem=%zu\n", c.what, c.dtype == MR_BF16 ? "bf16" : "fp32",
-                P.W, c.rows, P.vocab, P.window, grid.x, smem);
+        fprintf(stderr, "[mr] %s dtype=%s W=%d rows=%zu vocab=%u window=%u listed=%u grid=%u\n", c.what, c.dtype == MR_BF16 ? "bf16" : "fp32",
+                P.W, c.rows, P.vocab, P.window, P.listed, grid.x);
     return MR_OK;
 }
 

@@ -2,16 +2,22 @@
 // rows of scores that W simulated ranks hold in shards, and the way back.
 //
 // A CTA has a window of a row's columns, which may lie in several shards.  It
-// counts the row's history in shared memory (a word a column), streams the
-// window through with the mask, and then sets the columns of the history and
-// of the biases right, each once: an entry of a list takes its column's word
-// and leaves 0, so the next one with the same token finds nothing to do, and
-// the words are all 0 again for the next window.
+// puts the history's and the biases' columns that lie there into a hash table in
+// shared memory, with the times each occurs; reads their scores, each once, and
+// works out what they become; streams the window through with the mask; and then
+// writes the listed columns over it.  Their scores are read first because the
+// stream finds them in L2 then: after it, they had left L2 again.  A row's
+// history is read once for each of its windows, from L2 after the first.
 #include "adjust.h"
 #include "elements.cuh"
 
 namespace mr {
 namespace {
+
+// Loads that a thread has in flight: vectors (4096 x 131072 bf16 with lists and
+// a mask: 484, 475 and 500 us with 1, 2 and 4 of them, the last at 5 CTAs an SM
+// for its registers), entries of the history, listed columns' scores.
+constexpr int kAhead = 2, kEntries = 4, kGathers = 2;
 
 __device__ __forceinline__ uint64_t clamped(const long long* n, uint64_t row, uint64_t most, uint64_t none) {
     if (!n) return none;
@@ -20,22 +26,66 @@ __device__ __forceinline__ uint64_t clamped(const long long* n, uint64_t row, ui
 }
 
 __device__ __forceinline__ int rank_of(const AdjustParams& P, uint32_t col) {
-    int r = 0;
+    if (P.W == 1) return 0;
+    int r = min(P.W - 1, (int)((float)col * P.ranks_per_col));      // nearly
+    while (P.col0[r] > col) --r;
     while (P.col0[r + 1] <= col) ++r;
     return r;
 }
 
-// Bits [col, col + 32) of a row's mask, as far as `last` (the last column wanted).
-__device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, uint32_t col, uint32_t last) {
-    const uint32_t w = col / 32, lo = mask[w], hi = w < last / 32 ? mask[w + 1] : 0;
-    return __funnelshift_r(lo, hi, col % 32);
+// Bytes that each repeat the head bit of the byte the selector names (8 + its number).
+__device__ __forceinline__ uint32_t spread_heads(uint32_t v, uint32_t selector) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(v), "r"(selector));
+    return r;
+}
+// The words of a vector of which the mask allows no place but those of `bits`.
+// Multiplying four bits by 2^7 + 2^14 + 2^21 + 2^28 puts one at the head of each
+// byte; a byte permutation that spreads heads makes them masks.
+template <int DT, bool GRAD>
+__device__ __forceinline__ void apply_mask(uint32_t (&w)[4], uint32_t bits) {
+    constexpr uint32_t kSpread = 0x10204080u;
+    uint32_t m[4];
+    if constexpr (DT == MR_BF16) {
+        const uint32_t lo = (bits & 15u) * kSpread, hi = (bits >> 4) * kSpread;
+        m[0] = spread_heads(lo, 0x9988);
+        m[1] = spread_heads(lo, 0xbbaa);
+        m[2] = spread_heads(hi, 0x9988);
+        m[3] = spread_heads(hi, 0xbbaa);
+    } else {
+        const uint32_t all = bits * kSpread;
+        m[0] = spread_heads(all, 0x8888);
+        m[1] = spread_heads(all, 0x9999);
+        m[2] = spread_heads(all, 0xaaaa);
+        m[3] = spread_heads(all, 0xbbbb);
+    }
+    constexpr uint32_t kMasked = GRAD ? 0u : DT == MR_BF16 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = (w[k] & m[k]) | (kMasked & ~m[k]);
 }
 
+// The mask's bits of a thread's vectors: kThreads vectors on, the same place in
+// other words.
+template <uint32_t V>
+struct VectorBits {
+    const uint32_t* word;
+    uint32_t shift;
+    static constexpr uint32_t kAll = (1u << V) - 1, kStep = kThreads * V / 32;
+    __device__ __forceinline__ VectorBits(const uint32_t* words, uint32_t col) : word(words + col / 32), shift(col % 32) {}
+    // of the vector j * kThreads on
+    __device__ __forceinline__ uint32_t at(uint32_t j) const {
+        uint32_t b = word[j * kStep] >> shift;
+        if (shift + V > 32) b |= word[j * kStep + 1] << (32 - shift);
+        return b & kAll;
+    }
+};
+__device__ __forceinline__ bool is_allowed(const uint32_t* mask, uint32_t col) { return !mask || (mask[col / 32] >> (col % 32) & 1); }
+
 template <int DT, bool GRAD>
-__device__ __forceinline__ void dense(const AdjustParams& P, uint64_t row, const uint32_t* mask, uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ void stream(const AdjustParams& P, uint64_t row, const uint32_t* mask, uint32_t lo, uint32_t hi) {
     using E = Element<DT>;
     using Raw = typename E::Raw;
-    constexpr uint32_t V = E::kLanes;
+    constexpr uint32_t V = E::kLanes, kAll = VectorBits<V>::kAll;
     const Raw masked = GRAD ? (Raw)0 : (Raw)E::kMinusInf;
     for (int r = rank_of(P, lo); r < P.W && P.col0[r] < hi; ++r) {
         const uint32_t a = max(lo, P.col0[r]), b = min(hi, P.col0[r + 1]);
@@ -50,46 +100,69 @@ __device__ __forceinline__ void dense(const AdjustParams& P, uint64_t row, const
         const uint32_t head = vec ? min(n, (V - at) % V) : n, vectors = (n - head) / V, tail = head + vectors * V;
         for (uint32_t i = threadIdx.x; i < head + (n - tail); i += kThreads) {
             const uint32_t c = i < head ? i : tail + (i - head);
-            const bool keep = !mask || (mask[(a + c) / 32] >> ((a + c) % 32) & 1);
-            if (!keep) to[c] = masked;
+            if (!is_allowed(mask, a + c)) to[c] = masked;
             else if (!in_place) to[c] = from[c];
         }
-        for (uint32_t i = threadIdx.x; i < vectors; i += kThreads) {
-            const uint32_t c = head + i * V;
-            const uint32_t bits = mask ? mask_bits(mask, a + c, a + c + V - 1) & ((1u << V) - 1) : (1u << V) - 1;
-            if (bits == (1u << V) - 1 && in_place) continue;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (bits) v = load16_once(from + c);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t first = head + threadIdx.x * V;
+        const uint32_t mine = threadIdx.x < vectors ? (vectors - threadIdx.x + kThreads - 1) / kThreads : 0;    // this thread's vectors
+        const VectorBits<V> allowed(mask, a + first);
+        from += first;
+        to += first;
+        uint32_t keep[kAhead];      // a round ahead
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (V == 4) {
-                    if (!(bits >> k & 1)) w[k] = masked;
-                } else {
-                    if (!(bits >> (2 * k) & 1)) w[k] = (w[k] & 0xffff0000u) | masked;
-                    if (!(bits >> (2 * k + 1) & 1)) w[k] = (w[k] & 0xffffu) | (uint32_t)masked << 16;
-                }
+        for (uint32_t j = 0; j < kAhead; ++j) keep[j] = mask && j < mine ? allowed.at(j) : kAll;
+        for (uint32_t i = 0; i < mine; i += kAhead) {
+            uint32_t next[kAhead];
+            uint4 v[kAhead];
+#pragma unroll
+            for (uint32_t j = 0; j < kAhead; ++j) {
+                // masked as a whole, or left as it is: not read
+                if (i + j < mine && keep[j] && !(in_place && keep[j] == kAll)) v[j] = load16_once(from + (i + j) * (kThreads * V));
+                else v[j] = make_uint4(0, 0, 0, 0);
             }
-            store16(to + c, make_uint4(w[0], w[1], w[2], w[3]));
+#pragma unroll
+            for (uint32_t j = 0; j < kAhead; ++j) next[j] = mask && i + kAhead + j < mine ? allowed.at(i + kAhead + j) : kAll;
+#pragma unroll
+            for (uint32_t j = 0; j < kAhead; ++j) {
+                if (i + j < mine && !(in_place && keep[j] == kAll)) {
+                    uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                    if (mask) apply_mask<DT, GRAD>(w, keep[j]);
+                    store16(to + (i + j) * (kThreads * V), make_uint4(w[0], w[1], w[2], w[3]));
+                }
+                keep[j] = next[j];
+            }
         }
     }
 }
 
-// Column col's word, taken; its score or gradient set right.
-template <int DT, bool GRAD>
-__device__ __forceinline__ void fix(const AdjustParams& P, uint64_t row, const uint32_t* mask, uint32_t col, uint32_t* word) {
-    using E = Element<DT>;
-    const uint32_t v = atomicExch(word, 0);
-    if (!v || (mask && !(mask[col / 32] >> (col % 32) & 1))) return;
-    const int r = rank_of(P, col);
-    const uint64_t c = col - P.col0[r];
-    const float x = P.x[r] ? E::get(P.x[r], row * P.ldx[r] + c) : 0.0f;
-    const uint32_t times = v & kTimes;
-    float y = GRAD ? E::get(P.in[r], row * P.ldi[r] + c) : x;
-    if ((v & kSeen || times) && P.repetition) {
-        const float rep = P.repetition[row];
-        y = (x > 0.0f) ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+// The listed columns of the window.
+struct Table {
+    uint32_t* key;      // column + 1; 0: free
+    uint32_t* word;
+    uint16_t* taken;    // the slots that are not free
+    uint32_t slots;
+    // a column's word, of a slot that is taken if it has none
+    __device__ __forceinline__ uint32_t* put(uint32_t c, uint32_t* count) const {
+        for (uint32_t h = __umulhi(c * 2654435769u, slots);; h = h + 1 < slots ? h + 1 : 0) {
+            uint32_t k = *(volatile uint32_t*)(key + h);
+            if (k == 0) {
+                k = atomicCAS(key + h, 0u, c + 1);
+                if (k == 0) {
+                    taken[atomicAdd(count, 1u)] = (uint16_t)h;
+                    return word + h;
+                }
+            }
+            if (k == c + 1) return word + h;
+        }
     }
+};
+
+// What a row's listed column becomes.  y: its score, or the gradient that came
+// back to it; x: its score; v: its word.
+template <bool GRAD>
+__device__ __forceinline__ float adjusted(const AdjustParams& P, uint64_t row, uint32_t col, uint32_t v, float x, float y) {
+    const uint32_t times = v & kTimes;
+    if (P.repetition && (v & kSeen || times)) y = x > 0.0f ? __fdiv_rn(y, P.repetition[row]) : __fmul_rn(y, P.repetition[row]);
     if constexpr (!GRAD) {
         if (times) {
             if (P.frequency) y = __fsub_rn(y, __fmul_rn(P.frequency[row], (float)times));
@@ -102,63 +175,99 @@ __device__ __forceinline__ void fix(const AdjustParams& P, uint64_t row, const u
             y = __fadd_rn(y, sum);
         }
     }
-    E::put(P.out[r], row * P.ldo[r] + c, y);
+    return y;
 }
 
-template <int DT, bool GRAD>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant__ AdjustParams P) {
+template <int DT, bool GRAD, bool LISTS>
+__global__ void __launch_bounds__(kThreads, 6) adjust_kernel(const __grid_constant__ AdjustParams P) {
+    using E = Element<DT>;
     extern __shared__ uint32_t words[];
-    const bool lists = P.history || P.K;
-    if (lists)
-        for (uint32_t i = threadIdx.x; i < P.window; i += kThreads) words[i] = 0;
-    pdl_enter();
+    __shared__ uint32_t count;
+    const uint32_t slots = adjust_slots(P.listed);
+    const Table table{words, words + slots, reinterpret_cast<uint16_t*>(words + 2 * slots), slots};
     const uint64_t units = P.rows * P.windows;
+    pdl_enter();
     for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const uint64_t row = u / P.windows;
-        const uint32_t lo = (uint32_t)(u - row * P.windows) * P.window, hi = min(P.vocab, lo + P.window);
+        const uint32_t lo = (uint32_t)(u - row * P.windows) * P.window, width = min(P.vocab - lo, P.window);
         const uint32_t* mask = P.mask ? P.mask + row * P.ld_mask : nullptr;
-        const long long* history = P.history ? P.history + row * P.ld_history : nullptr;
-        const uint64_t n = history ? clamped(P.n_history, row, P.ld_history, P.ld_history) : 0;
-        if (lists) {
-            const uint64_t prompt = history ? clamped(P.n_prompt, row, n, 0) : 0;
+        if constexpr (LISTS) {
+            if (u != blockIdx.x) __syncthreads();       // the last window's listed columns are written
+            for (uint32_t i = threadIdx.x; i < 2 * slots; i += kThreads) words[i] = 0;
+            if (threadIdx.x == 0) count = 0;
             __syncthreads();
-            for (uint64_t i = threadIdx.x; i < n; i += kThreads) {
-                const uint64_t c = (uint64_t)history[i] - lo;
-                if (c >= hi - lo) continue;
-                if (i < prompt) atomicOr(&words[c], kSeen);
-                else atomicAdd(&words[c], 1u);
+            if (P.history) {
+                const long long* history = P.history + row * P.ld_history;
+                const uint64_t n = clamped(P.n_history, row, P.ld_history, P.ld_history), prompt = clamped(P.n_prompt, row, n, 0);
+                for (uint64_t i0 = threadIdx.x; i0 < n; i0 += kEntries * kThreads) {
+                    uint64_t c[kEntries];
+#pragma unroll
+                    for (int j = 0; j < kEntries; ++j) {
+                        const uint64_t i = i0 + j * kThreads;
+                        c[j] = i < n ? (uint64_t)history[i] - lo : ~0ull;
+                    }
+#pragma unroll
+                    for (int j = 0; j < kEntries; ++j) {
+                        if (c[j] >= width) continue;
+                        uint32_t* word = table.put((uint32_t)c[j], &count);
+                        if (i0 + j * kThreads < prompt) atomicOr(word, kSeen);
+                        else atomicAdd(word, 1u);
+                    }
+                }
             }
             for (uint32_t k = threadIdx.x; k < P.K; k += kThreads) {
                 const uint64_t c = (uint64_t)P.bias_ids[row * P.K + k] - lo;
-                if (c < hi - lo) atomicOr(&words[c], kBiased);
+                if (c < width) atomicOr(table.put((uint32_t)c, &count), kBiased);
+            }
+            __syncthreads();
+            for (uint32_t i0 = threadIdx.x; i0 < count; i0 += kGathers * kThreads) {
+                uint32_t h[kGathers], col[kGathers];
+                float x[kGathers], y[kGathers];
+#pragma unroll
+                for (int j = 0; j < kGathers; ++j) {
+                    if (i0 + j * kThreads >= count) continue;
+                    h[j] = table.taken[i0 + j * kThreads];
+                    col[j] = lo + table.key[h[j]] - 1;
+                    const int r = rank_of(P, col[j]);
+                    const uint64_t c = col[j] - P.col0[r];
+                    x[j] = P.x[r] ? E::get(P.x[r], row * P.ldx[r] + c) : 0.0f;
+                    y[j] = GRAD ? E::get(P.in[r], row * P.ldi[r] + c) : x[j];
+                }
+#pragma unroll
+                for (int j = 0; j < kGathers; ++j)
+                    if (i0 + j * kThreads < count)
+                        table.word[h[j]] = __float_as_uint(adjusted<GRAD>(P, row, col[j], table.word[h[j]], x[j], y[j]));
             }
         }
-        dense<DT, GRAD>(P, row, mask, lo, hi);
-        if (lists) {
-            __syncthreads();
-            for (uint64_t i = threadIdx.x; i < n; i += kThreads) {
-                const uint64_t c = (uint64_t)history[i] - lo;
-                if (c < hi - lo) fix<DT, GRAD>(P, row, mask, lo + (uint32_t)c, &words[c]);
-            }
-            for (uint32_t k = threadIdx.x; k < P.K; k += kThreads) {
-                const uint64_t c = (uint64_t)P.bias_ids[row * P.K + k] - lo;
-                if (c < hi - lo) fix<DT, GRAD>(P, row, mask, lo + (uint32_t)c, &words[c]);
+        stream<DT, GRAD>(P, row, mask, lo, lo + width);
+        if constexpr (LISTS) {
+            __syncthreads();        // the window is written
+            for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
+                const uint32_t h = table.taken[i], col = lo + table.key[h] - 1;
+                if (!is_allowed(mask, col)) continue;
+                const int r = rank_of(P, col);
+                E::put(P.out[r], row * P.ldo[r] + (col - P.col0[r]), __uint_as_float(table.word[h]));
             }
         }
     }
 }
 
+template <int DT, bool GRAD, bool LISTS>
+cudaError_t launch(const AdjustParams& P, dim3 grid, cudaStream_t s) {
+    const size_t smem = adjust_smem(LISTS ? P.listed : 0);
+    const cudaError_t e = allow_dynamic_smem(adjust_kernel<DT, GRAD, LISTS>, smem);
+    return e != cudaSuccess ? e : launch_kernel(adjust_kernel<DT, GRAD, LISTS>, grid, smem, s, 0, P);
+}
 template <int DT, bool GRAD>
-cudaError_t launch(const AdjustParams& P, dim3 grid, size_t smem, cudaStream_t s) {
-    const cudaError_t e = allow_dynamic_smem(adjust_kernel<DT, GRAD>, smem);
-    return e != cudaSuccess ? e : launch_kernel(adjust_kernel<DT, GRAD>, grid, smem, s, 0, P);
+cudaError_t launch(const AdjustParams& P, dim3 grid, cudaStream_t s) {
+    return P.listed ? launch<DT, GRAD, true>(P, grid, s) : launch<DT, GRAD, false>(P, grid, s);
 }
 
 }  // namespace
 
-cudaError_t launch_adjust(const AdjustParams& P, int dtype, bool grad, dim3 grid, size_t smem, cudaStream_t s) {
-    if (dtype == MR_BF16) return grad ? launch<MR_BF16, true>(P, grid, smem, s) : launch<MR_BF16, false>(P, grid, smem, s);
-    return grad ? launch<MR_FP32, true>(P, grid, smem, s) : launch<MR_FP32, false>(P, grid, smem, s);
+cudaError_t launch_adjust(const AdjustParams& P, int dtype, bool grad, dim3 grid, cudaStream_t s) {
+    if (dtype == MR_BF16) return grad ? launch<MR_BF16, true>(P, grid, s) : launch<MR_BF16, false>(P, grid, s);
+    return grad ? launch<MR_FP32, true>(P, grid, s) : launch<MR_FP32, false>(P, grid, s);
 }
 
 }  // namespace mr
