@@ -13,6 +13,7 @@ anything elsewhere.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -470,75 +471,92 @@ def mr_distill_topk_step(logits, teacher_ids, teacher_val, weight, loss, grad, m
 # embedding, adjusted scores, gradient norm
 # --------------------------------------------------------------------------
 
+# These calls are short (a single token's take 2 to 6 us of the GPU), and so is
+# the way to them: torch is looked up once, a tensor is asked for what is needed
+# and no more.
+_torch = None
+_current_device = None
+_raw_stream = None
+
+
+def _setup():
+    """torch, and its ways to the current device and stream."""
+    global _torch, _current_device, _raw_stream
+    if _torch is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        _torch = torch
+    return _torch
+
+
 def _on_device(dev, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current; the current stream is that device's."""
-    import torch
-    if torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
             return _on_device(dev, stream, fn, *args)
     if stream is None:
-        direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        stream = direct(dev) if direct is not None else torch.cuda.current_stream().cuda_stream
-    st = fn(*args, stream if isinstance(stream, int) else stream.cuda_stream)
+        stream = _raw_stream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    st = fn(*args, stream)
     if st:
         _raise(st)
 
 
 def _workspace(workspace, need, dev, stream):
-    """The caller's workspace, or one of torch's memory that belongs to the stream of the call."""
-    import torch
+    """(the caller's workspace, or one of torch's memory that belongs to the stream of the call; its address; its bytes)"""
     if workspace is not None:
-        if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace: a contiguous CUDA tensor on the other tensors' device is needed")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if need == 0:
-        return None, None, 0
-    if stream is not None:
-        s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
-        with torch.cuda.stream(s):
-            t = torch.empty(need, dtype=torch.uint8, device=dev)
+    if stream is None:
+        t = _torch.empty(need, dtype=_torch.uint8, device=dev)
     else:
-        t = torch.empty(need, dtype=torch.uint8, device=dev)
+        s = _torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+        with _torch.cuda.stream(s):
+            t = _torch.empty(need, dtype=_torch.uint8, device=dev)
     return t, t.data_ptr(), need
 
 
-def _rows_2d(t, name, dev, what="rows"):
+def _rows_2d(t, name, dev):
     """(address, elements from a row to the next) of a 2-D CUDA tensor whose rows are dense."""
-    if t.dim() != 2 or not t.is_cuda or t.get_device() != dev:
+    if t.dim() != 2 or dev < 0 or t.get_device() != dev:
         raise ValueError(f"{name}: a 2-D CUDA tensor on the other tensors' device is needed")
-    n = t.shape[1]
+    rows, n = t.shape
     ld, step = t.stride()
-    if (step != 1 and n > 1) or (ld < n and t.shape[0] > 1):
+    if (step != 1 and n > 1) or (ld < n and rows > 1):
         raise ValueError(f"{name}: the elements of a row must lie beside each other and rows must not overlap")
     return t.data_ptr(), ld if ld > n else n
 
 
 def _table(tensors, name):
     """W rank buffers [rows of the rank, hidden] -> (pointers, strides, vocab, hidden, dtype code, device)."""
+    _setup()
     if not tensors:
         raise ValueError(f"{name}: empty list of rank buffers")
     W, t0 = len(tensors), tensors[0]
-    dev, hidden, vocab = t0.get_device(), t0.shape[-1], 0
-    ptrs, lds = [], []
+    dev, dtype, hidden, vocab = t0.get_device(), t0.dtype, t0.shape[-1], 0
+    ptrs, lds, rows = (ctypes.c_void_p * W)(), (ctypes.c_size_t * W)(), []
     for r, t in enumerate(tensors):
-        p, ld = _rows_2d(t, f"{name}[{r}]", dev)
-        if t.dtype is not t0.dtype or t.shape[1] != hidden:
+        ptrs[r], lds[r] = _rows_2d(t, name, dev)
+        if t.dtype is not dtype or t.shape[1] != hidden:
             raise ValueError(f"{name}: rank buffers must be of one dtype and row length")
-        ptrs.append(p)
-        lds.append(ld)
-        vocab += t.shape[0]
-    for r, t in enumerate(tensors):
-        if t.shape[0] != (r + 1) * vocab // W - r * vocab // W:
-            raise ValueError(f"{name}[{r}]: {t.shape[0]} rows, but rank {r} of {W} holds rows "
+        rows.append(t.shape[0])
+    vocab = sum(rows)
+    for r, n in enumerate(rows):
+        if n != (r + 1) * vocab // W - r * vocab // W:
+            raise ValueError(f"{name}[{r}]: {n} rows, but rank {r} of {W} holds rows "
                              f"[{r * vocab // W}, {(r + 1) * vocab // W}) of {vocab}")
-    return (ctypes.c_void_p * W)(*ptrs), (ctypes.c_size_t * W)(*lds), vocab, hidden, _dtype_code(t0), dev
+    return ptrs, lds, vocab, hidden, _dtype_code(t0), dev
 
 
 def _array(t, name, shape, dtype, dev):
     """The address of a contiguous array of that shape on that device (None stays None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on the other tensors' device is needed")
     return t.data_ptr()
 
@@ -548,14 +566,13 @@ def mr_embedding(table, ids, out, scale=1.0, stream=None):
     rank, hidden] (fp32 or bf16; rows may be strided); ids: [T] int64, negative
     gives zeros, past the vocabulary NaN; out: [T, hidden] of the table's
     dtype."""
-    from torch import int64
     tp, ld, vocab, hidden, code, dev = _table(table, "table")
     T = ids.numel()
     op, ld_out = _rows_2d(out, "out", dev)
     if out.dtype is not table[0].dtype or out.shape[0] != T or out.shape[1] != hidden:
         raise ValueError(f"out: [{T}, {hidden}] of the table's dtype is needed")
     _on_device(dev, stream, load().mr_embedding, tp, ld, len(table), vocab, hidden, code, scale,
-               _array(ids, "ids", (T,), int64, dev), T, op, ld_out)
+               _array(ids, "ids", (T,), _torch.int64, dev), T, op, ld_out)
 
 
 def mr_embedding_grad_workspace_bytes(rows: int, vocab: int, hidden: int) -> int:
@@ -569,7 +586,6 @@ def mr_embedding_grad(g_out, ids, grad, scale=1.0, accumulate=False, workspace=N
     to what grad holds, else every row is written.  workspace:
     mr_embedding_grad_workspace_bytes(T, vocab, hidden) bytes (None: torch
     provides them)."""
-    from torch import int64
     gp, ld_grad, vocab, hidden, code, dev = _table(grad, "grad")
     T = ids.numel()
     xp, ld_g = _rows_2d(g_out, "g_out", dev)
@@ -577,7 +593,7 @@ def mr_embedding_grad(g_out, ids, grad, scale=1.0, accumulate=False, workspace=N
         raise ValueError(f"g_out: [{T}, {hidden}] is needed")
     L = load()
     keep, ws, n = _workspace(workspace, L.mr_embedding_grad_workspace_bytes(T, vocab, hidden), dev, stream)
-    _on_device(dev, stream, L.mr_embedding_grad, xp, ld_g, _dtype_code(g_out), _array(ids, "ids", (T,), int64, dev), T, scale, gp,
+    _on_device(dev, stream, L.mr_embedding_grad, xp, ld_g, _dtype_code(g_out), _array(ids, "ids", (T,), _torch.int64, dev), T, scale, gp,
                ld_grad, len(grad), vocab, hidden, code, 1 if accumulate else 0, ws, n)
 
 
@@ -588,28 +604,36 @@ def _same_device(tensors, name, dev):
 
 
 def _adjust(rows, vocab, dev, history, n_history, n_prompt, repetition, frequency, presence, bias_ids, bias, mask):
-    from torch import float32, int32, int64
-    L = K = 0
+    int64, float32 = _setup().int64, _torch.float32
+    a = Adjust()
     if history is not None:
         if history.dim() != 2:
             raise ValueError("history: a [rows, entries] tensor is needed")
         L = history.shape[1]
+        h = _array(history, "history", (rows, L), int64, dev)
+        each = (rows,)
+        lists = [_array(n_history, "n_history", each, int64, dev), _array(n_prompt, "n_prompt", each, int64, dev),
+                 _array(repetition, "repetition", each, float32, dev), _array(frequency, "frequency", each, float32, dev),
+                 _array(presence, "presence", each, float32, dev)]
+        if L:           # a history without entries is none
+            a.history, a.history_len = h, L
+            a.n_history, a.n_prompt, a.repetition, a.frequency, a.presence = lists
+    elif not n_history is n_prompt is repetition is frequency is presence is None:
+        raise ValueError("lengths and penalties need a history")
     if bias_ids is not None:
-        if bias_ids.dim() != 2:
-            raise ValueError("bias_ids: a [rows, entries] tensor is needed")
+        if bias_ids.dim() != 2 or bias is None:
+            raise ValueError("bias_ids: a [rows, entries] tensor is needed, and bias with it")
         K = bias_ids.shape[1]
-    ld_mask = 0
+        ids, values = _array(bias_ids, "bias_ids", (rows, K), int64, dev), _array(bias, "bias", (rows, K), float32, dev)
+        if K:
+            a.bias_ids, a.bias, a.bias_count = ids, values, K
+    elif bias is not None:
+        raise ValueError("bias needs bias_ids")
     if mask is not None:
-        if mask.dtype is not int32 or mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] * 32 < vocab:
+        if mask.dtype is not _torch.int32 or mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] * 32 < vocab:
             raise ValueError(f"mask: int32 words [{rows}, {(vocab + 31) // 32}] are needed")
-        mask, ld_mask = _rows_2d(mask, "mask", dev)
-    if L == 0:          # a history without entries is none
-        history = n_history = n_prompt = repetition = frequency = presence = None
-    return Adjust(_array(history, "history", (rows, L), int64, dev), L, _array(n_history, "n_history", (rows,), int64, dev),
-                  _array(n_prompt, "n_prompt", (rows,), int64, dev), _array(repetition, "repetition", (rows,), float32, dev),
-                  _array(frequency, "frequency", (rows,), float32, dev), _array(presence, "presence", (rows,), float32, dev),
-                  _array(bias_ids, "bias_ids", (rows, K), int64, dev) if K else None,
-                  _array(bias, "bias", (rows, K), float32, dev) if K else None, K, mask, ld_mask)
+        a.mask, a.ld_mask = _rows_2d(mask, "mask", dev)
+    return a
 
 
 def _like(logits, tensors, name, rows, vocab, code):
@@ -659,27 +683,34 @@ def mr_grad_norm_workspace_bytes(count: int) -> int:
     return int(load().mr_grad_norm_workspace_bytes(count))
 
 
-def _tensor_list(tensors, name, like=None):
-    """Any number of dense tensors -> (pointers, sizes, dtype codes, device)."""
-    n = len(tensors)
-    dev = tensors[0].get_device() if n else -1
-    ptrs, sizes, codes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)(), (ctypes.c_int * n)()
-    for i, t in enumerate(tensors):
-        if not t.is_contiguous() or t.get_device() != dev or dev < 0:
-            raise ValueError(f"{name}[{i}]: contiguous CUDA tensors on one device are needed")
-        if like is not None and (t.dtype is not like[i].dtype or t.shape != like[i].shape or dev != like[i].get_device()):
-            raise ValueError(f"{name}[{i}]: the shape, dtype and device of the gradient are needed")
-        ptrs[i], sizes[i], codes[i] = t.data_ptr(), t.numel(), _dtype_code(t)
-    return ptrs, sizes, codes, dev
+def _tensor_list(tensors, name):
+    """Any number of dense tensors -> (addresses, sizes, dtype codes, device), as arrays."""
+    T = _setup().Tensor
+    devices = set(map(T.get_device, tensors))
+    if len(devices) > 1 or -1 in devices or not all(map(T.is_contiguous, tensors)):
+        raise ValueError(f"{name}: contiguous CUDA tensors on one device are needed")
+    codes = {_torch.float32: 0, _torch.bfloat16: 1, _torch.int32: 2}
+    try:
+        codes = array.array("i", [codes[t.dtype] for t in tensors])
+    except KeyError as e:
+        raise TypeError(f"{name}: unsupported dtype {e.args[0]}: fp32 or bf16") from None
+    return (array.array("Q", map(T.data_ptr, tensors)), array.array("Q", map(T.numel, tensors)), codes,
+            devices.pop() if devices else -1)
 
 
-def _norm_device(norm, dev):
-    """The device of the call: the tensors', or the norm's where there is no tensor."""
-    if dev < 0:
-        if norm is None or not norm.is_cuda:
+def _norm_call(fn, dev, norm, count, workspace, stream, *args):
+    if dev < 0:         # no tensor: the norm's device
+        if norm is None or norm.get_device() < 0:
             raise ValueError("norm: a CUDA tensor is needed")
-        return norm.get_device()
-    return dev
+        dev = norm.get_device()
+    if norm is not None and (norm.dtype is not _torch.float32 or norm.numel() != 1 or norm.get_device() != dev):
+        raise ValueError("norm: one fp32 value on the gradients' device is needed")
+    keep, ws, n = _workspace(workspace, load().mr_grad_norm_workspace_bytes(count), dev, stream)
+    _on_device(dev, stream, fn, *args, None if norm is None else norm.data_ptr(), ws, n)
+
+
+def _at(a):
+    return a.buffer_info()[0]
 
 
 def mr_grad_norm(grads, norm, workspace=None, stream=None):
@@ -687,30 +718,28 @@ def mr_grad_norm(grads, norm, workspace=None, stream=None):
     bf16, mixed as they come) taken together.  workspace:
     mr_grad_norm_workspace_bytes(len(grads)) bytes (None: torch provides
     them)."""
-    from torch import float32
     ptrs, sizes, codes, dev = _tensor_list(grads, "grads")
-    dev = _norm_device(norm, dev)
-    L = load()
-    keep, ws, n = _workspace(workspace, L.mr_grad_norm_workspace_bytes(len(grads)), dev, stream)
-    _on_device(dev, stream, L.mr_grad_norm, ptrs, sizes, codes, len(grads), _row_ptr(norm, "norm", 1, float32), ws, n)
+    if norm is None:
+        raise ValueError("norm: a CUDA tensor is needed")
+    _norm_call(load().mr_grad_norm, dev, norm, len(grads), workspace, stream, _at(ptrs), _at(sizes), _at(codes), len(grads))
 
 
 def mr_clip_grad_norm(grads, out, max_norm, norm=None, workspace=None, stream=None):
     """out[i] = grads[i] * min(1, max_norm / norm) with the norm of all tensors
     taken together, which ``norm`` (one fp32 value, may be None) receives.
     ``out`` may be ``grads``, in whole or in part."""
-    from torch import float32
     if len(out) != len(grads):
         raise ValueError("out: one tensor for each gradient is needed")
     ptrs, sizes, codes, dev = _tensor_list(grads, "grads")
-    outs = ptrs if out is grads else _tensor_list(out, "out", grads)[0]
-    if dev < 0 and norm is None:
+    outs = ptrs
+    if out is not grads:
+        outs, out_sizes, out_codes, out_dev = _tensor_list(out, "out")
+        if out_sizes != sizes or out_codes != codes or out_dev != dev:
+            raise ValueError("out: tensors of the gradients' sizes, dtypes and device are needed")
+    if not grads and norm is None:
         return
-    dev = _norm_device(norm, dev)
-    L = load()
-    keep, ws, n = _workspace(workspace, L.mr_grad_norm_workspace_bytes(len(grads)), dev, stream)
-    _on_device(dev, stream, L.mr_clip_grad_norm, ptrs, outs, sizes, codes, len(grads), max_norm,
-               _row_ptr(norm, "norm", 1, float32), ws, n)
+    _norm_call(load().mr_clip_grad_norm, dev, norm, len(grads), workspace, stream, _at(ptrs), _at(outs), _at(sizes), _at(codes),
+               len(grads), max_norm)
 
 
 def mr_allreduce_ptrs(send_ptrs, recv_ptrs, N, dtype, op, algo, stream):

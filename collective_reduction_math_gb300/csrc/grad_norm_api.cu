@@ -70,7 +70,7 @@ mr_status_t check(const Call& c, size_t workspace_bytes) {
             return report_error(MR_ERR_INVALID_ARGUMENT, "%s: out[%d] is NULL or not aligned to its element", c.what, i);
         s[k++] = {(uintptr_t)c.out[i], (uintptr_t)c.out[i] + bytes, bytes, bytes, "out", i, true};
     }
-    if (tiles >> 31) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: the tensors are too large together", c.what);
+    if (tiles >> 30) return report_error(MR_ERR_INVALID_ARGUMENT, "%s: the tensors are too large together", c.what);
     s[k++] = {(uintptr_t)c.workspace, (uintptr_t)c.workspace + need, 0, 0, "workspace", -1, true};
     if (c.norm) s[k++] = {(uintptr_t)c.norm, (uintptr_t)c.norm + sizeof(float), 0, 0, "norm", -1, true};
     return mr::check_spans(s.get(), open.get(), k);
@@ -105,7 +105,7 @@ mr_status_t run(const Call& c, float max_norm, cudaStream_t s) {
     for (int j = 0; j < launches(c.count); ++j) {
         const uint32_t tiles = fill(L, c, j * mr::kListTensors);
         if (tiles == 0) continue;
-        const unsigned ctas = std::min<unsigned>({tiles, (unsigned)mr::device_sms() * 6, (unsigned)mr::kMostNormGrid});
+        const unsigned ctas = std::min<unsigned>({tiles, (unsigned)(mr::device_sms() * mr::kNormCtas), (unsigned)mr::kMostNormGrid});
         const cudaError_t e = mr::launch_norm_parts(L, parts + N.count, dim3(ctas, 1, 1), s);
         if (e != cudaSuccess) return failed(c, e);
         mr::count_launch();

@@ -8,12 +8,14 @@
 // and at least 2^-60, what it lost below 2^-126 is nothing beside it; where
 // it overflowed, some |x| is over 2^60 and the second has all that counts;
 // below 2^-60 every |x| is below 2^-30 and the third can neither overflow nor
-// lose a bit that counts.  A thread's sums are fp32 over a tile, then
-// fp32 pairs (the rounding of each addition is kept beside the sum); CTAs and
-// the whole list are joined in 64 bits, over a fixed split: the same bits on
-// every run.
+// lose a bit that counts.  A thread's sums are fp32 over a tile; tiles, threads,
+// CTAs and launches are joined in pairs of floats (the rounding of each addition
+// kept beside the sum), over a fixed split: the same bits on every run.  (In
+// 64 bits the joins took longer than small lists' sums: this GPU does some two
+// such operations a cycle and SM.)
 #include "elements.cuh"
 #include "grad_norm.h"
+#include "packed.cuh"
 
 namespace mr {
 namespace {
@@ -21,40 +23,65 @@ namespace {
 constexpr float kDown = 0x1p-80f, kUp = 0x1p90f;
 constexpr unsigned kAll = 0xffffffffu;
 
-struct Sum3 {
-    float mid = 0.0f, big = 0.0f, small = 0.0f;
-    __device__ __forceinline__ void add(float x) {
-        const float d = __fmul_rn(x, kDown), u = __fmul_rn(x, kUp);
-        mid = __fmaf_rn(x, x, mid);
-        big = __fmaf_rn(d, d, big);
-        small = __fmaf_rn(u, u, small);
+// The squares of a tile, in two lanes each.
+struct TileSum {
+    F2 mid{0}, big{0}, small{0};
+    __device__ __forceinline__ void add(float a, float b) {
+        const F2 x = f2(a, b), d = mul2(x, f2(kDown, kDown)), u = mul2(x, f2(kUp, kUp));
+        mid = fma2(x, x, mid);
+        big = fma2(d, d, big);
+        small = fma2(u, u, small);
     }
 };
 
-// A sum with what its additions lost (nothing once it is no number).
-struct Pair {
-    float hi = 0.0f, lo = 0.0f;
-    __device__ __forceinline__ void add(float x) {
-        const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
-        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
-        hi = s;
-    }
-    __device__ __forceinline__ double value() const { return isfinite(hi) ? (double)hi + (double)lo : (double)hi; }
-};
-
-// A tile of tensor i: the elements [lo, hi), from a 16-byte boundary where lo > 0.
-struct Tile {
-    int i;
-    uint64_t lo, hi;
-};
-template <int DT>
-__device__ __forceinline__ void tile_range(const TensorList& L, int i, uint32_t tile, uint64_t& lo, uint64_t& hi) {
-    constexpr uint64_t per = kTileBytes / Element<DT>::kBytes;
-    const uint64_t n = L.n[i] & ~kIsBf16, before = (uintptr_t)L.in[i] % 16 / Element<DT>::kBytes;
-    const uint64_t p = (uint64_t)(tile - L.tile0[i]) * per;
-    lo = p > before ? p - before : 0;
-    hi = min(n, p + per - before);
+// a + b, and what the addition lost.
+__device__ __forceinline__ SumPair exact_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
+// What was lost is nothing once the sum is no number.
+__device__ __forceinline__ SumPair plus(SumPair p, SumPair q) {
+    const SumPair s = exact_sum(p.hi, q.hi);
+    const float lo = __fadd_rn(s.lo, __fadd_rn(p.lo, q.lo)), hi = __fadd_rn(s.hi, lo);
+    return isfinite(s.hi) ? SumPair{hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))} : SumPair{s.hi, 0.0f};
+}
+__device__ __forceinline__ SumPair plus(SumPair p, F2 lanes) {
+    float a, b;
+    unpack(lanes, a, b);
+    return plus(p, exact_sum(a, b));
+}
+__device__ __forceinline__ NormPart plus(const NormPart& a, const NormPart& b) {
+    return {plus(a.mid, b.mid), plus(a.big, b.big), plus(a.small, b.small)};
+}
+
+// A tile of a tensor: the bytes [first, first + kTileBytes) of it, counted from
+// its start rounded down to 16 bytes, of which [before, end) are its elements.
+struct Tile {
+    const char* base;
+    uint64_t first, before, end;
+    __device__ __forceinline__ Tile(const TensorList& L, int i, uint32_t tile) {
+        before = (uintptr_t)L.in[i] % 16;
+        base = static_cast<const char*>(L.in[i]) - before;
+        first = (uint64_t)(tile - L.tile0[i]) * kTileBytes;
+        end = before + (L.n[i] & ~kIsBf16) * (L.n[i] & kIsBf16 ? 2 : 4);
+    }
+    __device__ __forceinline__ bool whole() const { return first >= before && first + kTileBytes <= end; }
+    // the thread's vector j, and whether it lies in the tensor as a whole
+    __device__ __forceinline__ uint64_t at(uint32_t j) const { return first + (j * kThreads + threadIdx.x) * 16; }
+    __device__ __forceinline__ bool has(uint64_t at) const { return at >= before && at + 16 <= end; }
+    __device__ __forceinline__ void load(uint4 (&v)[kTileVectors]) const {
+        if (whole()) {
+#pragma unroll
+            for (uint32_t j = 0; j < kTileVectors; ++j) v[j] = load16_once(base + at(j));
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < kTileVectors; ++j) {
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (has(at(j))) v[j] = load16_once(base + at(j));
+            }
+        }
+    }
+};
 
 __device__ __forceinline__ int tensor_of(const TensorList& L, uint32_t tile) {
     int lo = 0, hi = L.count;       // tile0[lo] <= tile < tile0[hi]
@@ -67,123 +94,159 @@ __device__ __forceinline__ int tensor_of(const TensorList& L, uint32_t tile) {
 }
 
 template <int DT>
-__device__ __forceinline__ void sum_tile(const TensorList& L, int i, uint32_t tile, Sum3& s) {
+__device__ __forceinline__ void sum_tile(const Tile& t, const uint4 (&v)[kTileVectors], TileSum& s) {
     using E = Element<DT>;
-    constexpr uint32_t V = E::kLanes;
-    uint64_t lo, hi;
-    tile_range<DT>(L, i, tile, lo, hi);
-    const char* p = static_cast<const char*>(L.in[i]);
-    if (hi - lo == kTileBytes / E::kBytes) {        // whole vectors, on their boundaries
-        uint4 v[kTileVectors];
 #pragma unroll
-        for (uint32_t j = 0; j < kTileVectors; ++j) v[j] = load16_once(p + (lo + (j * kThreads + threadIdx.x) * V) * E::kBytes);
+    for (uint32_t j = 0; j < kTileVectors; ++j) {
+        float f[E::kLanes];
+        E::unpack(v[j], f);
 #pragma unroll
-        for (uint32_t j = 0; j < kTileVectors; ++j) {
-            float f[V];
-            E::unpack(v[j], f);
-#pragma unroll
-            for (uint32_t k = 0; k < V; ++k) s.add(f[k]);
-        }
-    } else {
-        for (uint64_t e = lo + threadIdx.x; e < hi; e += kThreads) s.add(E::get(p, e));
+        for (int k = 0; k < E::kLanes; k += 2) s.add(f[k], f[k + 1]);
+    }
+    if (t.whole()) return;
+    // vectors over the tensor's start or end: their elements one by one
+    for (uint32_t j = 0; j < kTileVectors; ++j) {
+        const uint64_t p = t.at(j);
+        if (t.has(p)) continue;
+        for (uint64_t e = max(p, t.before); e < min(p + 16, t.end); e += E::kBytes) s.add(E::get(t.base + e, 0), 0.0f);
     }
 }
 
 // The same on every thread of the CTA (kThreads threads).
 __device__ __forceinline__ NormPart join(NormPart v) {
     __shared__ NormPart part[kThreads / 32];
+#pragma unroll
     for (int d = 16; d; d /= 2) {
-        v.mid += __shfl_xor_sync(kAll, v.mid, d);
-        v.big += __shfl_xor_sync(kAll, v.big, d);
-        v.small += __shfl_xor_sync(kAll, v.small, d);
+        NormPart o;
+        o.mid = {__shfl_xor_sync(kAll, v.mid.hi, d), __shfl_xor_sync(kAll, v.mid.lo, d)};
+        o.big = {__shfl_xor_sync(kAll, v.big.hi, d), __shfl_xor_sync(kAll, v.big.lo, d)};
+        o.small = {__shfl_xor_sync(kAll, v.small.hi, d), __shfl_xor_sync(kAll, v.small.lo, d)};
+        v = plus(v, o);
     }
-    __syncthreads();
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
     NormPart t = part[0];
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) {
-        t.mid += part[w].mid;
-        t.big += part[w].big;
-        t.small += part[w].small;
-    }
+    for (int w = 1; w < kThreads / 32; ++w) t = plus(t, part[w]);
     return t;
 }
 
-__global__ void __launch_bounds__(kThreads) norm_parts_kernel(const __grid_constant__ TensorList L, NormPart* parts) {
-    const uint32_t tiles = L.tile0[L.count];
-    Pair mid, big, small;
-    pdl_enter();
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int i = tensor_of(L, t);
-        Sum3 s;
-        if (L.n[i] & kIsBf16) sum_tile<MR_BF16>(L, i, t, s);
-        else sum_tile<MR_FP32>(L, i, t, s);
-        mid.add(s.mid);
-        big.add(s.big);
-        small.add(s.small);
-    }
-    const NormPart all = join({mid.value(), big.value(), small.value()});
-    if (threadIdx.x == 0) parts[blockIdx.x] = all;
+// The tensor of a tile that is no earlier than tensor i's first.
+__device__ __forceinline__ int tensor_from(const TensorList& L, int i, uint32_t tile) {
+    while (L.tile0[i + 1] <= tile) ++i;
+    return i;
 }
 
-// The norm in 64 bits, on every thread.
-__device__ __forceinline__ double norm_of(const NormOfParts& N) {
-    NormPart v{0.0, 0.0, 0.0};
-    for (int i = threadIdx.x; i < N.count; i += kThreads) {
-        const volatile NormPart& p = N.parts[i];
-        v.mid += p.mid;
-        v.big += p.big;
-        v.small += p.small;
+__global__ void __launch_bounds__(kThreads, kNormCtas) norm_parts_kernel(const __grid_constant__ TensorList L, NormPart* parts) {
+    const uint32_t tiles = L.tile0[L.count];
+    NormPart sum{};
+    int i = tensor_of(L, blockIdx.x);
+    pdl_enter();
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        i = tensor_from(L, i, t);
+        const Tile tile(L, i, t);
+        uint4 v[kTileVectors];
+        tile.load(v);
+        TileSum s;
+        if (L.n[i] & kIsBf16) sum_tile<MR_BF16>(tile, v, s);
+        else sum_tile<MR_FP32>(tile, v, s);
+        sum = {plus(sum.mid, s.mid), plus(sum.big, s.big), plus(sum.small, s.small)};
     }
+    sum = join(sum);
+    if (threadIdx.x == 0) parts[blockIdx.x] = sum;
+}
+
+// The norm as root * 2^power, with what the root is short of; power 0, 80 or -90.
+struct Norm {
+    float root, rest;
+    int power;
+    __device__ __forceinline__ float value() const {
+        return power == 0 ? root : power > 0 ? __fmul_rn(root, 0x1p80f) : __fmul_rn(root, 0x1p-90f);
+    }
+    // max / norm where that is below 1, else 1; NaN where the norm is
+    __device__ __forceinline__ float factor(float max) const {
+        if (isnan(root)) return root;
+        const float scaled = power == 0 ? max : power > 0 ? __fmul_rn(max, 0x1p-80f) : __fmul_rn(max, 0x1p90f);
+        if (!(root > scaled || (root == scaled && rest > 0.0f))) return 1.0f;
+        if (isinf(root)) return 0.0f;
+        // scaled, but where 2^-80 would cost bits of max
+        return power > 0 ? __fmul_rn(__fdiv_rn(max, root), 0x1p-80f) : __fdiv_rn(scaled, root);
+    }
+};
+// On every thread.
+__device__ __forceinline__ Norm norm_of(const NormOfParts& N) {
+    NormPart v{};
+    for (int i = threadIdx.x; i < N.count; i += kThreads) v = plus(v, N.parts[i]);
     v = join(v);
-    if (v.mid >= 0x1p-60 && isfinite(v.mid)) return sqrt(v.mid);
-    if (v.mid < 0x1p-60) return sqrt(v.small) * 0x1p-90;
-    return isnan(v.mid) ? v.mid : sqrt(v.big) * 0x1p80;
+    Norm n;
+    SumPair s = v.mid;
+    n.power = 0;
+    if (s.hi < 0x1p-60f) {
+        s = v.small;
+        n.power = -90;
+    } else if (isinf(s.hi)) {
+        s = v.big;
+        n.power = 80;
+    }
+    n.root = __fsqrt_rn(s.hi);
+    // a step of Newton's iteration for what it lacks
+    n.rest = s.hi > 0.0f && isfinite(s.hi) ? __fdiv_rn(__fadd_rn(__fmaf_rn(-n.root, n.root, s.hi), s.lo), __fmul_rn(2.0f, n.root)) : 0.0f;
+    return n;
 }
 
 __global__ void __launch_bounds__(kThreads) norm_join_kernel(const __grid_constant__ NormOfParts N) {
     pdl_enter();
-    const double norm = norm_of(N);
-    if (threadIdx.x == 0) *N.norm = (float)norm;
+    const Norm norm = norm_of(N);
+    if (threadIdx.x == 0) *N.norm = norm.value();
 }
 
+// The tile's vectors, scaled; `to` is where its base goes.
 template <int DT>
-__device__ __forceinline__ void clip_tile(const TensorList& L, int i, uint32_t tile, float coef) {
+__device__ __forceinline__ void clip_tile(const Tile& t, const uint4 (&v)[kTileVectors], float coef, char* to) {
     using E = Element<DT>;
-    constexpr uint32_t V = E::kLanes;
-    uint64_t lo, hi;
-    tile_range<DT>(L, i, tile, lo, hi);
-    const char* p = static_cast<const char*>(L.in[i]);
-    char* q = static_cast<char*>(L.out[i]);
-    if (hi - lo == kTileBytes / E::kBytes && (uintptr_t)p % 16 == (uintptr_t)q % 16) {
-        uint4 v[kTileVectors];
+    const bool whole = t.whole(), vectors = (uintptr_t)to % 16 == 0;
 #pragma unroll
-        for (uint32_t j = 0; j < kTileVectors; ++j) v[j] = load16_once(p + (lo + (j * kThreads + threadIdx.x) * V) * E::kBytes);
-#pragma unroll
-        for (uint32_t j = 0; j < kTileVectors; ++j) {
-            float f[V];
+    for (uint32_t j = 0; j < kTileVectors; ++j) {
+        const uint64_t p = t.at(j);
+        if (vectors && (whole || t.has(p))) {
+            float f[E::kLanes];
             E::unpack(v[j], f);
 #pragma unroll
-            for (uint32_t k = 0; k < V; ++k) f[k] = __fmul_rn(f[k], coef);
-            store16_once(q + (lo + (j * kThreads + threadIdx.x) * V) * E::kBytes, E::pack(f));
+            for (int k = 0; k < E::kLanes; ++k) f[k] = __fmul_rn(f[k], coef);
+            store16_once(to + p, E::pack(f));
+        } else {
+            for (uint64_t e = max(p, t.before); e < min(p + 16, t.end); e += E::kBytes)
+                E::put(to + e, 0, __fmul_rn(E::get(t.base + e, 0), coef));
         }
-    } else {
-        for (uint64_t e = lo + threadIdx.x; e < hi; e += kThreads) E::put(q, e, __fmul_rn(E::get(p, e), coef));
     }
 }
 
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ TensorList L, const __grid_constant__ NormOfParts N) {
+// The tiles backwards: the last that the norm has read are still in L2.  A CTA's
+// first tile is on its way while the norm is put together.
+__global__ void __launch_bounds__(kThreads, kNormCtas) clip_kernel(const __grid_constant__ TensorList L, const __grid_constant__ NormOfParts N) {
     const uint32_t tiles = L.tile0[L.count];
+    int i = L.count - 1;
+    float coef = 0.0f;
+    bool first = true;
     pdl_enter();
-    const double norm = norm_of(N);
-    if (N.norm && blockIdx.x == 0 && threadIdx.x == 0) *N.norm = (float)norm;
-    const float coef = norm <= (double)N.max_norm ? 1.0f : (float)((double)N.max_norm / norm);     // NaN where the norm is
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int i = tensor_of(L, t);
-        if (coef == 1.0f && L.in[i] == L.out[i]) continue;
-        if (L.n[i] & kIsBf16) clip_tile<MR_BF16>(L, i, t, coef);
-        else clip_tile<MR_FP32>(L, i, t, coef);
+    for (uint32_t k = blockIdx.x; k < tiles; k += gridDim.x) {
+        const uint32_t t = tiles - 1 - k;
+        while (L.tile0[i] > t) --i;
+        const bool in_place = L.in[i] == L.out[i];
+        if (!first && coef == 1.0f && in_place) continue;
+        const Tile tile(L, i, t);
+        uint4 v[kTileVectors];
+        tile.load(v);
+        if (first) {
+            const Norm norm = norm_of(N);
+            if (N.norm && blockIdx.x == 0 && threadIdx.x == 0) *N.norm = norm.value();
+            coef = norm.factor(N.max_norm);
+            first = false;
+            if (coef == 1.0f && in_place) continue;
+        }
+        char* to = static_cast<char*>(L.out[i]) - tile.before;
+        if (L.n[i] & kIsBf16) clip_tile<MR_BF16>(tile, v, coef, to);
+        else clip_tile<MR_FP32>(tile, v, coef, to);
     }
 }
 
