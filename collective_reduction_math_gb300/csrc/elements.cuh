@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mr.h"
 
 namespace mr {
@@ -26,6 +28,16 @@ __device__ __forceinline__ void store16(void* p, uint4 v) {
 // What nothing reads soon.
 __device__ __forceinline__ void store16_once(void* p, uint4 v) {
     asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// A warp clears n bytes from p on (both multiples of B, the element's bytes).
+template <int B>
+__device__ __forceinline__ void clear_bytes(char* p, uint64_t n, uint32_t lane) {
+    using Raw = typename std::conditional<B == 2, uint16_t, uint32_t>::type;
+    const uint64_t head = min(n, (16 - (uintptr_t)p % 16) % 16), body = (n - head) / 16 * 16;
+    for (uint64_t i = lane * B; i < head; i += 32 * B) *reinterpret_cast<Raw*>(p + i) = 0;
+    for (uint64_t i = head + lane * 16; i < head + body; i += 512) store16(p + i, make_uint4(0, 0, 0, 0));
+    for (uint64_t i = head + body + lane * B; i < n; i += 32 * B) *reinterpret_cast<Raw*>(p + i) = 0;
 }
 
 // Two fp32 values to packed bf16, each rounded to nearest even: a in the low half.

@@ -57,6 +57,8 @@ struct EmbeddingGradParams {
     int accumulate;
     uint32_t slabs;                 // warps a unit: kSlab columns each
     uint32_t passes, digit;         // of the sort, and bits in each
+    uint32_t ahead;                 // rows of g asked for from L2 while the sort runs
+    uint32_t cleared;               // table rows cleared meanwhile, a multiple of 8
     // the workspace
     SortCounts* counts;
     uint32_t* tokens;               // by position: the token
@@ -74,11 +76,25 @@ constexpr int kLookupVectors = 4;   // 16-byte vectors a lane takes of a row at 
 constexpr int kSlab = 256;          // columns that a warp of the gradient sums
 constexpr uint32_t kFillBytes = 4096;   // of a row without tokens, that a warp clears at a time
 
+// The buffer row of table row v (v < vocab): an estimate of its rank, put right.
+#ifdef __CUDACC__
+__device__ __forceinline__ char* row_of(const TableRows& T, uint32_t v, int bytes) {
+    int r = 0;
+    if (T.W > 1) {
+        r = min(T.W - 1, (int)((float)v * T.ranks_per_row));
+        while (T.first[r] > v) --r;
+        while (T.first[r + 1] <= v) ++r;
+    }
+    return static_cast<char*>(T.row0[r]) + (uint64_t)(v - T.first[r]) * T.ld[r] * bytes;
+}
+#endif
+
 // vec: every row of the table and of the output starts on a 16-byte boundary
 // and holds whole vectors.
 cudaError_t launch_embedding(const EmbeddingParams& P, int dtype, bool vec, dim3 grid, cudaStream_t s);
-// Sorts P.rows <= cluster * kSortThreads * items tokens and cuts them into units.
-cudaError_t launch_token_sort(const EmbeddingGradParams& P, int cluster, int items, cudaStream_t s);
+// Sorts P.rows <= cluster * kSortThreads * items tokens and cuts them into
+// units; `helpers` more clusters prepare the table and g.
+cudaError_t launch_token_sort(const EmbeddingGradParams& P, int g_dtype, int table_dtype, int cluster, int helpers, int items, cudaStream_t s);
 cudaError_t launch_embedding_sum(const EmbeddingGradParams& P, int g_dtype, int table_dtype, bool vec, dim3 grid, cudaStream_t s);
 cudaError_t launch_embedding_join(const EmbeddingGradParams& P, int table_dtype, dim3 grid, cudaStream_t s);
 

@@ -14,17 +14,6 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// The buffer row of table row v (v < vocab): an estimate of its rank, put right.
-__device__ __forceinline__ char* row_of(const TableRows& T, uint32_t v, int bytes) {
-    int r = 0;
-    if (T.W > 1) {
-        r = min(T.W - 1, (int)((float)v * T.ranks_per_row));
-        while (T.first[r] > v) --r;
-        while (T.first[r + 1] <= v) ++r;
-    }
-    return static_cast<char*>(T.row0[r]) + (uint64_t)(v - T.first[r]) * T.ld[r] * bytes;
-}
-
 // ---------------------------------------------------------------------------
 // Lookup: a warp takes 32 lanes x 4 vectors of 16 bytes (2 KiB) of a row.  A
 // row is left out by a negative id (zeros), and NaN past the vocabulary.
@@ -80,6 +69,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
 // rows of no token.
 // ---------------------------------------------------------------------------
 constexpr int kPer = kSlab / 32;    // columns a lane
+constexpr int kSumCtas = 4;         // CTAs an SM
 
 // column i of lane l: beside one another where they are read in vectors
 template <bool VEC>
@@ -136,51 +126,38 @@ struct Piece {
 };
 
 // Clears kFillBytes of each of eight rows that no token has.
-template <int DT, bool VEC>
+template <int DT>
 __device__ __forceinline__ void fill(const EmbeddingGradParams& P, uint64_t task, uint32_t chunks, uint32_t lane) {
-    using E = Element<DT>;
-    const uint32_t group = (uint32_t)(task / chunks), chunk = (uint32_t)(task - (uint64_t)group * chunks);
-    constexpr uint32_t kColumns = kFillBytes / E::kBytes;
-    const uint32_t there = P.present[group / 4] >> (group % 4 * 8) & 0xffu;
-    const uint64_t c0 = (uint64_t)chunk * kColumns, c1 = min(P.hidden, c0 + kColumns);
-    for (uint32_t i = 0; i < 8; ++i) {
-        const uint32_t v = group * 8 + i;
-        if (v >= P.grad.vocab || there >> i & 1) continue;
-        char* row = row_of(P.grad, v, E::kBytes);
-        if constexpr (VEC) {
-#pragma unroll
-            for (int k = 0; k < (int)(kFillBytes / 512); ++k) {
-                const uint64_t c = c0 + (k * 32 + lane) * E::kLanes;
-                if (c < c1) store16(row + c * E::kBytes, make_uint4(0, 0, 0, 0));
-            }
-        } else {
-            for (uint64_t c = c0 + lane; c < c1; c += 32) E::put(row, c, 0.0f);
-        }
-    }
+    constexpr int b = Element<DT>::kBytes;
+    const uint32_t group = (uint32_t)(task / chunks), chunk = (uint32_t)(task - (uint64_t)group * chunks), first = P.cleared + group * 8;
+    const uint32_t there = P.present[first / 32] >> (first % 32) & 0xffu;
+    const uint64_t from = (uint64_t)chunk * kFillBytes, upto = min(P.hidden * b, from + kFillBytes);
+    for (uint32_t i = 0; i < 8; ++i)
+        if (first + i < P.grad.vocab && !(there >> i & 1)) clear_bytes<b>(row_of(P.grad, first + i, b) + from, upto - from, lane);
 }
 
 template <int DG, int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ EmbeddingGradParams P) {
-    constexpr int kRows = DG == MR_BF16 || !VEC ? 8 : 4;
+__global__ void __launch_bounds__(kThreads, kSumCtas) embedding_sum_kernel(const __grid_constant__ EmbeddingGradParams P) {
+    constexpr int kRows = 4;
     const uint32_t lane = threadIdx.x % 32;
     const uint32_t warps = gridDim.x * (kThreads / 32), first = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     const char* g = static_cast<const char*>(P.g);
+    // from a task to this warp's next: units, and slabs
+    const uint32_t unit_step = warps / P.slabs, slab_step = warps % P.slabs;
+    uint32_t u = first / P.slabs, slab = first % P.slabs;
     pdl_enter();
-    const uint64_t sums = (uint64_t)P.counts->units * P.slabs;
-    const uint32_t chunks = (uint32_t)((P.hidden * Element<DT>::kBytes + kFillBytes - 1) / kFillBytes);
-    const uint64_t tasks = sums + (P.accumulate ? 0 : (uint64_t)((P.grad.vocab + 7) / 8) * chunks);
-    for (uint64_t task = first; task < tasks; task += warps) {
-        if (task >= sums) {
-            fill<DT, VEC>(P, task - sums, chunks, lane);
-            continue;
+    const uint32_t units = P.counts->units;
+    for (; u < units; u += unit_step, slab += slab_step) {
+        if (slab >= P.slabs) {
+            slab -= P.slabs;
+            if (++u >= units) break;
         }
-        const uint32_t u = (uint32_t)(task / P.slabs);
-        const uint64_t c0 = (task - (uint64_t)u * P.slabs) * kSlab;
-        const Unit unit = P.units[u];
-        const uint32_t start = unit.start & kStart, n = (P.units[u + 1].start & kStart) - start;
+        const Unit now = P.units[u];
+        const uint32_t start = now.start & kStart, n = (P.units[u + 1].start & kStart) - start;
         const uint32_t token = lane < n ? P.tokens[start + lane] : 0;
-        char* row = row_of(P.grad, unit.row, Element<DT>::kBytes);
-        const bool whole = !(unit.start & kPart), add = whole && P.accumulate;
+        const uint64_t c0 = (uint64_t)slab * kSlab;
+        char* row = row_of(P.grad, now.row, Element<DT>::kBytes);
+        const bool whole = !(now.start & kPart), add = whole && P.accumulate;
         Piece<DT, VEC> old;
         if (add) old.load(row, c0, P.hidden, lane);
         float acc[kPer];
@@ -202,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
             }
         }
         if (!whole) {
-            float* to = P.partial + partial_slot(start, unit.start & kFirst) * P.ld_partial;
+            float* to = P.partial + partial_slot(start, now.start & kFirst) * P.ld_partial;
             Piece<MR_FP32, VEC>::store(reinterpret_cast<char*>(to), c0, P.hidden, lane, acc);
             continue;
         }
@@ -215,6 +192,15 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
         }
         Piece<DT, VEC>::store(row, c0, P.hidden, lane, acc);
     }
+    if (P.accumulate) return;
+    if (slab >= P.slabs) {
+        slab -= P.slabs;
+        ++u;
+    }
+    // rows of no token, of those not cleared yet
+    const uint32_t chunks = (uint32_t)((P.hidden * Element<DT>::kBytes + kFillBytes - 1) / kFillBytes);
+    const uint64_t tasks = P.cleared < P.grad.vocab ? (uint64_t)((P.grad.vocab - P.cleared + 7) / 8) * chunks : 0;
+    for (uint64_t task = (u - units) * (uint64_t)P.slabs + slab; task < tasks; task += warps) fill<DT>(P, task, chunks, lane);
 }
 
 // A CTA adds a row's partial sums of 128 columns: each warp a run of them,
@@ -234,8 +220,8 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
         const uint64_t c = task % slabs * kJoinColumns + lane * 4;
         const uint32_t start = P.units[u].start & kStart, row = P.units[u].row;
         uint32_t parts = 1;     // the units of this row
-        for (bool all = true; all;) {
-            const uint32_t here = __ballot_sync(kAll, P.units[min(u + parts + lane, units)].row == row);
+        for (bool all = true; all && u + parts < units;) {
+            const uint32_t at = u + parts + lane, here = __ballot_sync(kAll, at < units && P.units[at].row == row);
             parts += __popc(here);
             all = here == kAll;
         }

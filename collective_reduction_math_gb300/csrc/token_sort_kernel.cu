@@ -4,8 +4,8 @@
 // One cluster sorts them all, in its shared memory: a stable radix sort from
 // the lowest digit, of as many passes as the vocabulary's bits need at
 // kSortDigit bits a pass (2 up to a vocabulary of 2^20 - 1).  In a pass a warp
-// ranks its tokens among themselves, round by round (match of the digit, a
-// count a digit and warp); the counts are summed over the CTA's warps, the
+// ranks its tokens among themselves, round by round (votes on the digit's bits,
+// a count a digit and warp); the counts are summed over the CTA's warps, the
 // CTAs' totals are exchanged, and each token goes to its place in the CTA that
 // has it, over distributed shared memory.  Tokens stay in registers between a
 // pass's reads and its writes, so one buffer is enough.
@@ -16,6 +16,7 @@
 // Then the runs of one row: each position finds its run's start (the last
 // start among the lanes, warps and CTAs before it); a unit starts every kUnit
 // positions of a run; units are numbered by a scan.
+#include "elements.cuh"
 #include "embedding.h"
 
 namespace mr {
@@ -78,9 +79,22 @@ __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* sums) {
     return s - v + (warp ? sums[warp - 1] : 0);
 }
 
+// While one cluster sorts, the others ask for the first rows of g from L2 and
+// clear the first rows of the table (those of tokens are written again).
+__device__ __forceinline__ void help(const EmbeddingGradParams& P, int g_bytes, int table_bytes, uint32_t cta, uint32_t ctas) {
+    for (uint32_t t = threadIdx.x * ctas + cta; t < P.ahead; t += ctas * kSortThreads) {
+        const uint64_t p = (uint64_t)P.g + (uint64_t)t * P.ld_g * g_bytes, from = (p + 15) / 16 * 16, upto = (p + P.hidden * g_bytes) / 16 * 16;
+        if (from < upto) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(upto - from)) : "memory");
+    }
+    for (uint32_t v = threadIdx.x / 32 * ctas + cta; v < P.cleared; v += ctas * kWarps) {
+        if (table_bytes == 2) clear_bytes<2>(row_of(P.grad, v, 2), P.hidden * 2, threadIdx.x % 32);
+        else clear_bytes<4>(row_of(P.grad, v, 4), P.hidden * 4, threadIdx.x % 32);
+    }
+}
+
 // x: the key, y: the token
 template <int K>
-__global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(const __grid_constant__ EmbeddingGradParams P) {
+__global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(const __grid_constant__ EmbeddingGradParams P, int g_bytes, int table_bytes) {
     constexpr uint32_t E = kSortThreads * K;        // tokens a CTA
     extern __shared__ uint4 dynamic[];
     uint2* item = reinterpret_cast<uint2*>(dynamic);
@@ -92,7 +106,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(const __gri
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, cta = cluster_rank(), ctas = cluster_ctas();
     const uint32_t before = (1u << lane) - 1;
     const uint32_t at0 = warp * 32 * K + lane;      // this thread's tokens: at0 + 32 j of the CTA's
-    pdl_enter();
+    // no early launch of the next kernel: its CTAs, waiting, took the helpers' places
+    // (777 rows of 1001 into 32003 x 1001 fp32: 30.9 us against 26.7)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x >= ctas) return help(P, g_bytes, table_bytes, blockIdx.x - ctas, gridDim.x - ctas);
 
     if (cta == 0 && threadIdx.x == 0) P.counts->longs = 0;
     if (!P.accumulate)
@@ -115,15 +132,30 @@ __global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(const __gri
         __syncthreads();
         uint16_t* mine = count + warp * bins;
         uint32_t rank[K];
+        // the lanes with a lane's digit, from a vote on each of its bits (the
+        // instruction that matches whole values took longer: 38 against 33 us for
+        // 65536 tokens), some rounds at a time
+        constexpr int kRounds = K < 4 ? K : 4;
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            const uint32_t d = v[j].x >> shift & (bins - 1);
-            const uint32_t same = __match_any_sync(kAll, d);
-            const uint32_t seen = mine[d];
-            __syncwarp();
-            if (!(same & before)) mine[d] = (uint16_t)(seen + __popc(same));
-            __syncwarp();
-            rank[j] = seen + __popc(same & before);
+        for (int j0 = 0; j0 < K; j0 += kRounds) {
+            uint32_t same[kRounds];
+#pragma unroll
+            for (int j = 0; j < kRounds; ++j) same[j] = kAll;
+            for (uint32_t bit = shift; bit < shift + P.digit; ++bit) {
+#pragma unroll
+                for (int j = 0; j < kRounds; ++j) {
+                    const uint32_t ones = __ballot_sync(kAll, v[j0 + j].x >> bit & 1);
+                    same[j] &= v[j0 + j].x >> bit & 1 ? ones : ~ones;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kRounds; ++j) {
+                const uint32_t d = v[j0 + j].x >> shift & (bins - 1), seen = mine[d];
+                __syncwarp();
+                if (!(same[j] & before)) mine[d] = (uint16_t)(seen + __popc(same[j]));
+                __syncwarp();
+                rank[j0 + j] = seen + __popc(same[j] & before);
+            }
         }
         __syncthreads();
         uint32_t n = 0;
@@ -238,24 +270,26 @@ __global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(const __gri
 }
 
 template <int K>
-cudaError_t launch(const EmbeddingGradParams& P, int cluster, cudaStream_t s) {
+cudaError_t launch(const EmbeddingGradParams& P, int g_bytes, int table_bytes, int cluster, int helpers, cudaStream_t s) {
     const size_t smem = kSortThreads * K * sizeof(uint2) + 2 * sizeof(uint32_t) * (1 << kSortDigit) + kWarps * sizeof(uint16_t) * (1 << kSortDigit);
     static_assert(kSortThreads * kMostSortItems * sizeof(uint2) + (8 + 2 * kWarps) * (1 << kSortDigit) <= kMostDynamicSmem, "the sort's shared memory");
     cudaError_t e = allow_dynamic_smem(token_sort_kernel<K>, smem);
     if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(token_sort_kernel<K>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    return launch_kernel_of(kSortThreads, token_sort_kernel<K>, dim3(cluster, 1, 1), smem, s, cluster > 1 ? cluster : 0, P);
+    return launch_kernel_of(kSortThreads, token_sort_kernel<K>, dim3(cluster * (1 + helpers), 1, 1), smem, s, cluster > 1 ? cluster : 0, P,
+                            g_bytes, table_bytes);
 }
 
 }  // namespace
 
-cudaError_t launch_token_sort(const EmbeddingGradParams& P, int cluster, int items, cudaStream_t s) {
+cudaError_t launch_token_sort(const EmbeddingGradParams& P, int g_dtype, int table_dtype, int cluster, int helpers, int items, cudaStream_t s) {
+    const int g = g_dtype == MR_BF16 ? 2 : 4, t = table_dtype == MR_BF16 ? 2 : 4;
     switch (items) {
-        case 1: return launch<1>(P, cluster, s);
-        case 2: return launch<2>(P, cluster, s);
-        case 4: return launch<4>(P, cluster, s);
-        case 8: return launch<8>(P, cluster, s);
-        default: return launch<kMostSortItems>(P, cluster, s);
+        case 1: return launch<1>(P, g, t, cluster, helpers, s);
+        case 2: return launch<2>(P, g, t, cluster, helpers, s);
+        case 4: return launch<4>(P, g, t, cluster, helpers, s);
+        case 8: return launch<8>(P, g, t, cluster, helpers, s);
+        default: return launch<kMostSortItems>(P, g, t, cluster, helpers, s);
     }
 }
 
