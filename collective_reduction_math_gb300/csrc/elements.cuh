@@ -54,7 +54,7 @@ struct Element<MR_FP32> {
     static constexpr int kBytes = 4, kLanes = 4;    // kLanes: elements in 16 bytes
     static constexpr uint32_t kMinusInf = 0xff800000u;
     using Raw = uint32_t;
-    static __device__ __forceinline__ float get(const void* p, uint64_t i) { return static_cast<const volatile float*>(p)[i]; }
+    static __device__ __forceinline__ float get(const void* p, uint64_t i) { return static_cast<const float*>(p)[i]; }
     static __device__ __forceinline__ void put(void* p, uint64_t i, float v) { static_cast<float*>(p)[i] = v; }
     static __device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
         f[0] = __uint_as_float(v.x);
@@ -72,7 +72,7 @@ struct Element<MR_BF16> {
     static constexpr uint32_t kMinusInf = 0xff80u;
     using Raw = uint16_t;
     static __device__ __forceinline__ float get(const void* p, uint64_t i) {
-        return __uint_as_float((uint32_t)static_cast<const volatile uint16_t*>(p)[i] << 16);
+        return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
     }
     static __device__ __forceinline__ void put(void* p, uint64_t i, float v) {
         static_cast<uint16_t*>(p)[i] = (uint16_t)pack_bf16(v, 0.0f);

@@ -48,13 +48,23 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
                 if (there) E::unpack(v[j], f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) f[i] = there ? __fmul_rn(f[i], P.scale) : other;
-                store16(to + c * E::kBytes, E::pack(f));
+                store16_once(to + c * E::kBytes, E::pack(f));
             }
         } else {
-#pragma unroll 8
-            for (int j = 0; j < N; ++j) {
-                const uint64_t c = c0 + (uint64_t)(j * 32 + lane);
-                if (c < P.hidden) E::put(to, c, there ? __fmul_rn(E::get(from, c), P.scale) : other);
+            constexpr int kAhead = 8;       // all read before any is written: the two may be one buffer's columns
+#pragma unroll 1
+            for (int j0 = 0; j0 < N; j0 += kAhead) {
+                float f[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const uint64_t c = c0 + (uint64_t)((j0 + j) * 32 + lane);
+                    f[j] = there && c < P.hidden ? __fmul_rn(E::get(from, c), P.scale) : other;
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const uint64_t c = c0 + (uint64_t)((j0 + j) * 32 + lane);
+                    if (c < P.hidden) E::put(to, c, f[j]);
+                }
             }
         }
     }
