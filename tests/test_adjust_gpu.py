@@ -233,6 +233,57 @@ def test_long_counts(mr):
     _check(mr, _scores(T, V, "fp32", 1), "fp32", 1, a)
 
 
+@pytest.mark.parametrize("L,K", [(6143, 1), (6144, 0), (5200, 944), (6144, 1), (20000, 0), (9000, 1024)])
+def test_long_histories(mr, L, K):
+    """Both sides of the longest list of which a wide window may name every entry, each entry another token."""
+    import torch
+    T, V = 2, 70001
+    g = torch.Generator().manual_seed(L)
+    a = _lists(T, V, L, K, 0.3, 11)
+    a["history"] = torch.stack([torch.randperm(V, generator=g)[:L] for _ in range(T)])
+    a["n_history"], a["n_prompt"] = torch.tensor([L, L]), torch.tensor([L // 3, 0])
+    # a window whose every column is named
+    a["history"][1] = (torch.arange(L) + 8192) % V
+    _check(mr, _scores(T, V, "bf16", 1), "bf16", 2, a)
+    _check(mr, _scores(T, V, "fp32", 1), "fp32", 1, a, in_place=True)
+    _check_grad(mr, _scores(T, V, "bf16", 1), "bf16", 1, a)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_sides_on_other_boundaries(mr, dtype):
+    """Rows of the output elsewhere past a 16-byte boundary than the scores'."""
+    import torch
+    T, V = 3, 9001
+    x = _scores(T, V, dtype, 1)
+    a = _lists(T, V, 300, 9, 0.4, 12)
+    logits, out = Shards(2, x, 3, 1), Shards(2, torch.zeros_like(x), 0, 2)
+    same = Shards(2, torch.zeros_like(x), 3, 1)
+    mr.mr_adjust_logits(logits.views, out.views, **_cuda(a))
+    mr.mr_adjust_logits(logits.views, same.views, **_cuda(a))
+    torch.cuda.synchronize()
+    assert torch.equal(out.host(), same.host())
+    out.fenced()
+
+
+def test_calls_side_by_side(mr):
+    """Two streams at once, other rows and lists on each."""
+    import torch
+    calls = []
+    for k in range(2):
+        x = _scores(40, 30011, "bf16", k).cuda()
+        a = _cuda(_lists(40, 30011, 500 + 100 * k, 8, 0.2, k))
+        want, out = torch.empty_like(x), torch.empty_like(x)
+        mr.mr_adjust_logits([x], [want], **a)
+        calls.append((x, a, want, out, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, a, _, out, stream in calls:
+            mr.mr_adjust_logits([x], [out], stream=stream, **a)
+    torch.cuda.synchronize()
+    for _, _, want, out, _ in calls:
+        assert torch.equal(out, want)
+
+
 def test_column_slices_of_one_buffer(mr):
     import torch
     T, V, W = 4, 1003, 3

@@ -158,6 +158,61 @@ def test_gradient_of_many_tokens(mr, T, kind):
     _check_grad(mr, 1, T, 1 << 17, 16, 0, 0, "bf16", "bf16", True, kind)
 
 
+@pytest.mark.parametrize("T", [131072, 131073, 262144])
+def test_gradient_of_the_most_tokens(mr, T):
+    """Sums of whole numbers, exact in fp32."""
+    import torch
+    V, H = 50021, 8
+    ids = _ids(T, V, 5).cuda()
+    g = torch.randint(-8, 9, (T, H), generator=torch.Generator().manual_seed(1)).float().cuda()
+    grad = torch.empty(V, H, device="cuda")
+    mr.mr_embedding_grad(g, ids, [grad])
+    on = (ids >= 0) & (ids < V)
+    want = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, ids[on], g[on].double())
+    assert torch.equal(grad.double(), want)
+
+
+def test_gradient_of_more_rows_than_a_call_takes(mr):
+    import torch
+    T = 262145
+    with pytest.raises(mr.MRError, match="UNSUPPORTED"):
+        mr.mr_embedding_grad(torch.zeros(T, 1, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda"), [torch.zeros(1, 1, device="cuda")])
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 31, 32, 1023, 1024, (1 << 20) - 1, 1 << 20, (1 << 20) + 1])
+def test_gradient_of_vocabularies_at_the_sort_digits(mr, V):
+    import torch
+    T, H = 3000, 4
+    ids = _ids(T, V, V).cuda()
+    ids[5] = V - 1
+    g = torch.randint(-8, 9, (T, H), generator=torch.Generator().manual_seed(1)).float().cuda()
+    grad = torch.empty(V, H, device="cuda")
+    mr.mr_embedding_grad(g, ids, [grad])
+    on = (ids >= 0) & (ids < V)
+    want = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, ids[on], g[on].double())
+    assert torch.equal(grad.double(), want)
+
+
+def test_gradients_side_by_side(mr):
+    """Two streams at once, a workspace each."""
+    import torch
+    calls = []
+    for k in range(2):
+        T, V, H = 3000 + 1000 * k, 7001, 264
+        g, ids = _random((T, H), "bf16", k).cuda(), _ids(T, V, k).cuda()
+        want, grad = torch.empty(V, H, device="cuda"), torch.empty(V, H, device="cuda")
+        mr.mr_embedding_grad(g, ids, [want])
+        work = torch.empty(mr.mr_embedding_grad_workspace_bytes(T, V, H), dtype=torch.uint8, device="cuda")
+        calls.append((g, ids, want, grad, work, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, ids, _, grad, work, stream in calls:
+            mr.mr_embedding_grad(g, ids, [grad], workspace=work, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, want, grad, _, _ in calls:
+        assert torch.equal(grad, want)
+
+
 def test_gradient_without_tokens(mr):
     import torch
     grad = torch.ones(10, 8, device="cuda")

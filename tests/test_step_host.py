@@ -109,6 +109,7 @@ def test_embedding_gradient_arguments(mr):
     assert _embed(mr, "grad", T=0, ids=None, g=None) == CUDA        # zeros are written
     for kw in (dict(g=EMBED["table"][1]), dict(ids=EMBED["table"][2] + 8), dict(table=[B, B, B + (1 << 30)])):
         assert _embed(mr, "grad", **kw) == ALIAS, kw
+    assert _embed(mr, "grad", T=(1 << 18) + 1, ws_bytes=1 << 60) == UNSUPPORTED
     need = mr.mr_embedding_grad_workspace_bytes(T, V, H)
     if need:
         for kw in (dict(ws=None), dict(ws=_at(3) + 8), dict(ws_bytes=need - 1)):
