@@ -50,6 +50,7 @@ constexpr uint32_t kMostListed = 6144;
 __host__ __device__ constexpr uint32_t adjust_slots(uint32_t listed) { return (listed * 5 / 4 + 2) / 2 * 2; }
 constexpr size_t adjust_smem(uint32_t listed) { return (size_t)10 * adjust_slots(listed); }
 
+constexpr int kAdjustCtas = 6;        // CTAs an SM
 cudaError_t launch_adjust(const AdjustParams& P, int dtype, bool grad, dim3 grid, cudaStream_t s);
 
 }  // namespace mr

@@ -179,7 +179,7 @@ __device__ __forceinline__ float adjusted(const AdjustParams& P, uint64_t row, u
 }
 
 template <int DT, bool GRAD, bool LISTS>
-__global__ void __launch_bounds__(kThreads, 6) adjust_kernel(const __grid_constant__ AdjustParams P) {
+__global__ void __launch_bounds__(kThreads, kAdjustCtas) adjust_kernel(const __grid_constant__ AdjustParams P) {
     using E = Element<DT>;
     extern __shared__ uint32_t words[];
     __shared__ uint32_t count;

@@ -79,7 +79,10 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
 // rows of no token.
 // ---------------------------------------------------------------------------
 constexpr int kPer = kSlab / 32;    // columns a lane
-constexpr int kSumCtas = 4;         // CTAs an SM
+// CTAs an SM, for 16384 rows of 4096 bf16 added to an fp32 table: 3 of them 99 us
+// (with eight rows' loads at a time as with four), 4 83, 5 (which spill) 109;
+// reads and writes that leave nothing in L1 and go first from L2, 80.
+constexpr int kSumCtas = 4;
 
 // column i of lane l: beside one another where they are read in vectors
 template <bool VEC>
@@ -99,7 +102,7 @@ struct Piece {
             const uint64_t c = c0 + column<VEC>(lane, VEC ? i * E::kLanes : i);
             if constexpr (VEC) {
                 w[i] = make_uint4(0, 0, 0, 0);
-                if (c < hidden) w[i] = load16(row + c * E::kBytes);
+                if (c < hidden) w[i] = load16_once(row + c * E::kBytes);
             } else {
                 w[i] = c < hidden ? E::get(row, c) : 0.0f;
             }
@@ -127,7 +130,7 @@ struct Piece {
                 float part[E::kLanes];
 #pragma unroll
                 for (int k = 0; k < E::kLanes; ++k) part[k] = f[i * E::kLanes + k];
-                store16(row + c * E::kBytes, E::pack(part));
+                store16_once(row + c * E::kBytes, E::pack(part));
             } else {
                 E::put(row, c, f[i]);
             }

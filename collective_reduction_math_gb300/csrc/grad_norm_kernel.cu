@@ -225,7 +225,7 @@ __device__ __forceinline__ void clip_tile(const Tile& t, const uint4 (&v)[kTileV
 // first tile is on its way while the norm is put together.
 __global__ void __launch_bounds__(kThreads, kNormCtas) clip_kernel(const __grid_constant__ TensorList L, const __grid_constant__ NormOfParts N) {
     const uint32_t tiles = L.tile0[L.count];
-    int i = L.count - 1;
+    int i = tensor_of(L, tiles - 1 - blockIdx.x);
     float coef = 0.0f;
     bool first = true;
     pdl_enter();

@@ -395,9 +395,10 @@ mr_status_t mr_embedding(const void* const* table, const size_t* ld, int W, size
  *   accumulate == 1: the sums are added to what is there (one fp32 addition,
  *     rounded once); rows of no token are not touched.
  *   The sums are fp32, in an order that depends on ids alone: the same bits on
- *     every run.  Each result is rounded to grad_dtype once.
+ *     every run.  Each result is rounded to grad_dtype once.  (32 tokens of a row
+ *     are added in their order; a row with more has the sums of each 32 added.)
  *   Tokens left out (ids[t] < 0) and past the vocabulary have no row and count
- *     nowhere; their rows of g_out are not read.
+ *     nowhere, whatever their rows of g_out hold.
  *   workspace: at least mr_embedding_grad_workspace_bytes(rows, vocab, hidden)
  *     bytes of device memory, owned by the caller, on a 16-byte boundary; it needs no initialisation and is scratch after the
  *     call.  Calls that share a workspace must not run at the same time.
@@ -432,9 +433,11 @@ mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, 
  *     c % 32 of word c / 32 is set where column c is allowed.  A row may allow
  *     none: all -inf.  NULL: all allowed.  What a masked place held has no part
  *     in anything, a NaN neither.
- *   out[r] may be logits[r] with the same stride (in place): then places that
+ *   out[r] may be logits[r] with the same stride (in place): then 16 bytes that
  *     nothing concerns are neither read nor written.  Else nothing that is
  *     written overlaps anything; rank buffers may be column slices of one buffer.
+ *     Rows of out[r] that start as far past a 16-byte boundary as those of
+ *     logits[r] are written in vectors, others element by element.
  */
 #define MR_MAX_BIAS 1024
 
