@@ -45,12 +45,17 @@ struct AdjustParams {
 constexpr uint32_t kSeen = 1u << 31, kBiased = 1u << 30, kTimes = kBiased - 1;
 
 // The listed columns of a window are kept in a hash table in shared memory: a
-// key, a word and a place in the list of the slots taken (at most four fifths).
+// key, a word and a place in the list of the slots taken (at most four fifths),
+// beside the window's mask.  Windows are a multiple of 1024 columns.
 constexpr uint32_t kMostListed = 6144;
 __host__ __device__ constexpr uint32_t adjust_slots(uint32_t listed) { return (listed * 5 / 4 + 2) / 2 * 2; }
-constexpr size_t adjust_smem(uint32_t listed) { return (size_t)10 * adjust_slots(listed); }
+constexpr size_t adjust_smem(uint32_t listed, uint32_t window) { return (size_t)10 * adjust_slots(listed) + window / 8; }
 
-constexpr int kAdjustCtas = 6;        // CTAs an SM
+// CTAs an SM, and vectors whose loads a thread has in flight.  4096 x 131072
+// bf16 with lists and a mask: 439 us at 6 CTAs with 2 vectors, 430 at 5 with 4,
+// 461 at 4 with 4; with a mask alone 344 at 6 with 2, 372 at 5 with 4.
+__host__ __device__ constexpr int adjust_ctas(bool lists) { return lists ? 5 : 6; }
+__host__ __device__ constexpr uint32_t adjust_ahead(bool lists) { return lists ? 4 : 2; }
 cudaError_t launch_adjust(const AdjustParams& P, int dtype, bool grad, dim3 grid, cudaStream_t s);
 
 }  // namespace mr

@@ -129,7 +129,7 @@ mr_status_t check_adjust(Call& c, const mr_adjust_t* a, bool grad) {
 // column fits.
 void plan_windows(mr::AdjustParams& P) {
     const uint64_t listed = (P.history ? P.ld_history : 0) + P.K;
-    const uint64_t held = (uint64_t)mr::device_sms() * mr::kAdjustCtas / P.rows;        // windows of a row
+    const uint64_t held = (uint64_t)mr::device_sms() * mr::adjust_ctas(listed > 0) / P.rows;        // windows of a row
     P.window = listed > mr::kMostListed ? 4096 : 32768;
     if (held > 0) P.window = (uint32_t)std::min<uint64_t>(P.window, ((P.vocab + held - 1) / held + 1023) / 1024 * 1024);
     P.windows = (P.vocab + P.window - 1) / P.window;

@@ -14,10 +14,8 @@
 namespace mr {
 namespace {
 
-// Loads that a thread has in flight: vectors (4096 x 131072 bf16 with lists and
-// a mask: 484, 475 and 500 us with 1, 2 and 4 of them, the last at 5 CTAs an SM
-// for its registers), entries of the history, listed columns' scores.
-constexpr int kAhead = 2, kEntries = 4, kGathers = 2;
+// Entries of the history, and listed columns' scores, whose loads a thread has in flight.
+constexpr int kEntries = 4, kGathers = 2;
 
 __device__ __forceinline__ uint64_t clamped(const long long* n, uint64_t row, uint64_t most, uint64_t none) {
     if (!n) return none;
@@ -81,8 +79,9 @@ struct VectorBits {
 };
 __device__ __forceinline__ bool is_allowed(const uint32_t* mask, uint32_t col) { return !mask || (mask[col / 32] >> (col % 32) & 1); }
 
-template <int DT, bool GRAD>
-__device__ __forceinline__ void stream(const AdjustParams& P, uint64_t row, const uint32_t* mask, uint32_t lo, uint32_t hi) {
+// mask: the bits from column mask0 on (null: all are allowed).
+template <int DT, bool GRAD, uint32_t kAhead>
+__device__ __forceinline__ void stream(const AdjustParams& P, uint64_t row, const uint32_t* mask, uint32_t mask0, uint32_t lo, uint32_t hi) {
     using E = Element<DT>;
     using Raw = typename E::Raw;
     constexpr uint32_t V = E::kLanes, kAll = VectorBits<V>::kAll;
@@ -100,12 +99,12 @@ __device__ __forceinline__ void stream(const AdjustParams& P, uint64_t row, cons
         const uint32_t head = vec ? min(n, (V - at) % V) : n, vectors = (n - head) / V, tail = head + vectors * V;
         for (uint32_t i = threadIdx.x; i < head + (n - tail); i += kThreads) {
             const uint32_t c = i < head ? i : tail + (i - head);
-            if (!is_allowed(mask, a + c)) to[c] = masked;
+            if (!is_allowed(mask, a + c - mask0)) to[c] = masked;
             else if (!in_place) to[c] = from[c];
         }
         const uint32_t first = head + threadIdx.x * V;
         const uint32_t mine = threadIdx.x < vectors ? (vectors - threadIdx.x + kThreads - 1) / kThreads : 0;    // this thread's vectors
-        const VectorBits<V> allowed(mask, a + first);
+        const VectorBits<V> allowed(mask, a + first - mask0);
         from += first;
         to += first;
         uint32_t keep[kAhead];      // a round ahead
@@ -179,12 +178,13 @@ __device__ __forceinline__ float adjusted(const AdjustParams& P, uint64_t row, u
 }
 
 template <int DT, bool GRAD, bool LISTS>
-__global__ void __launch_bounds__(kThreads, kAdjustCtas) adjust_kernel(const __grid_constant__ AdjustParams P) {
+__global__ void __launch_bounds__(kThreads, adjust_ctas(LISTS)) adjust_kernel(const __grid_constant__ AdjustParams P) {
     using E = Element<DT>;
     extern __shared__ uint32_t words[];
     __shared__ uint32_t count;
     const uint32_t slots = adjust_slots(P.listed);
     const Table table{words, words + slots, reinterpret_cast<uint16_t*>(words + 2 * slots), slots};
+    uint32_t* const bits = words + 2 * slots + slots / 2;      // the window's mask
     const uint64_t units = P.rows * P.windows;
     pdl_enter();
     for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -195,6 +195,10 @@ __global__ void __launch_bounds__(kThreads, kAdjustCtas) adjust_kernel(const __g
             if (u != blockIdx.x) __syncthreads();       // the last window's listed columns are written
             for (uint32_t i = threadIdx.x; i < 2 * slots; i += kThreads) words[i] = 0;
             if (threadIdx.x == 0) count = 0;
+            // the stream would wait for the mask each time it asks for scores (4096 x 131072
+            // bf16: 468 us, with the window's mask in shared memory 439)
+            if (mask)
+                for (uint32_t i = threadIdx.x; i < (width + 31) / 32; i += kThreads) bits[i] = mask[lo / 32 + i];
             __syncthreads();
             if (P.history) {
                 const long long* history = P.history + row * P.ld_history;
@@ -239,12 +243,14 @@ __global__ void __launch_bounds__(kThreads, kAdjustCtas) adjust_kernel(const __g
                         table.word[h[j]] = __float_as_uint(adjusted<GRAD>(P, row, col[j], table.word[h[j]], x[j], y[j]));
             }
         }
-        stream<DT, GRAD>(P, row, mask, lo, lo + width);
-        if constexpr (LISTS) {
+        if constexpr (!LISTS) {
+            stream<DT, GRAD, adjust_ahead(false)>(P, row, mask, 0, lo, lo + width);
+        } else {
+            stream<DT, GRAD, adjust_ahead(true)>(P, row, mask ? bits : nullptr, lo, lo, lo + width);
             __syncthreads();        // the window is written
             for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
                 const uint32_t h = table.taken[i], col = lo + table.key[h] - 1;
-                if (!is_allowed(mask, col)) continue;
+                if (!is_allowed(mask ? bits : nullptr, col - lo)) continue;
                 const int r = rank_of(P, col);
                 E::put(P.out[r], row * P.ldo[r] + (col - P.col0[r]), __uint_as_float(table.word[h]));
             }
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, kAdjustCtas) adjust_kernel(const __g
 
 template <int DT, bool GRAD, bool LISTS>
 cudaError_t launch(const AdjustParams& P, dim3 grid, cudaStream_t s) {
-    const size_t smem = adjust_smem(LISTS ? P.listed : 0);
+    const size_t smem = LISTS ? adjust_smem(P.listed, P.window) : 0;
     const cudaError_t e = allow_dynamic_smem(adjust_kernel<DT, GRAD, LISTS>, smem);
     return e != cudaSuccess ? e : launch_kernel(adjust_kernel<DT, GRAD, LISTS>, grid, smem, s, 0, P);
 }
