@@ -139,11 +139,10 @@ def load():
 # --------------------------------------------------------------------------
 
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.float32: 0, torch.bfloat16: 1, torch.int32: 2}
-    if t.dtype not in codes:
+    _setup()
+    if t.dtype not in _codes:
         raise TypeError(f"unsupported dtype {t.dtype}: fp32, bf16 or int32")
-    return codes[t.dtype]
+    return _codes[t.dtype]
 
 
 def _pointers(tensors):
@@ -477,16 +476,18 @@ def mr_distill_topk_step(logits, teacher_ids, teacher_val, weight, loss, grad, m
 _torch = None
 _current_device = None
 _raw_stream = None
+_codes = None       # of the dtypes
 
 
 def _setup():
     """torch, and its ways to the current device and stream."""
-    global _torch, _current_device, _raw_stream
+    global _torch, _current_device, _raw_stream, _codes
     if _torch is None:
         import torch
         _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
                        or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        _codes = {torch.float32: 0, torch.bfloat16: 1, torch.int32: 2}
         _torch = torch
     return _torch
 
@@ -518,6 +519,11 @@ def _workspace(workspace, need, dev, stream):
         with _torch.cuda.stream(s):
             t = _torch.empty(need, dtype=_torch.uint8, device=dev)
     return t, t.data_ptr(), need
+
+
+def _at(a):
+    """The address of an array's elements."""
+    return a.buffer_info()[0]
 
 
 def _rows_2d(t, name, dev):
@@ -597,27 +603,51 @@ def mr_embedding_grad(g_out, ids, grad, scale=1.0, accumulate=False, workspace=N
                ld_grad, len(grad), vocab, hidden, code, 1 if accumulate else 0, ws, n)
 
 
-def _same_device(tensors, name, dev):
-    for r, t in enumerate(tensors):
-        if t.get_device() != dev:
-            raise ValueError(f"{name}[{r}]: on another device than the other tensors")
+def _columns(tensors, name, like=None):
+    """W rank buffers [rows, columns of the rank] -> (addresses, strides, widths, rows, dtype, device), the
+    first two as arrays; `like`: the answer for the buffers that these have to be alike."""
+    _setup()
+    if not tensors:
+        raise ValueError(f"{name}: empty list of rank buffers")
+    t0 = tensors[0]
+    dev, dtype, rows = t0.get_device(), t0.dtype, t0.shape[0]
+    ptrs, lds, widths = array.array("Q"), array.array("Q"), []
+    for t in tensors:
+        shape = t.shape
+        if len(shape) != 2 or dev < 0 or t.get_device() != dev or t.dtype is not dtype or shape[0] != rows:
+            raise ValueError(f"{name}: rank buffers must be 2-D CUDA tensors [rows, columns] of one dtype on one device")
+        n = shape[1]
+        ld, step = t.stride()
+        if (step != 1 and n > 1) or (ld < n and rows > 1):
+            raise ValueError(f"{name}: the columns of a row must lie beside each other and rows must not overlap")
+        ptrs.append(t.data_ptr())
+        lds.append(ld if ld > n else n)
+        widths.append(n)
+    if like is None:
+        W, vocab = len(tensors), sum(widths)
+        for r, n in enumerate(widths):
+            if n != (r + 1) * vocab // W - r * vocab // W:
+                raise ValueError(f"{name}[{r}]: {n} columns, but rank {r} of {W} holds columns "
+                                 f"[{r * vocab // W}, {(r + 1) * vocab // W}) of {vocab}")
+    elif (widths, rows, dtype, dev) != like[2:]:
+        raise ValueError(f"{name}: rank buffers of the scores' shape, dtype and device are needed")
+    return ptrs, lds, widths, rows, dtype, dev
 
 
 def _adjust(rows, vocab, dev, history, n_history, n_prompt, repetition, frequency, presence, bias_ids, bias, mask):
-    int64, float32 = _setup().int64, _torch.float32
-    a = Adjust()
+    int64, float32, each = _torch.int64, _torch.float32, (rows,)
+    h = ids = values = m = None
+    L = K = ld_mask = 0
     if history is not None:
         if history.dim() != 2:
             raise ValueError("history: a [rows, entries] tensor is needed")
         L = history.shape[1]
         h = _array(history, "history", (rows, L), int64, dev)
-        each = (rows,)
-        lists = [_array(n_history, "n_history", each, int64, dev), _array(n_prompt, "n_prompt", each, int64, dev),
-                 _array(repetition, "repetition", each, float32, dev), _array(frequency, "frequency", each, float32, dev),
-                 _array(presence, "presence", each, float32, dev)]
-        if L:           # a history without entries is none
-            a.history, a.history_len = h, L
-            a.n_history, a.n_prompt, a.repetition, a.frequency, a.presence = lists
+        n_history, n_prompt = _array(n_history, "n_history", each, int64, dev), _array(n_prompt, "n_prompt", each, int64, dev)
+        repetition = _array(repetition, "repetition", each, float32, dev)
+        frequency, presence = _array(frequency, "frequency", each, float32, dev), _array(presence, "presence", each, float32, dev)
+        if L == 0:          # a history without entries is none
+            h = n_history = n_prompt = repetition = frequency = presence = None
     elif not n_history is n_prompt is repetition is frequency is presence is None:
         raise ValueError("lengths and penalties need a history")
     if bias_ids is not None:
@@ -625,22 +655,15 @@ def _adjust(rows, vocab, dev, history, n_history, n_prompt, repetition, frequenc
             raise ValueError("bias_ids: a [rows, entries] tensor is needed, and bias with it")
         K = bias_ids.shape[1]
         ids, values = _array(bias_ids, "bias_ids", (rows, K), int64, dev), _array(bias, "bias", (rows, K), float32, dev)
-        if K:
-            a.bias_ids, a.bias, a.bias_count = ids, values, K
+        if K == 0:
+            ids = values = None
     elif bias is not None:
         raise ValueError("bias needs bias_ids")
     if mask is not None:
         if mask.dtype is not _torch.int32 or mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] * 32 < vocab:
             raise ValueError(f"mask: int32 words [{rows}, {(vocab + 31) // 32}] are needed")
-        a.mask, a.ld_mask = _rows_2d(mask, "mask", dev)
-    return a
-
-
-def _like(logits, tensors, name, rows, vocab, code):
-    p, ld, t_rows, t_vocab, t_code = _score_rows(tensors, name)
-    if len(tensors) != len(logits) or t_rows != rows or t_vocab != vocab or t_code != code:
-        raise ValueError(f"{name}: rank buffers of the scores' shape and dtype are needed")
-    return p, ld
+        m, ld_mask = _rows_2d(mask, "mask", dev)
+    return Adjust(h, L, n_history, n_prompt, repetition, frequency, presence, ids, values, K, m, ld_mask)
 
 
 def mr_adjust_logits(logits, out, history=None, n_history=None, n_prompt=None, repetition=None, frequency=None, presence=None,
@@ -653,13 +676,13 @@ def mr_adjust_logits(logits, out, history=None, n_history=None, n_prompt=None, r
     output), frequency and presence (output only): [T] fp32.  bias_ids [T, K]
     int64 and bias [T, K] fp32.  mask: [T, ceil(vocab / 32)] int32 words, bit c %
     32 of word c // 32 set where column c is allowed."""
-    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
-    op, ld_out = _like(logits, out, "out", rows, vocab, code)
-    dev = logits[0].get_device()
-    _same_device(logits, "logits", dev)
-    _same_device(out, "out", dev)
+    x = _columns(logits, "logits")
+    o = _columns(out, "out", x)
+    xp, ld, widths, rows, _, dev = x
+    vocab = sum(widths)
     a = _adjust(rows, vocab, dev, history, n_history, n_prompt, repetition, frequency, presence, bias_ids, bias, mask)
-    _on_device(dev, stream, load().mr_adjust_logits, xp, ld, len(logits), rows, vocab, code, ctypes.byref(a), op, ld_out)
+    _on_device(dev, stream, load().mr_adjust_logits, _at(xp), _at(ld), len(logits), rows, vocab, _dtype_code(logits[0]),
+               ctypes.addressof(a), _at(o[0]), _at(o[1]))
 
 
 def mr_adjust_logits_grad(logits, g_out, grad, history=None, n_history=None, n_prompt=None, repetition=None, frequency=None,
@@ -668,15 +691,13 @@ def mr_adjust_logits_grad(logits, g_out, grad, history=None, n_history=None, n_p
     rank buffers; may be ``g_out``, not ``logits``) from g_out.  logits are the
     scores as they were before; frequency, presence and biases do not change
     the gradient."""
-    xp, ld, rows, vocab, code = _score_rows(logits, "logits")
-    ip, ld_g = _like(logits, g_out, "g_out", rows, vocab, code)
-    gp, ld_grad = _like(logits, grad, "grad", rows, vocab, code)
-    dev = logits[0].get_device()
-    for t, name in ((logits, "logits"), (g_out, "g_out"), (grad, "grad")):
-        _same_device(t, name, dev)
+    x = _columns(logits, "logits")
+    i, g = _columns(g_out, "g_out", x), _columns(grad, "grad", x)
+    xp, ld, widths, rows, _, dev = x
+    vocab = sum(widths)
     a = _adjust(rows, vocab, dev, history, n_history, n_prompt, repetition, frequency, presence, None, None, mask)
-    _on_device(dev, stream, load().mr_adjust_logits_grad, xp, ld, len(logits), rows, vocab, code, ctypes.byref(a), ip, ld_g, gp,
-               ld_grad)
+    _on_device(dev, stream, load().mr_adjust_logits_grad, _at(xp), _at(ld), len(logits), rows, vocab, _dtype_code(logits[0]),
+               ctypes.addressof(a), _at(i[0]), _at(i[1]), _at(g[0]), _at(g[1]))
 
 
 def mr_grad_norm_workspace_bytes(count: int) -> int:
@@ -689,9 +710,8 @@ def _tensor_list(tensors, name):
     devices = set(map(T.get_device, tensors))
     if len(devices) > 1 or -1 in devices or not all(map(T.is_contiguous, tensors)):
         raise ValueError(f"{name}: contiguous CUDA tensors on one device are needed")
-    codes = {_torch.float32: 0, _torch.bfloat16: 1, _torch.int32: 2}
     try:
-        codes = array.array("i", [codes[t.dtype] for t in tensors])
+        codes = array.array("i", [_codes[t.dtype] for t in tensors])
     except KeyError as e:
         raise TypeError(f"{name}: unsupported dtype {e.args[0]}: fp32 or bf16") from None
     return (array.array("Q", map(T.data_ptr, tensors)), array.array("Q", map(T.numel, tensors)), codes,
@@ -707,10 +727,6 @@ def _norm_call(fn, dev, norm, count, workspace, stream, *args):
         raise ValueError("norm: one fp32 value on the gradients' device is needed")
     keep, ws, n = _workspace(workspace, load().mr_grad_norm_workspace_bytes(count), dev, stream)
     _on_device(dev, stream, fn, *args, None if norm is None else norm.data_ptr(), ws, n)
-
-
-def _at(a):
-    return a.buffer_info()[0]
 
 
 def mr_grad_norm(grads, norm, workspace=None, stream=None):
