@@ -46,8 +46,13 @@ constexpr uint32_t kSeen = 1u << 31, kBiased = 1u << 30, kTimes = kBiased - 1;
 
 // The listed columns of a window are kept in a hash table in shared memory: a
 // key, a word and a place in the list of the slots taken (at most four fifths),
-// beside the window's mask.  Windows are a multiple of 1024 columns.
-constexpr uint32_t kMostListed = 6144;
+// beside the window's mask.  Windows are a multiple of 1024 columns.  Up to
+// kMostListed entries of a row's lists, of which each may name another column,
+// two CTAs fit an SM and wide windows are faster; longer lists take windows of
+// kNarrowWindow columns, each of which has a place (512 x 131072 bf16: histories
+// of 4096 94 us in windows of 32768, 230 in windows of 4096; of 8192 179 and 302;
+// of 12000, one CTA an SM, 379 and 370).
+constexpr uint32_t kMostListed = 8448, kNarrowWindow = 4096;
 __host__ __device__ constexpr uint32_t adjust_slots(uint32_t listed) { return (listed * 5 / 4 + 2) / 2 * 2; }
 constexpr size_t adjust_smem(uint32_t listed, uint32_t window) { return (size_t)10 * adjust_slots(listed) + window / 8; }
 

@@ -125,12 +125,11 @@ mr_status_t check_adjust(Call& c, const mr_adjust_t* a, bool grad) {
 // 131072 bf16, histories of 1024 to 2048: 567, 508 and 513 us with windows of
 // 16384, 32768 and 65536).  Few rows are cut finer, as far as the device holds
 // the windows at once (64 rows: 13 windows of 10240, 19.5 us; 16 of 8192, more than
-// it holds, 22.6).  Lists too long for the table take windows of which every
-// column fits.
+// it holds, 22.6).  For long lists see kMostListed.
 void plan_windows(mr::AdjustParams& P) {
     const uint64_t listed = (P.history ? P.ld_history : 0) + P.K;
     const uint64_t held = (uint64_t)mr::device_sms() * mr::adjust_ctas(listed > 0) / P.rows;        // windows of a row
-    P.window = listed > mr::kMostListed ? 4096 : 32768;
+    P.window = listed > mr::kMostListed ? mr::kNarrowWindow : 32768;
     if (held > 0) P.window = (uint32_t)std::min<uint64_t>(P.window, ((P.vocab + held - 1) / held + 1023) / 1024 * 1024);
     P.windows = (P.vocab + P.window - 1) / P.window;
     P.listed = (uint32_t)std::min<uint64_t>(listed, P.window);

@@ -233,7 +233,7 @@ def test_long_counts(mr):
     _check(mr, _scores(T, V, "fp32", 1), "fp32", 1, a)
 
 
-@pytest.mark.parametrize("L,K", [(6143, 1), (6144, 0), (5200, 944), (6144, 1), (20000, 0), (9000, 1024)])
+@pytest.mark.parametrize("L,K", [(8447, 1), (8448, 0), (7500, 948), (8448, 1), (20000, 0), (9000, 1024)])
 def test_long_histories(mr, L, K):
     """Both sides of the longest list of which a wide window may name every entry, each entry another token."""
     import torch
