@@ -186,15 +186,21 @@ __global__ void __launch_bounds__(kThreads, adjust_ctas(LISTS)) adjust_kernel(co
     const Table table{words, words + slots, reinterpret_cast<uint16_t*>(words + 2 * slots), slots};
     uint32_t* const bits = words + 2 * slots + slots / 2;      // the window's mask
     const uint64_t units = P.rows * P.windows;
+    const auto clear = [&] {
+        for (uint32_t i = threadIdx.x; i < 2 * slots; i += kThreads) words[i] = 0;
+        if (threadIdx.x == 0) count = 0;
+    };
+    if constexpr (LISTS) clear();
     pdl_enter();
     for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const uint64_t row = u / P.windows;
         const uint32_t lo = (uint32_t)(u - row * P.windows) * P.window, width = min(P.vocab - lo, P.window);
         const uint32_t* mask = P.mask ? P.mask + row * P.ld_mask : nullptr;
         if constexpr (LISTS) {
-            if (u != blockIdx.x) __syncthreads();       // the last window's listed columns are written
-            for (uint32_t i = threadIdx.x; i < 2 * slots; i += kThreads) words[i] = 0;
-            if (threadIdx.x == 0) count = 0;
+            if (u != blockIdx.x) {
+                __syncthreads();        // the last window's listed columns are written
+                clear();
+            }
             // the stream would wait for the mask each time it asks for scores (4096 x 131072
             // bf16: 468 us, with the window's mask in shared memory 439)
             if (mask)

@@ -189,6 +189,57 @@ def test_the_same_on_every_run(mr):
     assert len(seen) == 1
 
 
+def test_host_threads(mr):
+    """Threads at once on one stream and on streams of their own, without workspaces of the caller's."""
+    import threading
+
+    import torch
+    lists = [[torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda() * (k + 1) for n in (70001, 300, 5000)] for k in range(4)]
+    wants = [ref.norm(_host(x)) for x in lists]
+    streams = [torch.cuda.current_stream()] * 2 + [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(k):
+        with torch.cuda.stream(streams[k]):
+            norms = [torch.empty(1, device="cuda") for _ in range(200)]
+            for n in norms:
+                mr.mr_grad_norm(lists[k], n)
+            streams[k].synchronize()
+            bad.extend(float(n) for n in norms if not abs(float(n) - wants[k]) <= NORM * wants[k])
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_two_graphs_and_calls_between(mr):
+    """Graphs captured without the caller's workspace, replayed on two streams beside calls on a third."""
+    import torch
+    lists = [[torch.randn(n, generator=torch.Generator().manual_seed(n + k)).cuda() for n in (200000, 77, 3000)] for k in range(3)]
+    wants = [ref.norm(_host(x)) for x in lists]
+    norms = [torch.zeros(1, device="cuda") for _ in range(3)]
+    graphs = []
+    for k in range(2):
+        mr.mr_grad_norm(lists[k], norms[k])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            mr.mr_grad_norm(lists[k], norms[k])
+        graphs.append((g, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        mr.mr_grad_norm(lists[2], norms[2])
+    torch.cuda.synchronize()
+    for n, w in zip(norms, wants):
+        assert abs(float(n) - w) <= NORM * w
+
+
 def test_streams_and_graphs(mr):
     import torch
     x = [torch.randn(n, device="cuda") for n in (5000, 12, 70000)]
