@@ -14,8 +14,11 @@
 namespace mr {
 namespace {
 
-// Entries of the history, and listed columns' scores, whose loads a thread has in flight.
-constexpr int kEntries = 4, kGathers = 2;
+// Entries of the history, and listed columns, whose loads a thread has in
+// flight (4096 x 131072 bf16: 417 us with one column, 420 with two; the gradient,
+// which reads two values a column, 437 and 413).
+constexpr int kEntries = 4;
+__host__ __device__ constexpr int gathers(bool grad) { return grad ? 2 : 1; }
 
 __device__ __forceinline__ uint64_t clamped(const long long* n, uint64_t row, uint64_t most, uint64_t none) {
     if (!n) return none;
@@ -156,38 +159,50 @@ struct Table {
     }
 };
 
-// What a row's listed column becomes.  y: its score, or the gradient that came
-// back to it; x: its score; v: its word.
+// What a row's listed columns become.
 template <bool GRAD>
-__device__ __forceinline__ float adjusted(const AdjustParams& P, uint64_t row, uint32_t col, uint32_t v, float x, float y) {
-    const uint32_t times = v & kTimes;
-    if (P.repetition && (v & kSeen || times)) y = x > 0.0f ? __fdiv_rn(y, P.repetition[row]) : __fmul_rn(y, P.repetition[row]);
-    if constexpr (!GRAD) {
-        if (times) {
-            if (P.frequency) y = __fsub_rn(y, __fmul_rn(P.frequency[row], (float)times));
-            if (P.presence) y = __fsub_rn(y, P.presence[row]);
-        }
-        if (v & kBiased) {
-            float sum = 0.0f;       // a token listed twice has the sum, in the list's order
-            for (uint32_t k = 0; k < P.K; ++k)
-                if (P.bias_ids[row * P.K + k] == (long long)col) sum = __fadd_rn(sum, P.bias[row * P.K + k]);
-            y = __fadd_rn(y, sum);
-        }
+struct Penalties {
+    const AdjustParams& P;
+    uint64_t row;
+    float repetition, frequency, presence;
+    __device__ __forceinline__ Penalties(const AdjustParams& P_, uint64_t row_) : P(P_), row(row_) {
+        repetition = P.repetition ? P.repetition[row] : 1.0f;
+        frequency = !GRAD && P.frequency ? P.frequency[row] : 0.0f;
+        presence = !GRAD && P.presence ? P.presence[row] : 0.0f;
     }
-    return y;
-}
+    // y: the column's score, or the gradient that came back to it; x: its score; v: its word
+    __device__ __forceinline__ float of(uint32_t col, uint32_t v, float x, float y) const {
+        const uint32_t times = v & kTimes;
+        if (P.repetition && (v & kSeen || times)) y = x > 0.0f ? __fdiv_rn(y, repetition) : __fmul_rn(y, repetition);
+        if constexpr (!GRAD) {
+            if (times) {
+                if (P.frequency) y = __fsub_rn(y, __fmul_rn(frequency, (float)times));
+                if (P.presence) y = __fsub_rn(y, presence);
+            }
+            if (v & kBiased) {
+                float sum = 0.0f;       // a token listed twice has the sum, in the list's order
+                for (uint32_t k = 0; k < P.K; ++k)
+                    if (P.bias_ids[row * P.K + k] == (long long)col) sum = __fadd_rn(sum, P.bias[row * P.K + k]);
+                y = __fadd_rn(y, sum);
+            }
+        }
+        return y;
+    }
+};
 
 template <int DT, bool GRAD, bool LISTS>
 __global__ void __launch_bounds__(kThreads, adjust_ctas(LISTS)) adjust_kernel(const __grid_constant__ AdjustParams P) {
     using E = Element<DT>;
-    extern __shared__ uint32_t words[];
+    constexpr int kGathers = gathers(GRAD);
+    extern __shared__ uint4 dynamic[];
+    uint32_t* const words = reinterpret_cast<uint32_t*>(dynamic);
     __shared__ uint32_t count;
     const uint32_t slots = adjust_slots(P.listed);
     const Table table{words, words + slots, reinterpret_cast<uint16_t*>(words + 2 * slots), slots};
     uint32_t* const bits = words + 2 * slots + slots / 2;      // the window's mask
     const uint64_t units = P.rows * P.windows;
     const auto clear = [&] {
-        for (uint32_t i = threadIdx.x; i < 2 * slots; i += kThreads) words[i] = 0;
+        for (uint32_t i = threadIdx.x; i < slots / 2; i += kThreads) dynamic[i] = make_uint4(0, 0, 0, 0);     // keys and words
         if (threadIdx.x == 0) count = 0;
     };
     if constexpr (LISTS) clear();
@@ -205,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, adjust_ctas(LISTS)) adjust_kernel(co
             // bf16: 468 us, with the window's mask in shared memory 439)
             if (mask)
                 for (uint32_t i = threadIdx.x; i < (width + 31) / 32; i += kThreads) bits[i] = mask[lo / 32 + i];
+            const Penalties<GRAD> penalties(P, row);
             __syncthreads();
             if (P.history) {
                 const long long* history = P.history + row * P.ld_history;
@@ -246,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, adjust_ctas(LISTS)) adjust_kernel(co
 #pragma unroll
                 for (int j = 0; j < kGathers; ++j)
                     if (i0 + j * kThreads < count)
-                        table.word[h[j]] = __float_as_uint(adjusted<GRAD>(P, row, col[j], table.word[h[j]], x[j], y[j]));
+                        table.word[h[j]] = __float_as_uint(penalties.of(col[j], table.word[h[j]], x[j], y[j]));
             }
         }
         if constexpr (!LISTS) {
