@@ -121,15 +121,17 @@ mr_status_t check_adjust(Call& c, const mr_adjust_t* a, bool grad) {
 }
 
 // Columns a CTA takes at a time, and how many of them the lists may name.  Wide
-// windows read the history less often and lose L2 for what they write (4096 x
-// 131072 bf16, histories of 1024 to 2048: 567, 508 and 513 us with windows of
-// 16384, 32768 and 65536).  Few rows are cut finer, as far as the device holds
-// the windows at once (64 rows: 13 windows of 10240, 19.5 us; 16 of 8192, more than
-// it holds, 22.6).  For long lists see kMostListed.
-void plan_windows(mr::AdjustParams& P) {
+// windows read the history less often and lose L2 for what they write: 128 KiB
+// of scores, or 64 KiB of gradients, beside which scores are read (4096 x 131072
+// bf16, histories of 1024 to 2048, windows of 64, 128 and 192 KiB: 417, 390 and
+// 407 us, the gradient 413, 422 and 442; 1024 x 131072 fp32 in 128 and 256 KiB:
+// 173 and 184).  Few rows are cut finer, as far as the device holds the windows
+// at once (64 rows: 13 windows of 10240 columns, 19.5 us; 16 of 8192, more than it
+// holds, 22.6).  For long lists see kMostListed.
+void plan_windows(mr::AdjustParams& P, size_t b, bool grad) {
     const uint64_t listed = (P.history ? P.ld_history : 0) + P.K;
     const uint64_t held = (uint64_t)mr::device_sms() * mr::adjust_ctas(listed > 0) / P.rows;        // windows of a row
-    P.window = listed > mr::kMostListed ? mr::kNarrowWindow : 32768;
+    P.window = listed > mr::kMostListed ? mr::kNarrowWindow : (grad ? 1u << 16 : 1u << 17) / (uint32_t)b;
     if (held > 0) P.window = (uint32_t)std::min<uint64_t>(P.window, ((P.vocab + held - 1) / held + 1023) / 1024 * 1024);
     P.windows = (P.vocab + P.window - 1) / P.window;
     P.listed = (uint32_t)std::min<uint64_t>(listed, P.window);
@@ -164,7 +166,7 @@ mr_status_t run(Call& c, bool grad, void* stream) {
     if (st != MR_OK) return st;
     mr::AdjustParams& P = c.P;
     join_ranks(P, c.b);
-    plan_windows(P);
+    plan_windows(P, c.b, grad);
     const dim3 grid((unsigned)std::min<uint64_t>(P.rows * P.windows, (uint64_t)1 << 30), 1, 1);
     const cudaError_t e = mr::launch_adjust(P, c.dtype, grad, grid, (cudaStream_t)stream);
     if (e != cudaSuccess) return report_error(MR_ERR_CUDA, "%s launch failed: %s", c.what, cudaGetErrorString(e));
