@@ -197,11 +197,13 @@ mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, 
     while (vocab >> bits) ++bits;
     P.passes = (bits + mr::kSortDigit - 1) / mr::kSortDigit;
     P.digit = (bits + P.passes - 1) / P.passes;
-    // eight CTAs sort as fast as sixteen (16384 tokens: 17.4 and 19.1 us), which have to be free in one group of SMs
+    // Up to 32768 tokens eight CTAs sort as fast as sixteen, which have to be free in
+    // one group of SMs (the whole call, rows of 256: 16384 tokens 25.4 and 28.8 us,
+    // 32768 33.3 and 32.6); beyond they do not (65536 48.6 and 44.0, 131072 87 and 66).
+    const int most_ctas = rows > 32768 ? mr::kMostSortCluster : mr::kMostSortCluster / 2;
     int cluster = 1, items = 1;
-    while (cluster < 8 && (size_t)mr::kSortThreads * cluster < rows) cluster *= 2;
+    while (cluster < most_ctas && (size_t)mr::kSortThreads * cluster < rows) cluster *= 2;
     while (items < mr::kMostSortItems && (size_t)mr::kSortThreads * cluster * items < rows) items *= 2;
-    while ((size_t)mr::kSortThreads * cluster * items < rows) cluster *= 2;
     // What the other SMs do meanwhile: as much as takes them no longer than the
     // sort.  Clearing 48 MiB of the table, also rows that are then written: 777
     // rows of 1001 into 32003 x 1001 fp32 32.9 us without, 29.7, 26.7 and 27.7
