@@ -28,6 +28,7 @@ __all__ = [
     "mr_allreduce_ptrs", "mr_plan_auto", "mr_plan_ring_order", "mr_plan_tree", "mr_chunk_lo", "mr_launch_count", "mr_launch_floor", "MRError",
     "load", "LIB_PATH",
     "DTYPES", "OPS", "ALGOS", "DISTILL_MODES", "MAX_RANKS", "MAX_TOP", "MAX_TEACHER", "MAX_BIAS",
+    "MAX_EMBEDDING_GRAD_ROWS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmr.so")
@@ -35,6 +36,7 @@ MAX_RANKS = 64
 MAX_TOP = 64            # top alternatives per row of mr_logprob
 MAX_TEACHER = 128       # teacher entries per row of mr_distill_topk
 MAX_BIAS = 1024         # biases per row of mr_adjust_logits
+MAX_EMBEDDING_GRAD_ROWS = 262144    # rows of a call of mr_embedding_grad
 DTYPES = {"fp32": 0, "bf16": 1, "int32": 2}
 OPS = {"sum": 0, "prod": 1, "min": 2, "max": 3, "avg": 4}
 ALGOS = {"ring": 0, "tree": 1, "hier": 2, "auto": 3}
