@@ -14,14 +14,25 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
+// A vector of a row, times the scale, or `other` where there is no row.
+template <int DT>
+__device__ __forceinline__ uint4 scaled(uint4 v, float scale, bool there, float other) {
+    using E = Element<DT>;
+    float f[E::kLanes];
+    E::unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < E::kLanes; ++i) f[i] = there ? __fmul_rn(f[i], scale) : other;
+    return E::pack(f);
+}
+
 // ---------------------------------------------------------------------------
 // Lookup: a warp takes 32 lanes x 4 vectors of 16 bytes (2 KiB) of a row.  A
 // row is left out by a negative id (zeros), and NaN past the vocabulary.
 // ---------------------------------------------------------------------------
-template <int DT, bool VEC>
+template <int DT>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ EmbeddingParams P) {
     using E = Element<DT>;
-    constexpr int V = VEC ? E::kLanes : 1, kPart = 32 * kLookupVectors * E::kLanes, N = kPart / (32 * V);
+    constexpr int V = E::kLanes, kPart = 32 * kLookupVectors * V;
     const uint32_t lane = threadIdx.x % 32;
     const uint64_t warps = (uint64_t)gridDim.x * (kThreads / 32), units = P.rows * P.parts;
     pdl_enter();
@@ -33,40 +44,76 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
         const char* from = there ? row_of(P.table, (uint32_t)id, E::kBytes) : nullptr;
         char* to = static_cast<char*>(P.out) + t * P.ld_out * E::kBytes;
         const float other = id < 0 ? 0.0f : __int_as_float(0x7fffffff);
-        if constexpr (VEC) {
-            uint4 v[N];
+        uint4 v[kLookupVectors];
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const uint64_t c = c0 + (uint64_t)(j * 32 + lane) * V;
-                if (there && c < P.hidden) v[j] = load16(from + c * E::kBytes);
-            }
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const uint64_t c = c0 + (uint64_t)(j * 32 + lane) * V;
-                if (c >= P.hidden) continue;
-                float f[V];
-                if (there) E::unpack(v[j], f);
-#pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = there ? __fmul_rn(f[i], P.scale) : other;
-                store16_once(to + c * E::kBytes, E::pack(f));
-            }
-        } else {
-            constexpr int kAhead = 8;       // all read before any is written: the two may be one buffer's columns
-#pragma unroll 1
-            for (int j0 = 0; j0 < N; j0 += kAhead) {
-                float f[kAhead];
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const uint64_t c = c0 + (uint64_t)((j0 + j) * 32 + lane);
-                    f[j] = there && c < P.hidden ? __fmul_rn(E::get(from, c), P.scale) : other;
-                }
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const uint64_t c = c0 + (uint64_t)((j0 + j) * 32 + lane);
-                    if (c < P.hidden) E::put(to, c, f[j]);
-                }
-            }
+        for (int j = 0; j < kLookupVectors; ++j) {
+            const uint64_t c = c0 + (uint64_t)(j * 32 + lane) * V;
+            if (there && c < P.hidden) v[j] = load16(from + c * E::kBytes);
         }
+#pragma unroll
+        for (int j = 0; j < kLookupVectors; ++j) {
+            const uint64_t c = c0 + (uint64_t)(j * 32 + lane) * V;
+            if (c < P.hidden) store16_once(to + c * E::kBytes, scaled<DT>(v[j], P.scale, there, other));
+        }
+    }
+}
+
+// 16 bytes from place m on of two vectors (m is the same in all lanes).
+__device__ __forceinline__ uint4 from_place(uint4 a, uint4 b, uint32_t m) {
+    const uint32_t s = m % 4 * 8;
+    switch (m / 4) {
+        case 0: return make_uint4(__funnelshift_r(a.x, a.y, s), __funnelshift_r(a.y, a.z, s), __funnelshift_r(a.z, a.w, s), __funnelshift_r(a.w, b.x, s));
+        case 1: return make_uint4(__funnelshift_r(a.y, a.z, s), __funnelshift_r(a.z, a.w, s), __funnelshift_r(a.w, b.x, s), __funnelshift_r(b.x, b.y, s));
+        case 2: return make_uint4(__funnelshift_r(a.z, a.w, s), __funnelshift_r(a.w, b.x, s), __funnelshift_r(b.x, b.y, s), __funnelshift_r(b.y, b.z, s));
+        default: return make_uint4(__funnelshift_r(a.w, b.x, s), __funnelshift_r(b.x, b.y, s), __funnelshift_r(b.y, b.z, s), __funnelshift_r(b.z, b.w, s));
+    }
+}
+
+// Rows that start anywhere.  The vectors are the output row's; where the table's
+// row lies otherwise past a 16-byte boundary, each is made of the two that it
+// lies in.  Those of the first and the last could reach over the row's ends, so
+// these two and what is left at the ends, 4 V - 2 elements at most, go one by one,
+// an element a lane.  (20000 x 2001 bf16: 43.5 us element by element, 27.5
+// so, at four CTAs an SM; 30.8 at three, 41.7 at five, which spill.)
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 4) embedding_any_kernel(const __grid_constant__ EmbeddingParams P) {
+    using E = Element<DT>;
+    constexpr uint32_t V = E::kLanes, kPart = 32 * kLookupVectors;      // vectors
+    const uint32_t lane = threadIdx.x % 32;
+    const uint64_t warps = (uint64_t)gridDim.x * (kThreads / 32), units = P.rows * P.parts;
+    pdl_enter();
+    for (uint64_t u = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; u < units; u += warps) {
+        const uint64_t t = u / P.parts, part = u - t * P.parts;
+        const long long id = P.ids[t];
+        const bool there = id >= 0 && id < (long long)P.table.vocab;
+        char* to = static_cast<char*>(P.out) + t * P.ld_out * E::kBytes;
+        const char* from = there ? row_of(P.table, (uint32_t)id, E::kBytes) : to;      // to: never read
+        const float other = id < 0 ? 0.0f : __int_as_float(0x7fffffff);
+        const uint64_t head = min(P.hidden, (uint64_t)((16 - (uintptr_t)to % 16) % 16 / E::kBytes));
+        const uint64_t vectors = (P.hidden - head) / V;
+        const uint32_t m = (uint32_t)(((uintptr_t)from + head * E::kBytes) % 16);
+        uint64_t lo = 0, hi = vectors;      // the vectors that are moved as such
+        if (m) {
+            lo = vectors > 2 ? 1 : 0;
+            hi = vectors > 2 ? vectors - 1 : 0;
+        }
+        uint4 v[kLookupVectors], w[kLookupVectors];
+#pragma unroll
+        for (int j = 0; j < kLookupVectors; ++j) {
+            const uint64_t i = part * kPart + j * 32 + lane;
+            if (!there || i < lo || i >= hi) continue;
+            const char* p = from + (head + i * V) * E::kBytes - m;
+            v[j] = load16(p);
+            if (m) w[j] = load16(p + 16);
+        }
+#pragma unroll
+        for (int j = 0; j < kLookupVectors; ++j) {
+            const uint64_t i = part * kPart + j * 32 + lane;
+            if (m) v[j] = from_place(v[j], w[j], m);
+            if (i >= lo && i < hi) store16_once(to + (head + i * V) * E::kBytes, scaled<DT>(v[j], P.scale, there, other));
+        }
+        const uint64_t e = lane < head + lo * V ? lane : lane + (hi - lo) * V;
+        if (part == 0 && e < P.hidden) E::put(to, e, there ? __fmul_rn(E::get(from, e), P.scale) : other);
     }
 }
 
@@ -277,11 +324,8 @@ cudaError_t launch_sum(const EmbeddingGradParams& P, bool vec, dim3 grid, cudaSt
 }  // namespace
 
 cudaError_t launch_embedding(const EmbeddingParams& P, int dtype, bool vec, dim3 grid, cudaStream_t s) {
-    if (dtype == MR_BF16)
-        return vec ? launch_kernel(embedding_kernel<MR_BF16, true>, grid, 0, s, 0, P)
-                   : launch_kernel(embedding_kernel<MR_BF16, false>, grid, 0, s, 0, P);
-    return vec ? launch_kernel(embedding_kernel<MR_FP32, true>, grid, 0, s, 0, P)
-               : launch_kernel(embedding_kernel<MR_FP32, false>, grid, 0, s, 0, P);
+    if (dtype == MR_BF16) return launch_kernel(vec ? embedding_kernel<MR_BF16> : embedding_any_kernel<MR_BF16>, grid, 0, s, 0, P);
+    return launch_kernel(vec ? embedding_kernel<MR_FP32> : embedding_any_kernel<MR_FP32>, grid, 0, s, 0, P);
 }
 
 cudaError_t launch_embedding_sum(const EmbeddingGradParams& P, int g_dtype, int table_dtype, bool vec, dim3 grid, cudaStream_t s) {

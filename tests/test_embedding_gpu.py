@@ -104,6 +104,23 @@ def test_lookup(mr, W, T, V, H, pad, offset, dtype):
         out.fenced()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_lookup_at_every_place(mr, dtype):
+    """Rows of the table and of the output at every place past a 16-byte boundary, rows of one vector to a few."""
+    import torch
+    lanes = 8 if dtype == "bf16" else 4
+    for H in list(range(1, 5 * lanes)) + [511, 1030]:
+        table = _random((9, H), dtype, H)
+        ids = torch.tensor([3, 0, 8, -1, 5, 9, 7])
+        want = (table[ids.clamp(0, 8)].float() * 1.5).to(_dt(dtype))
+        want[3], want[5] = 0.0, float("nan")
+        for a in range(lanes):
+            shard, out = Block(9, H, dtype, 1, a, table), Block(7, H, dtype, 2, (3 * a + H) % lanes)
+            mr.mr_embedding([shard.view], ids.cuda(), out.view, scale=1.5)
+            assert torch.equal(out.view.cpu().nan_to_num(99.0), want.nan_to_num(99.0)), (H, a)
+            out.fenced()
+
+
 def test_lookup_keeps_infinities(mr):
     import torch
     for dtype in ("fp32", "bf16"):
