@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "mr_internal.h"
+#include "sort_plan.h"
 
 namespace mr {
 
@@ -33,9 +34,6 @@ struct EmbeddingParams {
 // The gradient's tokens are sorted by their row and cut into units: runs of
 // positions of one row, at most kUnit long, which a warp sums.
 constexpr uint32_t kUnit = 32;
-constexpr int kSortThreads = 1024;
-constexpr int kMostSortItems = 16;      // tokens a thread of the sort holds
-constexpr int kMostSortCluster = 16;
 constexpr int kSortDigit = 10;          // bits sorted in a pass at most
 struct Unit {
     uint32_t start;     // first position; kPart: one of several units of its row, kFirst: the first of them
@@ -92,9 +90,10 @@ __device__ __forceinline__ char* row_of(const TableRows& T, uint32_t v, int byte
 // vec: every row of the table and of the output starts on a 16-byte boundary
 // and holds whole vectors.
 cudaError_t launch_embedding(const EmbeddingParams& P, int dtype, bool vec, dim3 grid, cudaStream_t s);
-// Sorts P.rows <= cluster * kSortThreads * items tokens and cuts them into
-// units; `helpers` more clusters prepare the table and g.
-cudaError_t launch_token_sort(const EmbeddingGradParams& P, int g_dtype, int table_dtype, int cluster, int helpers, int items, cudaStream_t s);
+// CTAs that the current device takes in a cluster of the sort, at most.
+int most_sort_cluster();
+// Sorts P.rows tokens as planned and cuts them into units.
+cudaError_t launch_token_sort(const EmbeddingGradParams& P, int g_dtype, int table_dtype, const SortPlan& plan, cudaStream_t s);
 cudaError_t launch_embedding_sum(const EmbeddingGradParams& P, int g_dtype, int table_dtype, bool vec, dim3 grid, cudaStream_t s);
 cudaError_t launch_embedding_join(const EmbeddingGradParams& P, int table_dtype, dim3 grid, cudaStream_t s);
 

@@ -197,22 +197,13 @@ mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, 
     while (vocab >> bits) ++bits;
     P.passes = (bits + mr::kSortDigit - 1) / mr::kSortDigit;
     P.digit = (bits + P.passes - 1) / P.passes;
-    // Up to 32768 tokens eight CTAs sort as fast as sixteen, which have to be free in
-    // one group of SMs (the whole call, rows of 256: 16384 tokens 25.4 and 28.8 us,
-    // 32768 33.3 and 32.6); beyond they do not (65536 48.6 and 44.0, 131072 87 and 66).
-    const int most_ctas = rows > 32768 ? mr::kMostSortCluster : mr::kMostSortCluster / 2;
-    int cluster = 1, items = 1;
-    while (cluster < most_ctas && (size_t)mr::kSortThreads * cluster < rows) cluster *= 2;
-    while (items < mr::kMostSortItems && (size_t)mr::kSortThreads * cluster * items < rows) items *= 2;
-    // What the other SMs do meanwhile: as much as takes them no longer than the
-    // sort.  Clearing 48 MiB of the table, also rows that are then written: 777
-    // rows of 1001 into 32003 x 1001 fp32 32.9 us without, 29.7, 26.7 and 27.7
-    // with 32, 48 and 64 MiB; 128 MiB of g asked for from L2: 16384 rows of 4096
-    // bf16 83.3 us without, 81.7 and 80.1 with 64 and 128 MiB.
-    P.ahead = (uint32_t)std::min<size_t>(rows, ((size_t)128 << 20) / (hidden * b));
-    P.cleared = accumulate ? 0 : (uint32_t)std::min<size_t>(vocab, ((size_t)48 << 20) / (hidden * bytes_of(grad_dtype))) / 8 * 8;
-    const int helpers = P.ahead || P.cleared ? mr::device_sms() / cluster - 1 : 0;
-    cudaError_t e = mr::launch_token_sort(P, dtype, grad_dtype, cluster, helpers, items, (cudaStream_t)stream);
+    const mr::SortPlan plan = mr::plan_sort(rows, vocab, hidden, b, bytes_of(grad_dtype), accumulate, mr::device_sms(),
+                                            rows > 32768 ? mr::most_sort_cluster() : mr::kMostSortCluster / 2);
+    if (plan.cluster == 0)
+        return report_error(MR_ERR_UNSUPPORTED, "%s: this device's clusters sort fewer than %zu rows a call", what, rows);
+    P.ahead = plan.ahead;
+    P.cleared = plan.cleared;
+    cudaError_t e = mr::launch_token_sort(P, dtype, grad_dtype, plan, (cudaStream_t)stream);
     if (e == cudaSuccess) {
         mr::count_launch();
         const uint64_t most = rows * P.slabs + (accumulate ? 0 : vocab);
@@ -221,7 +212,7 @@ mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, 
         if (mr::debug_log_level() > 0)
             fprintf(stderr, "[mr] %s dtype=%s grad=%s W=%d rows=%zu hidden=%zu vocab=%zu accumulate=%d vec=%d sort=%dx%d grid=%u\n", what,
                     dtype == MR_BF16 ? "bf16" : "fp32", grad_dtype == MR_BF16 ? "bf16" : "fp32", W, rows, hidden, vocab, accumulate, (int)vec,
-                    cluster, items, grid.x);
+                    plan.cluster, plan.items, grid.x);
     }
     if (e == cudaSuccess) {
         mr::count_launch();

@@ -16,6 +16,8 @@
 // Then the runs of one row: each position finds its run's start (the last
 // start among the lanes, warps and CTAs before it); a unit starts every kUnit
 // positions of a run; units are numbered by a scan.
+#include <atomic>
+
 #include "elements.cuh"
 #include "embedding.h"
 
@@ -270,26 +272,63 @@ __global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(const __gri
 }
 
 template <int K>
-cudaError_t launch(const EmbeddingGradParams& P, int g_bytes, int table_bytes, int cluster, int helpers, cudaStream_t s) {
-    const size_t smem = kSortThreads * K * sizeof(uint2) + 2 * sizeof(uint32_t) * (1 << kSortDigit) + kWarps * sizeof(uint16_t) * (1 << kSortDigit);
-    static_assert(kSortThreads * kMostSortItems * sizeof(uint2) + (8 + 2 * kWarps) * (1 << kSortDigit) <= kMostDynamicSmem, "the sort's shared memory");
-    cudaError_t e = allow_dynamic_smem(token_sort_kernel<K>, smem);
-    if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(token_sort_kernel<K>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+constexpr size_t sort_smem() {
+    return kSortThreads * K * sizeof(uint2) + 2 * sizeof(uint32_t) * (1 << kSortDigit) + kWarps * sizeof(uint16_t) * (1 << kSortDigit);
+}
+static_assert(sort_smem<kMostSortItems>() <= kMostDynamicSmem, "the sort's shared memory");
+
+template <int K>
+cudaError_t allow(int cluster) {
+    const cudaError_t e = allow_dynamic_smem(token_sort_kernel<K>, sort_smem<K>());
+    return e == cudaSuccess && cluster > 8 ? cudaFuncSetAttribute(token_sort_kernel<K>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
+}
+
+template <int K>
+cudaError_t launch(const EmbeddingGradParams& P, int g_bytes, int table_bytes, const SortPlan& plan, cudaStream_t s) {
+    const cudaError_t e = allow<K>(plan.cluster);
     if (e != cudaSuccess) return e;
-    return launch_kernel_of(kSortThreads, token_sort_kernel<K>, dim3(cluster * (1 + helpers), 1, 1), smem, s, cluster > 1 ? cluster : 0, P,
-                            g_bytes, table_bytes);
+    return launch_kernel_of(kSortThreads, token_sort_kernel<K>, dim3(plan.cluster * (1 + plan.helpers), 1, 1), sort_smem<K>(), s,
+                            plan.cluster > 1 ? plan.cluster : 0, P, g_bytes, table_bytes);
 }
 
 }  // namespace
 
-cudaError_t launch_token_sort(const EmbeddingGradParams& P, int g_dtype, int table_dtype, int cluster, int helpers, int items, cudaStream_t s) {
+// Clusters of more than eight CTAs are not promised by every device: the
+// driver is asked (some 10 us) once for each.
+int most_sort_cluster() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) dev = 64;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMostSortCluster, 1, 1);
+    cfg.blockDim = dim3(kSortThreads, 1, 1);
+    cfg.dynamicSmemBytes = sort_smem<kMostSortItems>();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMostSortCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = allow<kMostSortItems>(kMostSortCluster);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, token_sort_kernel<kMostSortItems>, &cfg);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return kMostSortCluster;        // not kept: the launch will say what is wrong
+    }
+    n = n > 0 ? kMostSortCluster : kMostSortCluster / 2;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+cudaError_t launch_token_sort(const EmbeddingGradParams& P, int g_dtype, int table_dtype, const SortPlan& plan, cudaStream_t s) {
     const int g = g_dtype == MR_BF16 ? 2 : 4, t = table_dtype == MR_BF16 ? 2 : 4;
-    switch (items) {
-        case 1: return launch<1>(P, g, t, cluster, helpers, s);
-        case 2: return launch<2>(P, g, t, cluster, helpers, s);
-        case 4: return launch<4>(P, g, t, cluster, helpers, s);
-        case 8: return launch<8>(P, g, t, cluster, helpers, s);
-        default: return launch<kMostSortItems>(P, g, t, cluster, helpers, s);
+    switch (plan.items) {
+        case 1: return launch<1>(P, g, t, plan, s);
+        case 2: return launch<2>(P, g, t, plan, s);
+        case 4: return launch<4>(P, g, t, plan, s);
+        case 8: return launch<8>(P, g, t, plan, s);
+        default: return launch<kMostSortItems>(P, g, t, plan, s);
     }
 }
 

@@ -404,7 +404,7 @@ mr_status_t mr_embedding(const void* const* table, const size_t* ld, int W, size
  *     call.  Calls that share a workspace must not run at the same time.
  *   Nothing that is written overlaps anything else.
  */
-#define MR_MAX_EMBEDDING_GRAD_ROWS 262144     /* rows of a call (more: MR_ERR_UNSUPPORTED) */
+#define MR_MAX_EMBEDDING_GRAD_ROWS 262144     /* rows of a call (more: MR_ERR_UNSUPPORTED; half, where a device has no clusters of 16 CTAs) */
 size_t mr_embedding_grad_workspace_bytes(size_t rows, size_t vocab, size_t hidden);
 mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, const long long* ids, size_t rows, float scale,
                               void* const* grad, const size_t* ld_grad, int W, size_t vocab, size_t hidden,
