@@ -32,7 +32,7 @@ constexpr uint64_t kIsBf16 = 1ull << 63;
 struct SumPair {
     float hi, lo;
 };
-// What a CTA has summed: the squares as they are, of x 2^-80, and of x 2^90.
+// What a CTA has summed: the squares as they are, of x 2^-90, and of x 2^90.
 struct NormPart {
     SumPair mid, big, small;
 };

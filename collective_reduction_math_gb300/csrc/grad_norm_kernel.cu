@@ -4,11 +4,12 @@
 //   norm = sqrt(sum x^2),   coef = norm > max ? max / norm : 1,   out = coef * x
 //
 // Squares of fp32 values leave fp32's range at both ends, so three sums are
-// kept: of x^2, of (x 2^-80)^2 and of (x 2^90)^2.  Where the first is finite
-// and at least 2^-60, what it lost below 2^-126 is nothing beside it; where
-// it overflowed, some |x| is over 2^60 and the second has all that counts;
-// below 2^-60 every |x| is below 2^-30 and the third can neither overflow nor
-// lose a bit that counts.  A thread's sums are fp32 over a tile; tiles, threads,
+// kept: of x^2, of (x 2^-90)^2 and of (x 2^90)^2.  Where the first is finite
+// and at least 2^-60, what it lost below 2^-126 is nothing beside it.  Where it
+// overflowed, the squares add up to 2^128 at least and the second sum to 2^-52:
+// it loses less than 2^-149 a term, of 2^44 terms at most (a call's tiles), and
+// as many of (2^128 2^-90)^2 = 2^76 do not overflow it.  Below 2^-60 every |x| is
+// below 2^-30 and the third can neither overflow nor lose a bit that counts.  A thread's sums are fp32 over a tile; tiles, threads,
 // CTAs and launches are joined in pairs of floats (the rounding of each addition
 // kept beside the sum), over a fixed split: the same bits on every run.  (In
 // 64 bits the joins took longer than small lists' sums: this GPU does some two
@@ -20,7 +21,7 @@
 namespace mr {
 namespace {
 
-constexpr float kDown = 0x1p-80f, kUp = 0x1p90f;
+constexpr float kDown = 0x1p-90f, kUp = 0x1p90f;
 constexpr unsigned kAll = 0xffffffffu;
 
 // The squares of a tile, in two lanes each.
@@ -156,21 +157,21 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) norm_parts_kernel(const _
     if (threadIdx.x == 0) parts[blockIdx.x] = sum;
 }
 
-// The norm as root * 2^power, with what the root is short of; power 0, 80 or -90.
+// The norm as root * 2^power, with what the root is short of; power 0, 90 or -90.
 struct Norm {
     float root, rest;
     int power;
     __device__ __forceinline__ float value() const {
-        return power == 0 ? root : power > 0 ? __fmul_rn(root, 0x1p80f) : __fmul_rn(root, 0x1p-90f);
+        return power == 0 ? root : power > 0 ? __fmul_rn(root, 0x1p90f) : __fmul_rn(root, 0x1p-90f);
     }
     // max / norm where that is below 1, else 1; NaN where the norm is
     __device__ __forceinline__ float factor(float max) const {
         if (isnan(root)) return root;
-        const float scaled = power == 0 ? max : power > 0 ? __fmul_rn(max, 0x1p-80f) : __fmul_rn(max, 0x1p90f);
+        const float scaled = power == 0 ? max : power > 0 ? __fmul_rn(max, 0x1p-90f) : __fmul_rn(max, 0x1p90f);
         if (!(root > scaled || (root == scaled && rest > 0.0f))) return 1.0f;
         if (isinf(root)) return 0.0f;
-        // scaled, but where 2^-80 would cost bits of max
-        return power > 0 ? __fmul_rn(__fdiv_rn(max, root), 0x1p-80f) : __fdiv_rn(scaled, root);
+        // scaled, but where 2^-90 would cost bits of max
+        return power > 0 ? __fmul_rn(__fdiv_rn(max, root), 0x1p-90f) : __fdiv_rn(scaled, root);
     }
 };
 // On every thread.
@@ -186,7 +187,7 @@ __device__ __forceinline__ Norm norm_of(const NormOfParts& N) {
         n.power = -90;
     } else if (isinf(s.hi)) {
         s = v.big;
-        n.power = 80;
+        n.power = 90;
     }
     n.root = __fsqrt_rn(s.hi);
     // a step of Newton's iteration for what it lacks
