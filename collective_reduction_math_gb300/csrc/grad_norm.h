@@ -32,7 +32,7 @@ constexpr uint64_t kIsBf16 = 1ull << 63;
 struct SumPair {
     float hi, lo;
 };
-// What a CTA has summed: the squares as they are, of x 2^-90, and of x 2^90.
+// What a thread, a CTA or all have summed, each element in one of the three: x^2, (x 2^-90)^2 or (x 2^90)^2.
 struct NormPart {
     SumPair mid, big, small;
 };

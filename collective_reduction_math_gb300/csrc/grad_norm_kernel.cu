@@ -3,17 +3,24 @@
 //
 //   norm = sqrt(sum x^2),   coef = norm > max ? max / norm : 1,   out = coef * x
 //
-// Squares of fp32 values leave fp32's range at both ends, so three sums are
-// kept: of x^2, of (x 2^-90)^2 and of (x 2^90)^2.  Where the first is finite
-// and at least 2^-60, what it lost below 2^-126 is nothing beside it.  Where it
-// overflowed, the squares add up to 2^128 at least and the second sum to 2^-52:
-// it loses less than 2^-149 a term, of 2^44 terms at most (a call's tiles), and
-// as many of (2^128 2^-90)^2 = 2^76 do not overflow it.  Below 2^-60 every |x| is
-// below 2^-30 and the third can neither overflow nor lose a bit that counts.  A thread's sums are fp32 over a tile; tiles, threads,
-// CTAs and launches are joined in pairs of floats (the rounding of each addition
-// kept beside the sum), over a fixed split: the same bits on every run.  (In
-// 64 bits the joins took longer than small lists' sums: this GPU does some two
-// such operations a cycle and SM.)
+// Squares of fp32 values leave fp32's range at both ends, so a thread's part of a
+// tile is squared as it is where that sum lies from 2^-100 to 2^88, else scaled
+// by 2^-90 or 2^90 first; each of the three kinds has a sum of its own, and the
+// three are put together at the end.  Terms lose at most 2^-149 each to the
+// range's lower end, less than 2^-42 of a part; 2^38 parts (a call's tiles) do
+// not overflow: 2^126 as they are, 2^120 scaled down (2^44 elements below
+// (2^128 2^-90)^2 each), 2^119 scaled up.  A thread tries the scale that its last
+// part had: one pass over a part, but where the size of the elements changes.
+//
+// A sum is a pair of floats, the second what the first's additions lost.  Two
+// squares are added to one another (off by 2 U = 2^-23 of themselves; bf16
+// squares have 16 bits, and two of them are nearly always exact), and then to
+// the pair without loss; threads, CTAs and launches are joined in pairs too,
+// over a fixed split: the same bits on every run.  (Chains of 32 fp32
+// multiply-adds left the norm of 1.5e9 normal bf16 values one step below the
+// nearest: each addition rounds 16-bit squares to even, and the sum ends up
+// 2.2e-8 low; chains of two are 6e-10 low.  In 64 bits the joins took longer
+// than small lists' sums: this GPU does some two such operations a cycle and SM.)
 #include "elements.cuh"
 #include "grad_norm.h"
 #include "packed.cuh"
@@ -22,18 +29,9 @@ namespace mr {
 namespace {
 
 constexpr float kDown = 0x1p-90f, kUp = 0x1p90f;
+// What a thread multiplies by before it squares: 1, kDown or kUp.
+enum Scale { kAsItIs, kScaledDown, kScaledUp };
 constexpr unsigned kAll = 0xffffffffu;
-
-// The squares of a tile, in two lanes each.
-struct TileSum {
-    F2 mid{0}, big{0}, small{0};
-    __device__ __forceinline__ void add(float a, float b) {
-        const F2 x = f2(a, b), d = mul2(x, f2(kDown, kDown)), u = mul2(x, f2(kUp, kUp));
-        mid = fma2(x, x, mid);
-        big = fma2(d, d, big);
-        small = fma2(u, u, small);
-    }
-};
 
 // a + b, and what the addition lost.
 __device__ __forceinline__ SumPair exact_sum(float a, float b) {
@@ -46,11 +44,21 @@ __device__ __forceinline__ SumPair plus(SumPair p, SumPair q) {
     const float lo = __fadd_rn(s.lo, __fadd_rn(p.lo, q.lo)), hi = __fadd_rn(s.hi, lo);
     return isfinite(s.hi) ? SumPair{hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))} : SumPair{s.hi, 0.0f};
 }
-__device__ __forceinline__ SumPair plus(SumPair p, F2 lanes) {
-    float a, b;
-    unpack(lanes, a, b);
-    return plus(p, exact_sum(a, b));
-}
+// A thread's sum over its part of a tile, in two lanes.
+struct LaneSums {
+    F2 hi{0}, lo{0};
+    __device__ __forceinline__ void add(F2 q) {
+        const F2 s = add2(hi, q), t = sub2(s, hi);
+        lo = add2(lo, add2(sub2(hi, sub2(s, t)), sub2(q, t)));
+        hi = s;
+    }
+    __device__ __forceinline__ SumPair value() const {
+        float a, b, c, d;
+        unpack(hi, a, b);
+        unpack(lo, c, d);
+        return plus(SumPair{a, c}, SumPair{b, d});
+    }
+};
 __device__ __forceinline__ NormPart plus(const NormPart& a, const NormPart& b) {
     return {plus(a.mid, b.mid), plus(a.big, b.big), plus(a.small, b.small)};
 }
@@ -94,23 +102,61 @@ __device__ __forceinline__ int tensor_of(const TensorList& L, uint32_t tile) {
     return lo;
 }
 
+// The sum of (x scale)^2 over the thread's part of a tile, and whether any of it is not +0.
 template <int DT>
-__device__ __forceinline__ void sum_tile(const Tile& t, const uint4 (&v)[kTileVectors], TileSum& s) {
+__device__ __forceinline__ SumPair sum_tile(const Tile& t, const uint4 (&v)[kTileVectors], float scale, bool& any) {
     using E = Element<DT>;
+    const F2 factor = f2(scale, scale);
+    LaneSums s;
+    uint32_t bits = 0;
 #pragma unroll
     for (uint32_t j = 0; j < kTileVectors; ++j) {
+        bits |= v[j].x | v[j].y | v[j].z | v[j].w;
         float f[E::kLanes];
         E::unpack(v[j], f);
 #pragma unroll
-        for (int k = 0; k < E::kLanes; k += 2) s.add(f[k], f[k + 1]);
+        for (int k = 0; k < E::kLanes; k += 4) {
+            const F2 a = mul2(f2(f[k], f[k + 1]), factor), b = mul2(f2(f[k + 2], f[k + 3]), factor);
+            s.add(fma2(b, b, mul2(a, a)));
+        }
     }
-    if (t.whole()) return;
-    // vectors over the tensor's start or end: their elements one by one
-    for (uint32_t j = 0; j < kTileVectors; ++j) {
-        const uint64_t p = t.at(j);
-        if (t.has(p)) continue;
-        for (uint64_t e = max(p, t.before); e < min(p + 16, t.end); e += E::kBytes) s.add(E::get(t.base + e, 0), 0.0f);
+    if (!t.whole()) {
+        // vectors over the tensor's start or end: their elements one by one
+        for (uint32_t j = 0; j < kTileVectors; ++j) {
+            const uint64_t p = t.at(j);
+            if (t.has(p)) continue;
+            for (uint64_t e = max(p, t.before); e < min(p + 16, t.end); e += E::kBytes) {
+                const float x = E::get(t.base + e, 0), y = __fmul_rn(x, scale);
+                bits |= __float_as_uint(x);
+                s.add(f2(__fmul_rn(y, y), 0.0f));
+            }
+        }
     }
+    any = bits != 0;
+    return s.value();
+}
+
+// Adds the thread's part of a tile to the sum that it belongs to.
+template <int DT>
+__device__ __forceinline__ void add_tile(NormPart& sum, int& scale, const Tile& t) {
+    SumPair s;
+    // three at most: down, as it is and up, in this order or the other
+#pragma unroll 1
+    for (int tries = 0; tries < 3; ++tries) {
+        uint4 v[kTileVectors];
+        t.load(v);      // again where the scale changes: kept for that, the vectors would spill
+        bool any;
+        s = sum_tile<DT>(t, v, scale == kAsItIs ? 1.0f : scale == kScaledDown ? kDown : kUp, any);
+        // a factor of 2 to spare on the way back, so that no sum is turned away by both
+        int other = scale;
+        if (scale == kAsItIs) other = !(s.hi < 0x1p88f) ? kScaledDown : s.hi < 0x1p-100f ? kScaledUp : kAsItIs;
+        else if (scale == kScaledDown ? s.hi < 0x1p-93f : !(s.hi < 0x1p81f)) other = kAsItIs;
+        if (other == scale || !any) break;      // zeros are right on any scale, and change none
+        scale = other;
+    }
+    if (scale == kAsItIs) sum.mid = plus(sum.mid, s);
+    else if (scale == kScaledDown) sum.big = plus(sum.big, s);
+    else sum.small = plus(sum.small, s);
 }
 
 // The same on every thread of the CTA (kThreads threads).
@@ -141,17 +187,13 @@ __device__ __forceinline__ int tensor_from(const TensorList& L, int i, uint32_t 
 __global__ void __launch_bounds__(kThreads, kNormCtas) norm_parts_kernel(const __grid_constant__ TensorList L, NormPart* parts) {
     const uint32_t tiles = L.tile0[L.count];
     NormPart sum{};
-    int i = tensor_of(L, blockIdx.x);
+    int scale = kAsItIs, i = tensor_of(L, blockIdx.x);
     pdl_enter();
     for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         i = tensor_from(L, i, t);
         const Tile tile(L, i, t);
-        uint4 v[kTileVectors];
-        tile.load(v);
-        TileSum s;
-        if (L.n[i] & kIsBf16) sum_tile<MR_BF16>(tile, v, s);
-        else sum_tile<MR_FP32>(tile, v, s);
-        sum = {plus(sum.mid, s.mid), plus(sum.big, s.big), plus(sum.small, s.small)};
+        if (L.n[i] & kIsBf16) add_tile<MR_BF16>(sum, scale, tile);
+        else add_tile<MR_FP32>(sum, scale, tile);
     }
     sum = join(sum);
     if (threadIdx.x == 0) parts[blockIdx.x] = sum;
@@ -179,19 +221,20 @@ __device__ __forceinline__ Norm norm_of(const NormOfParts& N) {
     NormPart v{};
     for (int i = threadIdx.x; i < N.count; i += kThreads) v = plus(v, N.parts[i]);
     v = join(v);
+    // the largest kind that there is, and 2^-180 of the next one, which may be something beside it
+    const bool down = !(v.big.hi == 0.0f), plain = v.mid.hi > 0.0f;
+    const SumPair first = down ? v.big : plain ? v.mid : v.small, next = down ? v.mid : plain ? v.small : SumPair{0.0f, 0.0f};
+    const SumPair s = plus(first, SumPair{__fmul_rn(__fmul_rn(next.hi, kDown), kDown), __fmul_rn(__fmul_rn(next.lo, kDown), kDown)});
     Norm n;
-    SumPair s = v.mid;
-    n.power = 0;
-    if (s.hi < 0x1p-60f) {
-        s = v.small;
-        n.power = -90;
-    } else if (isinf(s.hi)) {
-        s = v.big;
-        n.power = 90;
-    }
+    n.power = down ? 90 : plain ? 0 : -90;
     n.root = __fsqrt_rn(s.hi);
-    // a step of Newton's iteration for what it lacks
-    n.rest = s.hi > 0.0f && isfinite(s.hi) ? __fdiv_rn(__fadd_rn(__fmaf_rn(-n.root, n.root, s.hi), s.lo), __fmul_rn(2.0f, n.root)) : 0.0f;
+    n.rest = 0.0f;
+    if (s.hi > 0.0f && isfinite(s.hi)) {
+        // a step of Newton's iteration for what it lacks, which may be a step of the root's
+        const float lacks = __fdiv_rn(__fadd_rn(__fmaf_rn(-n.root, n.root, s.hi), s.lo), __fmul_rn(2.0f, n.root)), root = __fadd_rn(n.root, lacks);
+        n.rest = __fsub_rn(lacks, __fsub_rn(root, n.root));
+        n.root = root;
+    }
     return n;
 }
 

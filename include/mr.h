@@ -481,7 +481,8 @@ mr_status_t mr_adjust_logits_grad(const void* const* logits, const size_t* ld, i
  *     MR_ERR_UNSUPPORTED), any alignment to the element; n[i] == 0 is skipped;
  *     0 <= count <= 2^20 tensors, n[i] <= 2^40.  The three arrays are host
  *     arrays, as send and recv are.
- *   norm: one fp32 value in device memory (mr_clip_grad_norm: may be NULL).
+ *   norm: one fp32 value in device memory (mr_clip_grad_norm: may be NULL),
+ *     within 2^-23 of the exact norm relative to it, as a rule the nearest value.
  *     Sums neither overflow nor underflow where the norm does not; a norm
  *     beyond fp32 reads +inf, while coef comes from the norm itself.  A NaN
  *     makes the norm and every out NaN; infinities make the norm +inf, coef 0.
