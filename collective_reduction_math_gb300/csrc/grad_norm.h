@@ -37,12 +37,19 @@ struct NormPart {
     SumPair mid, big, small;
 };
 constexpr int kMostNormGrid = 1024;         // parts of a launch at most
+// Up to as many parts every CTA of the clipping joins for itself, while its first
+// tile is on its way; more, which only lists of several launches have, one CTA
+// joins in a launch before.  Else a call's time grew with the square of its list
+// (tensors of 2000 bf16: 1400 of them 49 us without that launch and 48 with it,
+// 2048 66 and 62, 4096 142 and 115, 10000 470 and 277; 1024, at this limit, 34 and 35).
+constexpr int kMostOwnJoin = kMostNormGrid;
 
 struct NormOfParts {
     const NormPart* parts;
     int count;
     float max_norm;
     float* norm;        // may be null
+    NormPart* all;      // where the join puts them together; may be null, and the first of them
 };
 
 cudaError_t launch_norm_parts(const TensorList& L, NormPart* parts, dim3 grid, cudaStream_t s);

@@ -101,7 +101,7 @@ mr_status_t failed(const Call& c, cudaError_t e) {
 mr_status_t run(const Call& c, float max_norm, cudaStream_t s) {
     TensorList L;
     mr::NormPart* parts = static_cast<mr::NormPart*>(c.workspace);
-    mr::NormOfParts N{parts, 0, max_norm, c.norm};
+    mr::NormOfParts N{parts, 0, max_norm, c.norm, nullptr};
     for (int j = 0; j < launches(c.count); ++j) {
         const uint32_t tiles = fill(L, c, j * mr::kListTensors);
         if (tiles == 0) continue;
@@ -113,7 +113,15 @@ mr_status_t run(const Call& c, float max_norm, cudaStream_t s) {
         if (mr::debug_log_level() > 0)
             fprintf(stderr, "[mr] %s tensors=%d of %d tiles=%u grid=%u\n", c.what, L.count, c.count, tiles, ctas);
     }
-    bool told = false;      // the clipping's first launch tells the norm
+    bool told = false;      // the norm: by a launch of its own or the clipping's first
+    if (c.out && N.count > mr::kMostOwnJoin) {
+        N.all = parts;
+        const cudaError_t e = mr::launch_norm_join(N, s);
+        if (e != cudaSuccess) return failed(c, e);
+        mr::count_launch();
+        N.count = 1;
+        told = true;
+    }
     for (int j = 0; c.out && j < launches(c.count); ++j) {
         const uint32_t tiles = fill(L, c, j * mr::kListTensors);
         if (tiles == 0) continue;

@@ -217,10 +217,12 @@ struct Norm {
     }
 };
 // On every thread.
-__device__ __forceinline__ Norm norm_of(const NormOfParts& N) {
+__device__ __forceinline__ NormPart joined(const NormOfParts& N) {
     NormPart v{};
     for (int i = threadIdx.x; i < N.count; i += kThreads) v = plus(v, N.parts[i]);
-    v = join(v);
+    return join(v);
+}
+__device__ __forceinline__ Norm norm_of(const NormPart& v) {
     // the largest kind that there is, and 2^-180 of the next one, which may be something beside it
     const bool down = !(v.big.hi == 0.0f), plain = v.mid.hi > 0.0f;
     const SumPair first = down ? v.big : plain ? v.mid : v.small, next = down ? v.mid : plain ? v.small : SumPair{0.0f, 0.0f};
@@ -240,8 +242,11 @@ __device__ __forceinline__ Norm norm_of(const NormOfParts& N) {
 
 __global__ void __launch_bounds__(kThreads) norm_join_kernel(const __grid_constant__ NormOfParts N) {
     pdl_enter();
-    const Norm norm = norm_of(N);
-    if (threadIdx.x == 0) *N.norm = norm.value();
+    const NormPart all = joined(N);
+    const Norm norm = norm_of(all);
+    if (threadIdx.x > 0) return;
+    if (N.norm) *N.norm = norm.value();
+    if (N.all) *N.all = all;        // may be one of the parts: they have been read
 }
 
 // The tile's vectors, scaled; `to` is where its base goes.
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) clip_kernel(const __grid_
         uint4 v[kTileVectors];
         tile.load(v);
         if (first) {
-            const Norm norm = norm_of(N);
+            const Norm norm = norm_of(joined(N));
             if (N.norm && blockIdx.x == 0 && threadIdx.x == 0) *N.norm = norm.value();
             coef = norm.factor(N.max_norm);
             first = false;
