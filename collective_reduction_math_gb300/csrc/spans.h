@@ -44,27 +44,45 @@ inline bool beside(const Span& a, const Span& b) {
     return d >= x.width && d + y.width <= x.ld;
 }
 
-// `open`: room for n indexes.
+// Whether two overlapping ranges of a call are allowed: both are read, or a rank
+// writes over its own input, row by row, or they share no byte.
+inline bool allowed(const Span& a, const Span& b) {
+    if (!a.written && !b.written) return true;
+    return (a.rank >= 0 && a.rank == b.rank && a.written != b.written && a.lo == b.lo && a.ld == b.ld) || beside(a, b);
+}
+
+// `open`: room for n indexes.  In the order of their starts, each range meets
+// those that have not ended: one that is read meets the written ones, which are few
+// (they may only lie beside one another); one that is written meets those read
+// too, and the first that is not allowed ends the search.  Ranges that are read
+// never meet, so a tensor that a call lists a million times costs no more than others.
 inline mr_status_t check_spans(Span* s, int* open, int n) {
     const auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
     if (!std::is_sorted(s, s + n, before)) std::sort(s, s + n, before);
-    int nopen = 0;
+    int reads = 0, writes = n;      // open[0, reads) are read, open[writes, n) written
     for (int i = 0; i < n; ++i) {
         const Span& b = s[i];
-        int keep = 0;
-        for (int j = 0; j < nopen; ++j) {
-            const Span& a = s[open[j]];
-            if (a.hi <= b.lo) continue;
-            open[keep++] = open[j];
-            if (!a.written && !b.written) continue;
-            // in place: what a rank writes over its own input, row by row
-            const bool in_place = a.rank >= 0 && a.rank == b.rank && a.written != b.written && a.lo == b.lo && a.ld == b.ld;
-            if (!in_place && !beside(a, b))
-                return report_error(MR_ERR_ALIAS, "%s[%d] overlaps %s[%d] in a form that is not an allowed in-place one",
-                                    a.name, std::max(0, a.rank), b.name, std::max(0, b.rank));
+        const Span* clash = nullptr;
+        const auto ended = [&](const Span& a) {
+            if (a.hi <= b.lo) return true;
+            if (!allowed(a, b)) clash = &a;
+            return false;
+        };
+        int keep = n;
+        for (int j = n - 1; j >= writes && !clash; --j)
+            if (!ended(s[open[j]])) open[--keep] = open[j];
+        writes = keep;
+        if (b.written) {
+            keep = 0;
+            for (int j = 0; j < reads && !clash; ++j)
+                if (!ended(s[open[j]])) open[keep++] = open[j];
+            reads = keep;
         }
-        nopen = keep;
-        open[nopen++] = i;
+        if (clash)
+            return report_error(MR_ERR_ALIAS, "%s[%d] overlaps %s[%d] in a form that is not an allowed in-place one",
+                                clash->name, std::max(0, clash->rank), b.name, std::max(0, b.rank));
+        if (b.written) open[--writes] = i;
+        else open[reads++] = i;
     }
     return MR_OK;
 }
