@@ -15,7 +15,7 @@ def _gpu_visible():
 # Fake device addresses that must never be dereferenced: only where no GPU is.
 no_gpu = pytest.mark.skipif(_gpu_visible(), reason="host-only checks with fake device addresses")
 
-ALIAS, CUDA = 3, 4
+INVALID, ALIAS, CUDA = 1, 3, 4
 B = 1 << 40
 
 
@@ -72,3 +72,35 @@ def test_few_ranges_in_every_order(mr):
             ins, outs = [B, B + a, B + 800], [B + (1 << 32), B + o, B + (1 << 33)]
             clear = all(abs(outs[1] - i) >= n for i in (ins[0], ins[2])) and (outs[1] == ins[1] or abs(outs[1] - ins[1]) >= n)
             assert lists.clip(ins, outs) == (CUDA if clear else ALIAS), (a, o)
+
+
+def test_embedding_gradient_workspace(mr):
+    need = mr.mr_embedding_grad_workspace_bytes
+    assert need(0, 10, 10) > 0          # zeros are written: the sort's counts and the map of rows
+    for few, many in (((0, 10, 10), (1, 10, 10)), ((31, 10, 10), (32, 10, 10)), ((1000, 50, 64), (1001, 50, 64)), ((4096, 50, 64), (262144, 50, 64)),
+                      ((100, 10, 64), (100, 50000, 64)), ((100, 50000, 64), (100, (1 << 31) - 1, 64))):
+        assert need(*few) <= need(*many)
+    # a record and a token each, a bit a table row, and partial sums of rows with more than 32 tokens
+    assert need(4096, 131072, 64) >= 4096 * 12 + 131072 // 8 + 2 * 128 * 64 * 4
+    assert need(32, 10, 64) == need(32, 10, 4096)
+    assert need(33, 10, 64) < need(33, 10, 4096)
+    assert need(262144, 10, 64) > 0
+    assert need(262145, 10, 64) == need(10, 1 << 31, 64) == need(10, 10, 1 << 31) == 0      # no such call
+
+
+@no_gpu
+@pytest.mark.parametrize("rows,hidden", [(0, 64), (6, 64), (40, 64), (262144, 8)])
+def test_embedding_gradient_refuses_workspaces(mr, rows, hidden):
+    V, L = 1001, mr.load()
+    need = mr.mr_embedding_grad_workspace_bytes(rows, V, hidden)
+    assert need > 0
+    table, g, ids, ws = B, B + (1 << 36), B + (1 << 37), B + (1 << 38)
+
+    def call(at=ws, size=need):
+        return L.mr_embedding_grad(g, 0, 0, ids, rows, 1.0, (ctypes.c_void_p * 1)(table), None, 1, V, hidden, 0, 0, at, size, None)
+    assert call() == CUDA
+    for kw in (dict(at=None), dict(at=ws + 8), dict(size=need - 1), dict(size=0)):
+        assert call(**kw) == INVALID, kw
+    assert call(at=table + V * hidden * 4 - 16) == ALIAS
+    if rows:
+        assert call(at=g) == ALIAS and call(at=ids) == ALIAS
