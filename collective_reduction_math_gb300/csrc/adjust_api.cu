@@ -125,9 +125,12 @@ mr_status_t check_adjust(Call& c, const mr_adjust_t* a, bool grad) {
 // of scores, or 64 KiB of gradients, beside which scores are read (4096 x 131072
 // bf16, histories of 1024 to 2048, windows of 64, 128 and 192 KiB: 417, 390 and
 // 407 us, the gradient 413, 422 and 442; 1024 x 131072 fp32 in 128 and 256 KiB:
-// 173 and 184).  Few rows are cut finer, as far as the device holds the windows
-// at once (64 rows: 13 windows of 10240 columns, 19.5 us; 16 of 8192, more than it
-// holds, 22.6).  For long lists see kMostListed.
+// 173 and 184).  Few rows are cut finer, as far as the device would hold the windows
+// at once with short lists (64 rows: 13 windows of 10240 columns, 19.5 us; 16 of
+// 8192, more than it holds, 22.6); lists beyond some 3000 entries a window leave
+// room for fewer CTAs than are counted with here.  The lists count by the room
+// that their rows have (history_len), whatever n_history says: a row's length is
+// known on the device alone.  For long lists see kMostListed.
 void plan_windows(mr::AdjustParams& P, size_t b, bool grad) {
     const uint64_t listed = (P.history ? P.ld_history : 0) + P.K;
     const uint64_t held = (uint64_t)mr::device_sms() * mr::adjust_ctas(listed > 0) / P.rows;        // windows of a row

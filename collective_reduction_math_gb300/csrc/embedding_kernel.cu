@@ -120,15 +120,16 @@ __global__ void __launch_bounds__(kThreads, 4) embedding_any_kernel(const __grid
 // ---------------------------------------------------------------------------
 // Gradient.  The tokens come sorted by row and cut into units
 // (token_sort_kernel.cu).  A warp has a unit and kSlab columns: it adds up to
-// kUnit rows of g in fp32, in the tokens' order, eight (bf16) or four rows'
-// loads at a time, and writes the table's row, or a partial sum where the row
-// has more units; embedding_join_kernel adds those.  Warps without a unit clear
+// kUnit rows of g in fp32, in the tokens' order, four rows' loads at a time, and
+// writes the table's row, or a partial sum where the row has more units; embedding_join_kernel adds those.  Warps without a unit clear
 // rows of no token.
 // ---------------------------------------------------------------------------
 constexpr int kPer = kSlab / 32;    // columns a lane
 // CTAs an SM, for 16384 rows of 4096 bf16 added to an fp32 table: 3 of them 99 us
 // (with eight rows' loads at a time as with four), 4 83, 5 (which spill) 109;
-// reads and writes that leave nothing in L1 and go first from L2, 80.
+// reads and writes that leave nothing in L1 and go first from L2, 80.  Measured
+// for bf16 rows in vectors alone, which do not spill at 4; the other variants
+// spill 20 to 68 bytes a thread.
 constexpr int kSumCtas = 4;
 
 // column i of lane l: beside one another where they are read in vectors

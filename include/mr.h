@@ -424,11 +424,15 @@ mr_status_t mr_embedding_grad(const void* g_out, size_t ld_g, mr_dtype_t dtype, 
  *   history: rows of history_len entries, those of row t in [0, n_history[t])
  *     (NULL: all; what is outside [0, history_len] is taken as the nearer end),
  *     the prompt's in [0, n_prompt[t]) (NULL: none).  An entry that is negative
- *     or past the vocabulary is none.  history_len < 2^30.
+ *     or past the vocabulary is none.  history_len < 2^30.  The work is laid out
+ *     for history_len entries a row, whatever n_history says: rows of a buffer much
+ *     wider than what they hold cost more than their entries, above all past 8448
+ *     entries and biases together.
  *   repetition, frequency, presence: one value a row; NULL: 1, 0, 0.
  *   bias_ids, bias: bias_count <= MR_MAX_BIAS entries a row.  A column that is
  *     listed more than once has the sum, in the list's order; one that is
- *     negative or past the vocabulary is none.
+ *     negative or past the vocabulary is none.  (Each column listed looks the row's
+ *     whole list through: lists of hundreds take longer than their length.)
  *   mask: rows of 32-bit words, ld_mask words apart (0: ceil(vocab / 32)); bit
  *     c % 32 of word c / 32 is set where column c is allowed.  A row may allow
  *     none: all -inf.  NULL: all allowed.  What a masked place held has no part
