@@ -190,6 +190,16 @@ struct Penalties {
     }
 };
 
+// A listed column's value; a NaN keeps its bits (a column that a prompt names and
+// no penalty changes is as it was).
+template <int DT>
+__device__ __forceinline__ void put_listed(void* p, uint64_t i, uint32_t value) {
+    using E = Element<DT>;
+    const float v = __uint_as_float(value);
+    if (DT == MR_BF16 && isnan(v)) static_cast<typename E::Raw*>(p)[i] = (typename E::Raw)(value >> 16);
+    else E::put(p, i, v);
+}
+
 template <int DT, bool GRAD, bool LISTS>
 __global__ void __launch_bounds__(kThreads, adjust_ctas(LISTS)) adjust_kernel(const __grid_constant__ AdjustParams P) {
     using E = Element<DT>;
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, adjust_ctas(LISTS)) adjust_kernel(co
                 const uint32_t h = table.taken[i], col = lo + table.key[h] - 1;
                 if (!is_allowed(mask ? bits : nullptr, col - lo)) continue;
                 const int r = rank_of(P, col);
-                E::put(P.out[r], row * P.ldo[r] + (col - P.col0[r]), __uint_as_float(table.word[h]));
+                put_listed<DT>(P.out[r], row * P.ldo[r] + (col - P.col0[r]), table.word[h]);
             }
         }
     }
