@@ -13,8 +13,9 @@ namespace mr {
 constexpr int kListTensors = 512;
 
 // A tensor is cut into tiles of kTileBytes, counted from its start rounded
-// down to 16 bytes.  8 vectors a thread and 4 CTAs an SM: 1.5e9 bf16 in 435 us
-// (103 % of the copy rate; 4 vectors: 483, and 6 CTAs an SM with them 692).
+// down to 16 bytes.  8 vectors a thread and 4 CTAs an SM: 1.5e9 bf16 in 427 us
+// (105 % of the copy rate; with chains of multiply-adds for sums it was 435, with
+// 4 vectors 483, and with 6 CTAs an SM besides 692).
 constexpr uint32_t kTileVectors = 8;        // 16-byte vectors a thread
 constexpr uint32_t kTileBytes = kThreads * kTileVectors * 16;
 constexpr int kNormCtas = 4;                // CTAs an SM
